@@ -22,10 +22,15 @@ from .binding import (  # noqa: F401
     hip_select_cached,
     HipSelectCache,
     hip_select_workspace_bytes,
+    kv_cache_read,
+    kv_cache_write,
     library_path,
     mixed_index_build,
     mixed_index_build_workspace_bytes,
     load,
+    paged_attn,
+    paged_attn_workspace_bytes,
+    PagedKVCache,
     profile_collect,
     profile_enable,
     refresh_mask,

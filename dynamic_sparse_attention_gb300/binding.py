@@ -64,6 +64,12 @@ class BsDebug(ctypes.Structure):
     _fields_ = [("q_pool", _vp), ("k_pool", _vp), ("scores", _vp)]
 
 
+class PagedShape(ctypes.Structure):
+    _fields_ = [("B", _c_int), ("n_tok", _c_int), ("max_pages", _c_int), ("n_pages", _c_int),
+                ("page_size", _c_int), ("H_q", _c_int), ("H_kv", _c_int), ("D", _c_int),
+                ("dtype", _c_int)]
+
+
 class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", _c_int), ("total_ms", ctypes.c_double)]
 
@@ -108,6 +114,12 @@ _SIGNATURES = {
                                      _vp, ctypes.c_float, _vp, _vp, _vp]),
     "sparse_attn_decode_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                             ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "kv_cache_write": (_c_int, [_vp, _vp, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _vp, _vp]),
+    "kv_cache_read": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp]),
+    "paged_attn_workspace": (_c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    "paged_attn": (_c_int, [_vp, ctypes.c_longlong, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int,
+                            _c_int, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "dsa_device_error": (_c_int, [ctypes.POINTER(_c_int)]),
     "dsa_set_wait_limit": (_c_int, [ctypes.c_ulonglong]),
     "dsa_profile_enable": (_c_int, [_c_int]),
@@ -118,7 +130,8 @@ _SIGNATURES = {
 def device_error() -> int:
     """Read and clear the library's device error words: 0 = none; bit 0 / bit 1: a
     prefill-attention / vertical-slash-estimate CTA gave up a wait; bit 2 (checked
-    build): a kernel met out-of-range device-side input."""
+    build): a kernel met out-of-range device-side input; bit 3: a paged-attention CTA gave
+    up a wait."""
     lib = load()
     c = _c_int()
     st = lib.dsa_device_error(ctypes.byref(c))
@@ -725,4 +738,191 @@ def sparse_attn_prefill(q, k, v, blk_cnt, blk_idx, col_cnt, col_idx, *, scale=No
                                  _ptr(blk_idx), _ptr(col_cnt), _ptr(col_idx),
                                  ctypes.c_float(scale), _ptr(out), _ptr(lse), _stream(stream))
     _check("sparse_attn_prefill", st)
+    return out, lse
+
+
+# ----------------------------------------------------------------------------- paged cache
+
+@dataclass
+class PagedKVCache:
+    """Keys and values in pages [n_pages, page_size, H_kv, D]: bf16, or FP8 E4M3 codes (a
+    uint8 or float8_e4m3fn tensor) with one scale byte per token and head in k_scale /
+    v_scale [n_pages, page_size, H_kv] (uint8; a row's values are code * 2**(byte - 127)).
+    The tensors are the caller's; `empty` allocates a cache."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, H_kv: int, D: int, *, fp8: bool = False,
+              device="cuda") -> "PagedKVCache":
+        shape = (n_pages, page_size, H_kv, D)
+        if not fp8:
+            return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        return cls(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+
+    @property
+    def fp8(self) -> bool:
+        return _is_fp8(self.k)
+
+    def check(self) -> None:
+        if self.k.dim() != 4 or self.v.shape != self.k.shape or self.v.dtype != self.k.dtype:
+            raise ValueError("k and v must be [n_pages, page_size, H_kv, D] tensors of one type")
+        if not self.fp8:
+            if self.k.dtype != torch.bfloat16:
+                raise TypeError(f"unsupported cache type {self.k.dtype}; use bfloat16 or FP8 E4M3 codes")
+            if self.k_scale is not None or self.v_scale is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+            return
+        for t in (self.k_scale, self.v_scale):
+            if t is None or t.dtype != torch.uint8 or t.shape != self.k.shape[:3]:
+                raise ValueError("an FP8 cache needs uint8 scales of [n_pages, page_size, H_kv]")
+
+
+def _paged_args(cache: PagedKVCache, kv_len, page_table, q_start, n_tok, H_q):
+    """Checked shape of a call over `cache`, and the device every tensor is on."""
+    cache.check()
+    _need_cuda(cache.k, cache.v, cache.k_scale, cache.v_scale, kv_len, page_table, q_start)
+    if page_table.dim() != 2 or kv_len.shape != (page_table.shape[0],):
+        raise ValueError("page_table must be [B, max_pages] and kv_len [B]")
+    B = page_table.shape[0]
+    if q_start is not None and q_start.shape != (B + 1,):
+        raise ValueError("q_start must be [B + 1]")
+    for t in (kv_len, page_table, q_start):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("kv_len, page_table and q_start must be int32")
+    dev = cache.k.device
+    for t in (cache.v, cache.k_scale, cache.v_scale, kv_len, page_table, q_start):
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor must be on the cache's device")
+    n_pages, page_size, H_kv, D = cache.k.shape
+    return PagedShape(B, n_tok, page_table.shape[1], n_pages, page_size, H_q, H_kv, D,
+                      BF16_FP8KV if cache.fp8 else BF16), dev
+
+
+def _token_rows(name, t, heads, D, dev):
+    """Token stride of a bf16 [n_tok, heads, D] tensor whose heads and dims are contiguous."""
+    if t.dim() != 3 or t.shape[1:] != (heads, D) or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 [n_tok, {heads}, {D}] tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    if t.shape[0] <= 1 and t.is_contiguous():
+        return heads * D
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (only tokens may be strided)")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+class _on:
+    """The tensors' device as the current one, and `stream` (default: its current stream) as
+    the stream that outputs and workspaces are allocated and the call is enqueued on."""
+
+    def __init__(self, dev, stream):
+        self.dev = torch.cuda.device(dev)
+        self.stream = stream
+
+    def __enter__(self):
+        self.dev.__enter__()
+        self.on = torch.cuda.stream(self.stream)
+        self.on.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        self.dev.__exit__(*exc)
+
+
+def kv_cache_write(cache: PagedKVCache, k_new, v_new, q_start, kv_len, page_table, *, stream=None) -> None:
+    """Write the chunks' keys and values (bf16 [n_tok, H_kv, D], tokens may be strided) into
+    their pages, quantised if the cache is FP8.  Sequence b's chunk is rows q_start[b] ..
+    q_start[b + 1] - 1 and holds its last positions; kv_len counts the chunk."""
+    lib = load()
+    H_kv, D = cache.k.shape[2], cache.k.shape[3]
+    shape, dev = _paged_args(cache, kv_len, page_table, q_start, k_new.shape[0], H_kv)
+    ks, vs = _token_rows("k_new", k_new, H_kv, D, dev), _token_rows("v_new", v_new, H_kv, D, dev)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    with _on(dev, stream) as st:
+        _check("kv_cache_write",
+               lib.kv_cache_write(_ptr(k_new), _ptr(v_new), ks, vs, _ptr(q_start), _ptr(kv_len),
+                                  _ptr(page_table), ctypes.byref(shape), _ptr(cache.k), _ptr(cache.v),
+                                  _ptr(cache.k_scale), _ptr(cache.v_scale), st))
+
+
+def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None = None, out=None,
+                  stream=None):
+    """The sequences' rows as contiguous bf16 (k, v) [B, T_max, H_kv, D], the layout that
+    hip_select, sparse_attn_decode and the index builders read.  `out`: (k, v) to write into
+    (rows behind a sequence's end stay as they are); else new tensors, zero there, of T_max
+    (default: max_pages * page_size) rows."""
+    lib = load()
+    n_pages, page_size, H_kv, D = cache.k.shape
+    shape, dev = _paged_args(cache, kv_len, page_table, None, 0, H_kv)
+    with _on(dev, stream) as st:
+        if out is None:
+            T_max = shape.max_pages * page_size if T_max is None else int(T_max)
+            out = tuple(torch.zeros(shape.B, T_max, H_kv, D, dtype=torch.bfloat16, device=dev)
+                        for _ in range(2))
+        k, v = out
+        _need_cuda(k, v)
+        if k.dim() != 4 or k.shape != v.shape or (k.shape[0],) + tuple(k.shape[2:]) != (shape.B, H_kv, D) or \
+                (T_max is not None and k.shape[1] != T_max):
+            raise ValueError("out must be two [B, T_max, H_kv, D] tensors")
+        if any(t.dtype != torch.bfloat16 or t.device != dev for t in out):
+            raise ValueError("out must be bfloat16 on the cache's device")
+        _check("kv_cache_read",
+               lib.kv_cache_read(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+                                 _ptr(kv_len), _ptr(page_table), ctypes.byref(shape), k.shape[1],
+                                 _ptr(k), _ptr(v), st))
+    return k, v
+
+
+def paged_attn_workspace_bytes(q, cache: PagedKVCache, page_table) -> int:
+    lib = load()
+    n = ctypes.c_size_t()
+    n_pages, page_size, H_kv, D = cache.k.shape
+    shape = PagedShape(page_table.shape[0], q.shape[0], page_table.shape[1], n_pages, page_size,
+                       q.shape[1], H_kv, D, BF16_FP8KV if cache.fp8 else BF16)
+    _check("paged_attn_workspace", lib.paged_attn_workspace(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: int = 0,
+               n_stream: int | None = None, scale: float | None = None, out=None, lse=None,
+               want_lse: bool = True, workspace=None, stream=None):
+    """Causal attention of the chunks q (bf16 [n_tok, H_q, D], tokens may be strided) over the
+    cache, which holds their own keys already (kv_cache_write).  A row at position p attends
+    every key j <= p, or with n_stream the n_stream newest of them (its own included) beside
+    the first n_sink.  Returns (out [n_tok, H_q, D], lse [n_tok, H_q] or None)."""
+    lib = load()
+    H_kv, D = cache.k.shape[2], cache.k.shape[3]
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tok, H_q, D]")
+    n_tok, H_q = q.shape[0], q.shape[1]
+    shape, dev = _paged_args(cache, kv_len, page_table, q_start, n_tok, H_q)
+    qs = _token_rows("q", q, H_q, D, dev)
+    if n_stream is not None and n_stream < 0:
+        raise ValueError("n_stream must be >= 0, or None for every key")
+    if scale is None:
+        scale = D ** -0.5
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty(n_tok, H_q, D, dtype=q.dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty(n_tok, H_q, dtype=torch.float32, device=dev)
+        _need_cuda(out, lse)
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must be a bfloat16 tensor of q's shape on its device")
+        if lse is not None and (lse.shape != (n_tok, H_q) or lse.dtype != torch.float32 or lse.device != dev):
+            raise ValueError("lse must be a float32 [n_tok, H_q] tensor on q's device")
+        nbytes = paged_attn_workspace_bytes(q, cache, page_table)
+        ws = _workspace(nbytes, dev, workspace)
+        _check("paged_attn",
+               lib.paged_attn(_ptr(q), qs, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+                              _ptr(cache.v_scale), _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                              ctypes.byref(shape), n_sink, -1 if n_stream is None else n_stream,
+                              ctypes.c_float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+                              ctypes.c_size_t(ws.numel() * ws.element_size()), st))
     return out, lse

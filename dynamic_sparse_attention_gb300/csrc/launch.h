@@ -248,4 +248,61 @@ struct PfListArgs {
 };
 cudaError_t launch_prefill_lists(const PfListArgs &a, cudaStream_t s);
 
+// Paged key/value cache: new rows into pages (bf16, or FP8 with row scales), pages into
+// contiguous bf16 (kv_cache.cu).
+struct CacheWriteArgs {
+  const uint16_t *k_new, *v_new;   // [n_tok, H_kv, D], token strides in elements
+  long long k_stride, v_stride;
+  const int32_t *q_start, *kv_len, *page_table;
+  int B, n_tok, max_pages, n_pages, page_size, H_kv, D;
+  bool fp8;
+  void *k_pages, *v_pages;
+  uint8_t *k_scale, *v_scale;
+  int tpc;                         // tokens per CTA (set by the launcher)
+};
+cudaError_t launch_kv_write(const CacheWriteArgs &a, cudaStream_t s);
+struct CacheReadArgs {
+  const void *k_pages, *v_pages;
+  const uint8_t *k_scale, *v_scale;
+  const int32_t *kv_len, *page_table;
+  int B, T_max, max_pages, n_pages, page_size, H_kv, D;
+  bool fp8;
+  void *k_out, *v_out;             // bf16 [B, T_max, H_kv, D]
+};
+cudaError_t launch_kv_read(const CacheReadArgs &a, cudaStream_t s);
+int kv_cache_check_word();
+
+// Chunk attention over the paged cache (paged_attn.cu).
+constexpr int kPagedMaxCtas = 152;   // shares of a launch, at most (GB300's SMs)
+// A cut item, as the share in which it begins describes it to the merge.
+struct PagedPiece {
+  long long item_u0, total;        // first schedule unit of the item; units of the launch
+  int n, w;                        // key tiles, units per tile
+  int tok0, ntok, g;               // first token row, tokens, KV head
+  int valid;
+};
+struct PagedAttnArgs {
+  const void *q;
+  long long q_stride;              // elements between tokens
+  const void *k_pages, *v_pages;
+  const uint8_t *k_scale, *v_scale;
+  const int32_t *q_start, *kv_len, *page_table;
+  int B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D;
+  bool fp8;
+  int n_sink, n_stream;
+  float scale;
+  uint16_t *out;
+  float *lse;
+  int part_rows;                   // paged_part_rows()
+  float *part;                     // [2 * kPagedMaxCtas][D / 4][part_rows][4]
+  float *part_ml;                  // [2 * kPagedMaxCtas][part_rows][2]
+  PagedPiece *piece;               // [kPagedMaxCtas]
+};
+int paged_part_rows(int n_tok, int G);
+int paged_attn_ready();            // the driver's tensor-map encoder is there (launch time)
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s);
+int paged_attn_device_error();
+int paged_attn_set_wait_limit(unsigned long long ns);
+int paged_attn_check_word();
+
 }  // namespace dsa

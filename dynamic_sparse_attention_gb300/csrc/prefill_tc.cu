@@ -906,15 +906,18 @@ extern "C" int dsa_device_error(int *code) {
   if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
   const int w = vs_tc_device_error();   // the vertical-slash estimate's word
   if (w < 0) return fail(DSA_ERR_CUDA, "reading the estimate's device error word");
+  const int pg = paged_attn_device_error();   // the paged attention's word
+  if (pg < 0) return fail(DSA_ERR_CUDA, "reading the paged attention's device error word");
   // checked builds: out-of-range device-side inputs met by the kernels
   int chk = 0;
-  const int words[5] = {decode_check_word(), decode_mma_check_word(), hip_select_check_word(),
-                        stage_tc_check_word(), prefill_tc_check_word()};
+  const int words[7] = {decode_check_word(),     decode_mma_check_word(), hip_select_check_word(),
+                        stage_tc_check_word(),   prefill_tc_check_word(), kv_cache_check_word(),
+                        paged_attn_check_word()};
   for (int x : words) {
     if (x < 0) return fail(DSA_ERR_CUDA, "reading a device check word");
     chk |= x;
   }
-  *code = v | (w << 1) | (chk ? 4 : 0);
+  *code = v | (w << 1) | (chk ? 4 : 0) | (pg << 3);
   if (chk)
     return fail(DSA_ERR_DEVICE_CHECK, "a kernel met a device-side input outside its range "
                                       "(length, count, selected position or list entry)");
@@ -931,7 +934,7 @@ extern "C" int dsa_set_wait_limit(unsigned long long ns) {
   using namespace dsa;
   clear_error();
   const unsigned long long v = ns ? ns : kWaitLimitNs;
-  if (prefill_tc_set_wait_limit(v) || vs_tc_set_wait_limit(v))
+  if (prefill_tc_set_wait_limit(v) || vs_tc_set_wait_limit(v) || paged_attn_set_wait_limit(v))
     return fail(DSA_ERR_CUDA, "setting the wait limit of the tensor-core kernels");
   return DSA_OK;
 }

@@ -1,7 +1,7 @@
 /*
  * dsa.h -- C ABI of the GB300 (sm_103a) dynamic sparse attention library (libdsa.so).
  *
- * Two halves of one hot path:
+ * Two halves of one hot path, and the cache that they stand on:
  *   decode : hip_select          -- InfiniteHiP hierarchical chunk pruning
  *            sparse_attn_decode  -- split-K online-softmax GQA decode over the
  *                                   sink + selected + window keys, with a merge
@@ -15,6 +15,11 @@
  *            hip_prefill_lists   -- its sink / selection / window as prefill lists
  *            sparse_attn_prefill -- causal attention over those 64x64 tiles and
  *                                   gathered columns
+ *   cache  : kv_cache_write      -- new keys and values into a paged cache, as bf16 or
+ *                                   quantised to FP8
+ *            kv_cache_read       -- pages back into contiguous bf16
+ *            paged_attn          -- attention of chunks of new tokens (or single tokens)
+ *                                   over the cache, optionally window + sinks only
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers owned by the caller.  Layouts are
@@ -400,6 +405,81 @@ int sparse_attn_prefill(const void *q, const void *k, const void *v,
                         const int32_t *col_idx, float scale, void *out, float *lse,
                         void *stream);
 
+/* ------------------------------------------------------------------ paged cache */
+
+/* A key/value cache in pages, shared by a batch of B sequences that bring ragged chunks of
+ * new tokens (one token each in a decode step, a prompt, or a mix of both).
+ *   k_pages, v_pages [n_pages, page_size, H_kv, D]   bf16, or FP8 E4M3 codes
+ *   k_scale, v_scale [n_pages, page_size, H_kv]      FP8 only: one byte s per token and head,
+ *                    the row's values are code * 2^(s - 127) (an E8M0 scale)
+ *   page_table [B, max_pages] int32   page that holds positions i*page_size .. of sequence b;
+ *                    entries that no position below kv_len[b] needs may hold anything
+ *   q_start [B + 1] int32   rows q_start[b] .. q_start[b+1]-1 of the token tensors (n_tok
+ *                    rows) are sequence b's chunk; non-decreasing, q_start[B] <= n_tok.  Rows
+ *                    outside every chunk are neither read for a result nor written
+ *   kv_len  [B] int32   keys of sequence b, its chunk included: the chunk holds the last
+ *                    positions, row n of it position kv_len[b] - (q_start[b+1] - n)
+ * dtype: DSA_BF16, or DSA_BF16_FP8KV (bf16 tokens, FP8 pages; D = 64 or 128 here).
+ * page_size: a power of two in [16, 1024].  max_pages * page_size <= 2^30.  B <= 4096 and
+ * H_q <= 128, else UNSUPPORTED.  n_tok may be 0 (nothing is launched).
+ * Bad device data is not dereferenced: lengths are clamped, rows whose position is negative
+ * are not written (cache write) or see no key (attention), and positions whose page lies
+ * outside [0, n_pages) are skipped.  One page may serve several sequences (a shared prefix),
+ * but a page that a call writes must belong to one. */
+typedef struct {
+  int B, n_tok, max_pages, n_pages, page_size;
+  int H_q, H_kv, D;
+  int dtype;
+} dsa_paged_shape;
+
+/* kv_cache_write -- the chunks' keys and values into their pages.
+ * k_new, v_new [n_tok, H_kv, D] bf16 with k_stride / v_stride elements between tokens (a
+ * multiple of 8, at least H_kv * D: slices of a fused projection need no copy).  An FP8 cache
+ * takes each (token, head) row with a = its largest finite magnitude as codes of x * 2^-e
+ * (nearest, ties to even, saturating at 448; NaN stays NaN), e the smallest integer with
+ * a * 2^-e <= 448, kept in [-116, 119] (0 for a row of zeros), and stores s = e + 127.  Every
+ * value the cache then stands for is exactly a bf16.  shape->H_q is not used but checked.
+ * Errors: INVALID_ARG / UNSUPPORTED (shape, strides), ALIGNMENT, CUDA. */
+int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, long long v_stride,
+                   const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
+                   const dsa_paged_shape *shape, void *k_pages, void *v_pages, uint8_t *k_scale,
+                   uint8_t *v_scale, void *stream);
+
+/* kv_cache_read -- the rows of every sequence as contiguous bf16: k_out, v_out [B, T_max,
+ * H_kv, D] (the layout hip_select, sparse_attn_decode and the prefill index builders read);
+ * row t of sequence b for t < min(kv_len[b], T_max), exactly the values the cache stands for
+ * (finite ones).  Rows behind a sequence's end, and those of pages outside the cache, are left
+ * as they were.  shape->n_tok and H_q are not used but checked. */
+int kv_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_scale,
+                  const uint8_t *v_scale, const int32_t *kv_len, const int32_t *page_table,
+                  const dsa_paged_shape *shape, int T_max, void *k_out, void *v_out, void *stream);
+
+/* Bytes of scratch paged_attn needs (partials of cut work; host only). */
+int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
+
+/* paged_attn -- causal attention of the chunks over the cache.
+ * Row n of sequence b, at position p, attends the keys
+ *   { j <= p : n_stream < 0 or j > p - n_stream or j < n_sink }
+ * i.e. every earlier key and itself (n_stream = -1), or the n_stream newest ones, itself
+ * included, beside the n_sink first ones -- what sparse_attn_decode attends with an empty
+ * selection, for every row of a chunk.  The chunk's own keys are read from the cache, so
+ * kv_cache_write comes first on the stream.
+ *   q [n_tok, H_q, D] bf16 with q_stride elements between tokens (a multiple of 8, at least
+ *   H_q * D); out [n_tok, H_q, D] bf16; lse [n_tok, H_q] fp32, natural log (NULL to skip);
+ *   scale positive and finite.  A row that attends nothing gets out = 0, lse = -inf.
+ * Nothing that the pages hold at positions no row of the call attends reaches a result.
+ * Deterministic: the same call gives the same bits.  out must not overlap the inputs; two
+ * calls (or two captured graphs) that may run at the same time need workspaces of their own.
+ * The launches use programmatic dependent launch and wait for the stream's previous kernel
+ * before they read anything.
+ * Errors: INVALID_ARG / UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA; a CTA whose bounded waits ran
+ * out leaves its rows unwritten and sets bit 3 of dsa_device_error. */
+int paged_attn(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
+               const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *q_start,
+               const int32_t *kv_len, const int32_t *page_table, const dsa_paged_shape *shape,
+               int n_sink, int n_stream, float scale, void *out, float *lse, void *ws,
+               size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------ timing */
 
 /* Per-kernel launch timing, off by default.  While enabled, every kernel the
@@ -420,13 +500,13 @@ int dsa_profile_collect(dsa_kernel_stat *out, int max_out, int *n_out);
 
 /* ------------------------------------------------------------------ diagnostics */
 
-/* Every wait inside the tensor-core kernels (the prefill attention and the two passes
- * of the vertical-slash estimate) is bounded; a CTA that gives up stops issuing work,
+/* Every wait inside the tensor-core kernels (the prefill attention, the paged attention and
+ * the two passes of the vertical-slash estimate) is bounded; a CTA that gives up stops issuing work,
  * frees its resources and sets a device error word (the prefill CTA also writes zero
  * output).  dsa_device_error copies the words to *code (0 = none; bit 0: the prefill
  * attention, bit 1: the estimate; bit 2: in a checked build, a kernel met a kv_len,
  * count, selected position or list entry outside its documented range -- the call then
- * returns DSA_ERR_DEVICE_CHECK) and clears them.  It synchronises with the device
+ * returns DSA_ERR_DEVICE_CHECK; bit 3: the paged attention) and clears them.  It synchronises with the device
  * (cudaMemcpyFromSymbol); call it between steps, not on a hot path.  Not a
  * source-page operation. */
 int dsa_device_error(int *code);
