@@ -9,6 +9,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -767,88 +768,128 @@ class PagedKVCache:
     def fp8(self) -> bool:
         return _is_fp8(self.k)
 
-    def check(self) -> None:
-        if self.k.dim() != 4 or self.v.shape != self.k.shape or self.v.dtype != self.k.dtype:
-            raise ValueError("k and v must be [n_pages, page_size, H_kv, D] tensors of one type")
-        if not self.fp8:
-            if self.k.dtype != torch.bfloat16:
-                raise TypeError(f"unsupported cache type {self.k.dtype}; use bfloat16 or FP8 E4M3 codes")
-            if self.k_scale is not None or self.v_scale is not None:
-                raise ValueError("a bfloat16 cache has no scales")
-            return
-        for t in (self.k_scale, self.v_scale):
-            if t is None or t.dtype != torch.uint8 or t.shape != self.k.shape[:3]:
-                raise ValueError("an FP8 cache needs uint8 scales of [n_pages, page_size, H_kv]")
+
+_FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+# Every decode step makes these calls, and a small one is over on the GPU in a few
+# microseconds: the checks below read each property of a tensor once, numbers that follow from
+# the shape alone are kept (_paged_shape), and the device and stream are only switched when
+# the call needs another one than the current.
+
+@functools.lru_cache(maxsize=1024)
+def _paged_shape(*sizes):
+    """(ctypes shape, workspace bytes of paged_attn) of B, n_tok, max_pages, n_pages,
+    page_size, H_q, H_kv, D, dtype."""
+    shape, n = PagedShape(*sizes), ctypes.c_size_t()
+    _check("paged_attn_workspace", load().paged_attn_workspace(ctypes.byref(shape), ctypes.byref(n)))
+    return ctypes.byref(shape), n.value
 
 
-def _paged_args(cache: PagedKVCache, kv_len, page_table, q_start, n_tok, H_q):
-    """Checked shape of a call over `cache`, and the device every tensor is on."""
-    cache.check()
-    _need_cuda(cache.k, cache.v, cache.k_scale, cache.v_scale, kv_len, page_table, q_start)
-    if page_table.dim() != 2 or kv_len.shape != (page_table.shape[0],):
-        raise ValueError("page_table must be [B, max_pages] and kv_len [B]")
-    B = page_table.shape[0]
-    if q_start is not None and q_start.shape != (B + 1,):
+def _index(t, name, dims, dev):
+    """Pointer of a contiguous int32 tensor of `dims` dimensions on device `dev`."""
+    if t.dtype != torch.int32 or t.dim() != dims:
+        raise TypeError(f"{name} must be a {dims}-dimensional int32 tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on the cache's device")
+    return t.data_ptr()
+
+
+def _cache_args(cache: PagedKVCache):
+    """(pointers of k, v, k_scale, v_scale, shape of k, dsa_dtype, device index), checked."""
+    k, v, ks, vs = cache.k, cache.v, cache.k_scale, cache.v_scale
+    dev, shape, dtype = k.get_device(), k.shape, k.dtype
+    if dev < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
+        raise ValueError("k and v must be [n_pages, page_size, H_kv, D] tensors of one type")
+    if v.get_device() != dev or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous CUDA tensors on one device")
+    if dtype == torch.bfloat16:
+        if ks is not None or vs is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        return k.data_ptr(), v.data_ptr(), None, None, shape, BF16, dev
+    if dtype not in _FP8_TYPES:
+        raise TypeError(f"unsupported cache type {dtype}; use bfloat16 or FP8 E4M3 codes")
+    for t in (ks, vs):
+        if t is None or t.dtype != torch.uint8 or t.shape != shape[:3]:
+            raise ValueError("an FP8 cache needs uint8 scales of [n_pages, page_size, H_kv]")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("the scales must be contiguous and on the cache's device")
+    return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape, BF16_FP8KV, dev
+
+
+def _table_args(page_table, kv_len, q_start, dev):
+    """(pointers of page_table, kv_len, q_start, B, max_pages), checked."""
+    B, max_pages = page_table.shape if page_table.dim() == 2 else (-1, -1)
+    table, lens = _index(page_table, "page_table", 2, dev), _index(kv_len, "kv_len", 1, dev)
+    if kv_len.shape[0] != B:
+        raise ValueError("kv_len must be [B], page_table [B, max_pages]")
+    if q_start is None:
+        return table, lens, None, B, max_pages
+    start = _index(q_start, "q_start", 1, dev)
+    if q_start.shape[0] != B + 1:
         raise ValueError("q_start must be [B + 1]")
-    for t in (kv_len, page_table, q_start):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("kv_len, page_table and q_start must be int32")
-    dev = cache.k.device
-    for t in (cache.v, cache.k_scale, cache.v_scale, kv_len, page_table, q_start):
-        if t is not None and t.device != dev:
-            raise ValueError("every tensor must be on the cache's device")
-    n_pages, page_size, H_kv, D = cache.k.shape
-    return PagedShape(B, n_tok, page_table.shape[1], n_pages, page_size, H_q, H_kv, D,
-                      BF16_FP8KV if cache.fp8 else BF16), dev
+    return table, lens, start, B, max_pages
 
 
-def _token_rows(name, t, heads, D, dev):
-    """Token stride of a bf16 [n_tok, heads, D] tensor whose heads and dims are contiguous."""
-    if t.dim() != 3 or t.shape[1:] != (heads, D) or t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be a bfloat16 [n_tok, {heads}, {D}] tensor")
-    if t.device != dev:
+def _token_rows(t, name, heads, D, dev):
+    """(rows, token stride) of a bf16 [n_tok, heads, D] tensor; only tokens may be strided."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or t.dtype != torch.bfloat16 or (heads and shape[1] != heads):
+        raise ValueError(f"{name} must be a bfloat16 [n_tok, {heads or 'H_q'}, {D}] tensor")
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
-    if t.shape[0] <= 1 and t.is_contiguous():
-        return heads * D
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous (only tokens may be strided)")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return shape[0], s[0] if shape[0] > 1 else shape[1] * D
+
+
+def _current_stream(dev):
+    """Raw current stream of device `dev` if that is the current device, else None."""
+    return torch._C._cuda_getCurrentRawStream(dev) if torch._C._cuda_getDevice() == dev else None
 
 
 class _on:
-    """The tensors' device as the current one, and `stream` (default: its current stream) as
-    the stream that outputs and workspaces are allocated and the call is enqueued on."""
+    """Device `dev` as the current one and `stream` (None: its current stream) as the stream
+    that outputs and workspaces are allocated and a call is enqueued on."""
 
     def __init__(self, dev, stream):
-        self.dev = torch.cuda.device(dev)
+        self.device_ctx = torch.cuda.device(dev)
         self.stream = stream
 
     def __enter__(self):
-        self.dev.__enter__()
-        self.on = torch.cuda.stream(self.stream)
-        self.on.__enter__()
-        return _stream(self.stream)
+        self.device_ctx.__enter__()
+        self.stream_ctx = torch.cuda.stream(self.stream)   # None: nothing changes
+        self.stream_ctx.__enter__()
+        return torch.cuda.current_stream()
 
     def __exit__(self, *exc):
-        self.on.__exit__(*exc)
-        self.dev.__exit__(*exc)
+        self.stream_ctx.__exit__(*exc)
+        self.device_ctx.__exit__(*exc)
 
 
 def kv_cache_write(cache: PagedKVCache, k_new, v_new, q_start, kv_len, page_table, *, stream=None) -> None:
     """Write the chunks' keys and values (bf16 [n_tok, H_kv, D], tokens may be strided) into
     their pages, quantised if the cache is FP8.  Sequence b's chunk is rows q_start[b] ..
     q_start[b + 1] - 1 and holds its last positions; kv_len counts the chunk."""
-    lib = load()
-    H_kv, D = cache.k.shape[2], cache.k.shape[3]
-    shape, dev = _paged_args(cache, kv_len, page_table, q_start, k_new.shape[0], H_kv)
-    ks, vs = _token_rows("k_new", k_new, H_kv, D, dev), _token_rows("v_new", v_new, H_kv, D, dev)
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have one shape")
-    with _on(dev, stream) as st:
-        _check("kv_cache_write",
-               lib.kv_cache_write(_ptr(k_new), _ptr(v_new), ks, vs, _ptr(q_start), _ptr(kv_len),
-                                  _ptr(page_table), ctypes.byref(shape), _ptr(cache.k), _ptr(cache.v),
-                                  _ptr(cache.k_scale), _ptr(cache.v_scale), st))
+    lib = _lib or load()
+    k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _current_stream(dev)
+    if stream is not None or st is None:
+        if stream is None or stream.cuda_stream != st:
+            with _on(dev, stream):
+                return kv_cache_write(cache, k_new, v_new, q_start, kv_len, page_table)
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    n_tok, k_stride = _token_rows(k_new, "k_new", H_kv, D, dev)
+    n_v, v_stride = _token_rows(v_new, "v_new", H_kv, D, dev)
+    if n_v != n_tok:
+        raise ValueError("k_new and v_new must have the same tokens")
+    shape, _ = _paged_shape(B, n_tok, max_pages, n_pages, page_size, H_kv, H_kv, D, dtype)
+    status = lib.kv_cache_write(k_new.data_ptr(), v_new.data_ptr(), k_stride, v_stride, start, lens,
+                                table, shape, k, v, ks, vs, st)
+    if status:
+        _check("kv_cache_write", status)
 
 
 def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None = None, out=None,
@@ -857,36 +898,36 @@ def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None 
     hip_select, sparse_attn_decode and the index builders read.  `out`: (k, v) to write into
     (rows behind a sequence's end stay as they are); else new tensors, zero there, of T_max
     (default: max_pages * page_size) rows."""
-    lib = load()
-    n_pages, page_size, H_kv, D = cache.k.shape
-    shape, dev = _paged_args(cache, kv_len, page_table, None, 0, H_kv)
-    with _on(dev, stream) as st:
-        if out is None:
-            T_max = shape.max_pages * page_size if T_max is None else int(T_max)
-            out = tuple(torch.zeros(shape.B, T_max, H_kv, D, dtype=torch.bfloat16, device=dev)
-                        for _ in range(2))
-        k, v = out
-        _need_cuda(k, v)
-        if k.dim() != 4 or k.shape != v.shape or (k.shape[0],) + tuple(k.shape[2:]) != (shape.B, H_kv, D) or \
-                (T_max is not None and k.shape[1] != T_max):
-            raise ValueError("out must be two [B, T_max, H_kv, D] tensors")
-        if any(t.dtype != torch.bfloat16 or t.device != dev for t in out):
-            raise ValueError("out must be bfloat16 on the cache's device")
-        _check("kv_cache_read",
-               lib.kv_cache_read(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-                                 _ptr(kv_len), _ptr(page_table), ctypes.byref(shape), k.shape[1],
-                                 _ptr(k), _ptr(v), st))
-    return k, v
+    lib = _lib or load()
+    k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _current_stream(dev)
+    if stream is not None or st is None:
+        if stream is None or stream.cuda_stream != st:
+            with _on(dev, stream):
+                return kv_cache_read(cache, kv_len, page_table, T_max=T_max, out=out)
+    table, lens, _, B, max_pages = _table_args(page_table, kv_len, None, dev)
+    shape, _ = _paged_shape(B, 0, max_pages, n_pages, page_size, H_kv, H_kv, D, dtype)
+    if out is None:
+        rows = max_pages * page_size if T_max is None else int(T_max)
+        out = tuple(torch.zeros(B, rows, H_kv, D, dtype=torch.bfloat16, device=cache.k.device)
+                    for _ in range(2))
+    k_out, v_out = out
+    rows = k_out.shape[1] if T_max is None else int(T_max)
+    for t in out:
+        if t.shape != (B, rows, H_kv, D) or t.dtype != torch.bfloat16:
+            raise ValueError("out must be two bfloat16 [B, T_max, H_kv, D] tensors")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("out must be contiguous and on the cache's device")
+    status = lib.kv_cache_read(k, v, ks, vs, lens, table, shape, rows, k_out.data_ptr(), v_out.data_ptr(), st)
+    if status:
+        _check("kv_cache_read", status)
+    return k_out, v_out
 
 
 def paged_attn_workspace_bytes(q, cache: PagedKVCache, page_table) -> int:
-    lib = load()
-    n = ctypes.c_size_t()
     n_pages, page_size, H_kv, D = cache.k.shape
-    shape = PagedShape(page_table.shape[0], q.shape[0], page_table.shape[1], n_pages, page_size,
-                       q.shape[1], H_kv, D, BF16_FP8KV if cache.fp8 else BF16)
-    _check("paged_attn_workspace", lib.paged_attn_workspace(ctypes.byref(shape), ctypes.byref(n)))
-    return n.value
+    return _paged_shape(page_table.shape[0], q.shape[0], page_table.shape[1], n_pages, page_size,
+                        q.shape[1], H_kv, D, BF16_FP8KV if cache.fp8 else BF16)[1]
 
 
 def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: int = 0,
@@ -896,33 +937,41 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
     cache, which holds their own keys already (kv_cache_write).  A row at position p attends
     every key j <= p, or with n_stream the n_stream newest of them (its own included) beside
     the first n_sink.  Returns (out [n_tok, H_q, D], lse [n_tok, H_q] or None)."""
-    lib = load()
-    H_kv, D = cache.k.shape[2], cache.k.shape[3]
-    if q.dim() != 3:
-        raise ValueError("q must be [n_tok, H_q, D]")
-    n_tok, H_q = q.shape[0], q.shape[1]
-    shape, dev = _paged_args(cache, kv_len, page_table, q_start, n_tok, H_q)
-    qs = _token_rows("q", q, H_q, D, dev)
-    if n_stream is not None and n_stream < 0:
+    lib = _lib or load()
+    k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _current_stream(dev)
+    if stream is not None or st is None:
+        if stream is None or stream.cuda_stream != st:
+            with _on(dev, stream):
+                return paged_attn(q, cache, q_start, kv_len, page_table, n_sink=n_sink, n_stream=n_stream,
+                                  scale=scale, out=out, lse=lse, want_lse=want_lse, workspace=workspace)
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
+    H_q = q.shape[1]
+    if n_stream is None:
+        n_stream = -1
+    elif n_stream < 0:
         raise ValueError("n_stream must be >= 0, or None for every key")
-    if scale is None:
-        scale = D ** -0.5
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty(n_tok, H_q, D, dtype=q.dtype, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(n_tok, H_q, dtype=torch.float32, device=dev)
-        _need_cuda(out, lse)
-        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
-            raise ValueError("out must be a bfloat16 tensor of q's shape on its device")
-        if lse is not None and (lse.shape != (n_tok, H_q) or lse.dtype != torch.float32 or lse.device != dev):
-            raise ValueError("lse must be a float32 [n_tok, H_q] tensor on q's device")
-        nbytes = paged_attn_workspace_bytes(q, cache, page_table)
-        ws = _workspace(nbytes, dev, workspace)
-        _check("paged_attn",
-               lib.paged_attn(_ptr(q), qs, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
-                              _ptr(cache.v_scale), _ptr(q_start), _ptr(kv_len), _ptr(page_table),
-                              ctypes.byref(shape), n_sink, -1 if n_stream is None else n_stream,
-                              ctypes.c_float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-                              ctypes.c_size_t(ws.numel() * ws.element_size()), st))
+    shape, nbytes = _paged_shape(B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D, dtype)
+    device = q.device
+    if out is None:
+        out = torch.empty((n_tok, H_q, D), dtype=torch.bfloat16, device=device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape on its device")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((n_tok, H_q), dtype=torch.float32, device=device)
+    elif lse.shape != (n_tok, H_q) or lse.dtype != torch.float32 or lse.get_device() != dev or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [n_tok, H_q] tensor on q's device")
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the cache's device")
+    status = lib.paged_attn(q.data_ptr(), q_stride, k, v, ks, vs, start, lens, table, shape, n_sink, n_stream,
+                            D ** -0.5 if scale is None else scale, out.data_ptr(),
+                            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), st)
+    if status:
+        _check("paged_attn", status)
     return out, lse

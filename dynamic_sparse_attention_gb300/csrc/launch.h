@@ -276,8 +276,10 @@ int kv_cache_check_word();
 constexpr int kPagedMaxCtas = 152;   // shares of a launch, at most (GB300's SMs)
 // A cut item, as the share in which it begins describes it to the merge.
 struct PagedPiece {
-  long long item_u0, total;        // first schedule unit of the item; units of the launch
-  int n, w;                        // key tiles, units per tile
+  long long item_u0;               // first schedule unit of the item
+  long long q;                     // units per share (the first r of the P shares: one more)
+  int r, P;
+  int n, lw;                       // key tiles, log2 of the units per tile
   int tok0, ntok, g;               // first token row, tokens, KV head
   int valid;
 };

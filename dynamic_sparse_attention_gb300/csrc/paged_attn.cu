@@ -42,6 +42,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "api_common.h"
@@ -85,6 +86,7 @@ struct Cfg {
   static constexpr int kSlots = FP8 ? 3 : 5;                // operand ring (K and V tiles in order)
   static constexpr int kRawSlots = FP8 ? 4 : 0;             // staging ring
   static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kClean = FP8 ? 0 : 4;                // value tiles checked ahead of their use
   // registers a thread after the split by warpgroup (softmax x 2, warps 8-11, converters);
   // what the launch holds, threads x kRegLaunch, is what the shares add up to
   static constexpr int kRegLaunch = FP8 ? 128 : 168;
@@ -97,10 +99,10 @@ struct Cfg {
   static constexpr uint32_t oMl = oMeta + kMetaRing * sizeof(TileMeta);
   static constexpr uint32_t oBar = oMl + kRows * 8;         // stream 1's (m, l) of one-tile items
   // q_full, q_empty, slot full/empty, raw full/empty, s_full x2, p_full x2, o_final x2,
-  // ml_ready, o1_free, fin
-  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 6 + 3;
+  // ml_ready, o1_free, fin, clean
+  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 6 + 3 + kClean;
   static constexpr uint32_t oMisc = oBar + kBars * 8;
-  static constexpr uint32_t kBytes = oMisc + 64 + 1024;
+  static constexpr uint32_t kBytes = oMisc + 96 + 1024;
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -116,7 +118,7 @@ struct Args {
   float *part_ml;        // [2 * max_ctas][part_rows][2]
   PagedPiece *piece;     // [max_ctas]
   int B, n_tok, max_pages, n_pages, page_size, lg_page, H_q, H_kv, G, TT;
-  int part_rows, min_units;
+  int part_rows, lg_min_units;
   int n_sink, n_stream;  // n_stream < 0: no window
   float sl2;
 };
@@ -130,7 +132,7 @@ struct Entry {
   int p_hi;            // position of the last one (< 0: no row sees a key)
   int ns, w0;          // tiles [0, ns), then [w0, w0 + n - ns)
   int n;               // tiles (at least 1: an entry without keys still writes its rows)
-  int w;               // schedule weight of a tile: 2 for two query tiles, 1 for one
+  int lw;              // log2 of a tile's schedule weight: two query tiles weigh 2, one 1
   bool keys;           // some row sees a key
 };
 
@@ -159,7 +161,7 @@ __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) 
   e.ntok = min(2 * a.TT, s.nq - m * 2 * a.TT);
   e.p0 = s.kv - s.nq + m * 2 * a.TT;
   e.p_hi = e.p0 + e.ntok - 1;
-  e.w = e.ntok > a.TT ? 2 : 1;
+  e.lw = e.ntok > a.TT ? 1 : 0;
   e.ns = e.w0 = e.n = 0;
   if (e.p_hi >= 0) {
     const int last = e.p_hi / kKeys;
@@ -183,6 +185,16 @@ __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) 
   return e;
 }
 
+// What a CTA's planning leaves for its warps: the share [u0, u1), the item it begins in (first
+// unit, sequence, pair, KV head) and how the launch's units are dealt out.
+struct Plan {
+  long long item_u0, u0, u1, q;
+  int r, P;
+  int b, m, g;
+  Seq s;
+};
+static_assert(sizeof(Plan) <= 80, "room behind the barriers");
+
 // A CTA's walk over the items of its share [u0, u1) of schedule units.
 struct Walk {
   long long u0, u1;     // the share
@@ -194,10 +206,14 @@ struct Walk {
   bool valid;
 };
 
-__device__ __forceinline__ void piece_of(long long u0, long long u1, long long item_u0, int n, int w,
+// first unit of share c: the units are dealt out q to each, the first r shares one more
+__device__ __forceinline__ long long share_begin(long long q, int r, int c) { return q * c + min(c, r); }
+
+// tiles [t0, t1) of an item (n tiles of 2^lw units from item_u0 on) in the share [u0, u1)
+__device__ __forceinline__ void piece_of(long long u0, long long u1, long long item_u0, int n, int lw,
                                          int &t0, int &t1) {
-  t0 = u0 > item_u0 ? static_cast<int>(min((u0 - item_u0) / w, static_cast<long long>(n))) : 0;
-  t1 = u1 < item_u0 + static_cast<long long>(n) * w ? static_cast<int>((u1 - item_u0) / w) : n;
+  t0 = u0 > item_u0 ? static_cast<int>(min((u0 - item_u0) >> lw, static_cast<long long>(n))) : 0;
+  t1 = u1 < item_u0 + (static_cast<long long>(n) << lw) ? static_cast<int>((u1 - item_u0) >> lw) : n;
 }
 
 // the first non-empty piece at or after the current item
@@ -205,9 +221,9 @@ __device__ __forceinline__ void walk_settle(const Args &a, Walk &w) {
   while (true) {
     w.valid = w.item_u0 < w.u1;
     if (!w.valid) return;
-    piece_of(w.u0, w.u1, w.item_u0, w.e.n, w.e.w, w.t0, w.t1);
+    piece_of(w.u0, w.u1, w.item_u0, w.e.n, w.e.lw, w.t0, w.t1);
     if (w.t1 > w.t0) return;
-    w.item_u0 += static_cast<long long>(w.e.n) * w.e.w;
+    w.item_u0 += static_cast<long long>(w.e.n) << w.e.lw;
     if (++w.g == a.H_kv) {
       w.g = 0;
       ++w.m;
@@ -225,7 +241,7 @@ __device__ __forceinline__ void walk_settle(const Args &a, Walk &w) {
 }
 
 __device__ __forceinline__ void walk_next(const Args &a, Walk &w) {
-  w.u0 = max(w.u0, w.item_u0 + static_cast<long long>(w.e.n) * w.e.w);   // this item is done
+  w.u0 = max(w.u0, w.item_u0 + (static_cast<long long>(w.e.n) << w.e.lw));   // this item is done
   walk_settle(a, w);
 }
 
@@ -300,6 +316,17 @@ __device__ __forceinline__ uint2 widen4(uint32_t c, uint32_t f) {
   return make_uint2(mul_bf16x2(y0, f), mul_bf16x2(y1, f));
 }
 
+// Lanes `mask` apart exchange: the one with `up` set gives x and takes the other's y for it.
+__device__ __forceinline__ void swap4(uint4 &x, uint4 &y, int up, int mask) {
+  uint4 t = up ? x : y;
+  t.x = __shfl_xor_sync(kFull, t.x, mask);
+  t.y = __shfl_xor_sync(kFull, t.y, mask);
+  t.z = __shfl_xor_sync(kFull, t.z, mask);
+  t.w = __shfl_xor_sync(kFull, t.w, mask);
+  if (up) x = t;
+  else y = t;
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <int N>
@@ -321,11 +348,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   uint64_t *full = bars + 2, *empty = full + C::kSlots;
   uint64_t *raw_full = empty + C::kSlots, *raw_empty = raw_full + C::kRawSlots;
   uint64_t *s_full = raw_empty + C::kRawSlots, *p_full = s_full + 2, *o_final = p_full + 2;
-  uint64_t *ml_ready = o_final + 2, *o1_free = ml_ready + 1, *fin = o1_free + 1;
+  uint64_t *ml_ready = o_final + 2, *o1_free = ml_ready + 1, *fin = o1_free + 1, *clean = fin + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + C::oMisc + 4);
-  int *s_pos = reinterpret_cast<int *>(sm + C::oMisc + 8);           // share start: b, m
-  long long *s_u = reinterpret_cast<long long *>(sm + C::oMisc + 16);   // item_u0, u0, u1, total
+  Plan *plan = reinterpret_cast<Plan *>(sm + C::oMisc + 16);
   TileMeta *meta = reinterpret_cast<TileMeta *>(sm + C::oMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -334,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], FP8 ? 4 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], FP8 ? 1 : 3);   // the MMAs that read it; bf16: and both cleaners
     }
     for (int i = 0; i < C::kRawSlots; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -348,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     mbar_init(ml_ready, 4);
     mbar_init(o1_free, 4);
     mbar_init(fin, 1);
+    for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 2);
     *abort = 0;
     fence_mbar_init();
   }
@@ -359,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   grid_dep_release();
 
   // ---------------------------------------------------------------- this CTA's share
-  // units of every sequence (in the still unused ring), their running sum, and the entry in
+  // units of every sequence (in the still unused ring), their running sum, and the item in
   // which the share begins
   {
     long long *su = reinterpret_cast<long long *>(sm);   // [B]
@@ -372,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         many = s.nq > 2 * a.TT;
         if (!many && s.nq > 0) {
           const Entry e = make_entry(a, s, 0);
-          u = static_cast<long long>(e.n) * e.w * a.H_kv;
+          u = (static_cast<long long>(e.n) << e.lw) * a.H_kv;
         }
       }
       uint32_t todo = __ballot_sync(kFull, many);
@@ -384,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         long long x = 0;
         for (int m = lane; m < np; m += 32) {
           const Entry e = make_entry(a, s, m);
-          x += static_cast<long long>(e.n) * e.w;
+          x += static_cast<long long>(e.n) << e.lw;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
@@ -408,9 +435,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       }
       // shares: at least min_units each, so that a short launch is not cut finer than pays
       const long long total = run;
-      const long long P = min(static_cast<long long>(gridDim.x), max(1ll, total / a.min_units));
-      const long long c = blockIdx.x;
-      const long long u0 = c < P ? total * c / P : total, u1 = c < P ? total * (c + 1) / P : total;
+      const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total >> a.lg_min_units)));
+      const long long q = total < (1ll << 31) ? static_cast<long long>(static_cast<uint32_t>(total) / static_cast<uint32_t>(P))
+                                              : total / P;
+      const int r = static_cast<int>(total - q * P);
+      const int c = blockIdx.x;
+      const long long u0 = c < P ? share_begin(q, r, c) : total, u1 = c < P ? share_begin(q, r, c + 1) : total;
       // the sequence that holds unit u0: the first with su[b] > u0
       int lo = 0, hi = a.B;   // su[hi] > u0 whenever u0 < total
       __syncwarp();
@@ -419,42 +449,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         if (su[mid] > u0) hi = mid;
         else lo = mid + 1;
       }
-      int m = 0;
+      int m = 0, g = 0;
       long long base = lo > 0 ? su[lo - 1] : 0;
+      Seq s = {0, 0, 0};
       if (u0 < u1 && lo < a.B) {
-        const Seq s = load_seq(a, lo);
+        s = load_seq(a, lo);
         const int np = n_pairs(a, s);
         // its pair that holds u0, 32 pairs at a time
         for (int m0 = 0; m0 < np; m0 += 32) {
           const int mm = m0 + lane;
-          long long v = 0;
+          uint32_t item = 0;   // units of one KV head: at most 2^24
           if (mm < np) {
             const Entry e = make_entry(a, s, mm);
-            v = static_cast<long long>(e.n) * e.w * a.H_kv;
+            item = static_cast<uint32_t>(e.n) << e.lw;
           }
-          const long long own = v;
+          const long long own = static_cast<long long>(item) * a.H_kv;
+          long long v = own;
+          if (np > 1) {
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(kFull, v, o);
-            if (lane >= o) v += y;
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long y = __shfl_up_sync(kFull, v, o);
+              if (lane >= o) v += y;
+            }
           }
-          const uint32_t past = __ballot_sync(kFull, base + v > u0);
+          const uint32_t past = __ballot_sync(kFull, item > 0 && base + v > u0);
           if (past) {
             const int l = __ffs(past) - 1;
             m = m0 + l;
             base += __shfl_sync(kFull, v - own, l);
+            item = __shfl_sync(kFull, item, l);
+            g = static_cast<int>(static_cast<uint32_t>(u0 - base) / item);   // below 2^31 units an entry
+            base += static_cast<long long>(item) * g;
             break;
           }
           base += __shfl_sync(kFull, v, 31);
         }
       }
       if (lane == 0) {
-        s_pos[0] = lo;
-        s_pos[1] = m;
-        s_u[0] = base;   // first unit of (b, m), KV head 0
-        s_u[1] = u0;
-        s_u[2] = u1;
-        s_u[3] = total;
+        *plan = Plan{base, u0, u1, q, r, P, lo, m, g, s};
       }
     }
   }
@@ -464,20 +496,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk w;
-  w.u0 = s_u[1];
-  w.u1 = s_u[2];
-  w.item_u0 = s_u[0];
-  w.b = s_pos[0];
-  w.m = s_pos[1];
-  w.g = 0;
+  w.u0 = plan->u0;
+  w.u1 = plan->u1;
+  w.item_u0 = plan->item_u0;
+  w.b = plan->b;
+  w.m = plan->m;
+  w.g = plan->g;
+  w.s = plan->s;
   w.valid = false;
-  const bool work = w.u0 < w.u1 && w.b < a.B;
-  if (work) {
-    w.s = load_seq(a, w.b);
+  if (w.u0 < w.u1 && w.b < a.B) {
     w.e = make_entry(a, w.s, w.m);
-    const long long item = static_cast<long long>(w.e.n) * w.e.w;
-    w.g = static_cast<int>((w.u0 - w.item_u0) / item);   // < H_kv: u0 lies in this entry
-    w.item_u0 += w.g * item;
     walk_settle(a, w);
   }
   if (tid == 0) a.piece[blockIdx.x].valid = 0;   // until this share begins a cut item
@@ -497,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     bool ok = true;
     for (; ok && w.valid; walk_next(a, w)) {
       const Entry &e = w.e;
-      const bool single = e.w == 1;
+      const bool single = e.lw == 0;
       const int T = w.t1 - w.t0;
       const int tok = rtok + (single ? 0 : i * a.TT); // token of the entry
       const bool row_ok = rtok < a.TT && tok < e.ntok;
@@ -635,6 +663,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
       const int prow = (single ? 0 : i * kRows) + row;
       if (warp_ok) {
+        long long quad_row[4];                        // output rows of the lane's quad (-1: none)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          quad_row[x] = __shfl_sync(kFull, row_ok ? static_cast<long long>(orow) : -1ll, (lane & ~3) + x);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -653,27 +685,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             for (int x = 0; x < 32; ++x)
               o[x] = !some || l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[x]) * g0);
           }
-          if (row_ok) {
-            if (whole) {
-              uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c);
+          if (whole) {
+            // 4 x 4 transpose of 16-byte pieces over four lanes: store j then covers 64
+            // contiguous bytes of row j of the quad instead of 16 bytes of every row
+            uint4 y[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                uint4 y;
-                y.x = pack_bf16x2(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1]));
-                y.y = pack_bf16x2(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3]));
-                y.z = pack_bf16x2(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5]));
-                y.w = pack_bf16x2(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7]));
-                dst[x] = y;
-              }
-            } else {
-              float4 *dst = reinterpret_cast<float4 *>(a.part) +
-                            (static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + prow;
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                dst[static_cast<size_t>(x) * a.part_rows] =
-                    make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+            for (int x = 0; x < 4; ++x) {
+              y[x].x = pack_bf16x2(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1]));
+              y[x].y = pack_bf16x2(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3]));
+              y[x].z = pack_bf16x2(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5]));
+              y[x].w = pack_bf16x2(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7]));
             }
+            swap4(y[0], y[1], lane & 1, 1);
+            swap4(y[2], y[3], lane & 1, 1);
+            swap4(y[0], y[2], lane & 2, 2);
+            swap4(y[1], y[3], lane & 2, 2);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (quad_row[x] >= 0)
+                *reinterpret_cast<uint4 *>(a.out + quad_row[x] * D + c + 8 * (lane & 3)) = y[x];
+          } else if (row_ok) {
+            float4 *dst = reinterpret_cast<float4 *>(a.part) +
+                          (static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + prow;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              dst[static_cast<size_t>(x) * a.part_rows] =
+                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
           }
         }
         if (row_ok) {
@@ -691,9 +729,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       if (i == 0 && row == 0 && w.t0 == 0 && !whole) {
         PagedPiece d;
         d.item_u0 = w.item_u0;
-        d.total = s_u[3];
+        d.q = plan->q;
+        d.r = plan->r;
+        d.P = plan->P;
         d.n = e.n;
-        d.w = e.w;
+        d.lw = e.lw;
         d.tok0 = e.tok0;
         d.ntok = e.ntok;
         d.g = w.g;
@@ -735,7 +775,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     for (; ok && w.valid; walk_next(a, w)) {
       const Entry &e = w.e;
       if (!e.keys) continue;
-      const bool single = e.w == 1;
+      const bool single = e.lw == 0;
       const int T = w.t1 - w.t0;
       // the item's query tiles, once the MMAs of the one before have read theirs
       if (q_open) {
@@ -754,17 +794,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       }
       __syncwarp();
       const int32_t *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
-      // pages and visible keys of tile k
-      auto describe = [&](int k) {
-        TileMeta *md = &meta[(tile + k) % kMetaRing];
-        const int base = tile_base(e, w.t0 + k);
+      // this lane's page of tile k
+      auto page_of = [&](int k) -> int {
         int page = a.n_pages;
-        const int pos = base + lane * R;
-        if (lane < parts && pos <= e.p_hi) {          // p_hi < capacity: inside the table
+        const int pos = tile_base(e, w.t0 + k) + lane * R;
+        if (k < T && lane < parts && pos <= e.p_hi) {   // p_hi < capacity: inside the table
           page = table[pos >> a.lg_page];
           DSA_CHECK(page >= 0 && page < a.n_pages);
           if (page < 0 || page >= a.n_pages) page = a.n_pages;
         }
+        return page;
+      };
+      int page_next = page_of(0);
+      // pages and visible keys of tile k; the next tile's pages are requested meanwhile
+      auto describe = [&](int k) {
+        TileMeta *md = &meta[(tile + k) % kMetaRing];
+        const int base = tile_base(e, w.t0 + k);
+        const int page = page_next;
+        page_next = page_of(k + 1);
         if (lane < 8) md->page[lane] = page;
         const int lo = a.n_stream < 0 ? 0 : a.n_stream == 0 ? 0x7fffffff : max(e.p0, 0) - a.n_stream + 1;
 #pragma unroll
@@ -841,21 +888,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       rp.step();
       return true;
     };
-    // value rows that no row of the item sees are zeroed in the slot
-    auto clean = [&](int k, int slot) {
+    // a value tile, once filled and (bf16 caches) rid of rows that no row of the item sees
+    Ring<FP8 ? 1 : C::kClean> rc;
+    auto next_v = [&](int &slot) -> bool {
+      if (!next(slot)) return false;
       if constexpr (!FP8) {
-        const uint4 s4 = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
-        if ((s4.x & s4.y & s4.z & s4.w) == 0xffffffffu) return;
-        const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll 1
-        for (int r = lane >> 3; r < kKeys; r += 4)    // eight lanes per 128-byte row
-          if (!((sw[r >> 5] >> (r & 31)) & 1u))
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              *reinterpret_cast<uint4 *>(sm + C::oRing + slot * C::kTile + hh * C::kHalf + r * 128 + (lane & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
+        if (!warp_wait(&clean[rc.slot], rc.phase, abort)) return false;
+        rc.step();
       }
+      return true;
     };
     auto wait_p = [&](int i) -> bool {
       if (!warp_wait(&p_full[i], p_phase[i], abort)) return false;
@@ -873,7 +914,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     for (; ok && w.valid; walk_next(a, w)) {
       const Entry &e = w.e;
       if (!e.keys) continue;
-      const bool single = e.w == 1;
+      const bool single = e.lw == 0;
       const int T = w.t1 - w.t0;
       if (!(ok = warp_wait(q_full, q_phase, abort))) break;
       q_phase ^= 1u;
@@ -888,8 +929,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           }
         for (int k = 0; ok && k < T; ++k) {
           const int i = k & 1;
-          if (!(ok = next(vs))) break;
-          clean(k, vs);
+          if (!(ok = next_v(vs))) break;
           if (!(ok = wait_p(i))) break;
           pv(i, vs, k < 2);
           release(vs);
@@ -911,8 +951,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         }
         for (int k = 0; ok && k < T; ++k) {
           const bool more = k + 1 < T;
-          if (!(ok = next(vs))) break;
-          clean(k, vs);
+          if (!(ok = next_v(vs))) break;
           if (!(ok = wait_p(0))) break;
           pv(0, vs, k == 0);
           if (more) {
@@ -946,16 +985,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       Ring<C::kSlots> rp;
       uint32_t tile = 0;
       bool ok = true;
-      auto convert = [&](int k, const uint8_t *scale) -> bool {
+      // tile k (already described) with this row's scale byte sb
+      auto convert = [&](int k, uint32_t sb_raw) -> bool {
         if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
         const TileMeta *md = &meta[(tile + k) % kMetaRing];
-        const int base = tile_base(w.e, w.t0 + k);
         const bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
-        int sb = 127;
-        if (seen) {
-          const int page = md->page[r / min(a.page_size, kKeys)];
-          sb = scale[(static_cast<size_t>(page) * a.page_size + ((base + r) & (a.page_size - 1))) * a.H_kv + w.g];
-        }
+        const int sb = seen ? static_cast<int>(sb_raw) : 127;
         // 2^e as 2^(120 + e) on the raw bits; scales above 2^7 take a second exact multiply
         const int e1 = min(sb - 127, 7);
         const uint32_t f = (static_cast<uint32_t>(e1 + 247) << 7) * 0x00010001u;
@@ -1000,18 +1035,98 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       };
       for (; ok && w.valid; walk_next(a, w)) {
         if (!w.e.keys) continue;
-        const int ahead = w.e.w == 1 ? 2 : 1;
+        const int ahead = w.e.lw == 0 ? 2 : 1;
         const int T = w.t1 - w.t0;
-        for (int k = 0; ok && k < min(ahead, T); ++k) ok = convert(k, a.k_scale);
+        // the row's page two tiles ahead and its scale bytes one tile ahead of the conversion
+        // of K, so that neither load's latency is waited for; a V byte waits (in `vq`, oldest
+        // lowest) for its tile's turn
+        const int32_t *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+        auto page_of = [&](int k) -> int {
+          const int pos = tile_base(w.e, w.t0 + k) + r;
+          if (k >= T || pos > w.e.p_hi) return -1;
+          const int page = table[pos >> a.lg_page];
+          return page >= 0 && page < a.n_pages ? page : -1;
+        };
+        auto scales_of = [&](int k, int page, uint32_t &ks, uint32_t &vs) {
+          ks = vs = 127;
+          if (page < 0) return;
+          const size_t at = (static_cast<size_t>(page) * a.page_size +
+                             ((tile_base(w.e, w.t0 + k) + r) & (a.page_size - 1))) * a.H_kv + w.g;
+          ks = a.k_scale[at];
+          vs = a.v_scale[at];
+        };
+        int front = 0, nv = 0;
+        uint32_t ks, vs, vq = 0;
+        int page = page_of(0);
+        int page_next = page_of(1);
+        scales_of(0, page, ks, vs);
+        auto convert_k = [&]() -> bool {
+          uint32_t ks1, vs1;
+          scales_of(front + 1, page_next, ks1, vs1);
+          page_next = page_of(front + 2);
+          if (!convert(front, ks)) return false;
+          vq |= vs << (8 * nv++);
+          ks = ks1;
+          vs = vs1;
+          ++front;
+          return true;
+        };
+        for (int k = 0; ok && k < min(ahead, T); ++k) ok = convert_k();
         for (int k = 0; ok && k < T; ++k) {
-          ok = convert(k, a.v_scale);
-          if (ok && k + ahead < T) ok = convert(k + ahead, a.k_scale);
+          ok = convert(k, vq & 0xffu);
+          vq >>= 8;
+          --nv;
+          if (ok && k + ahead < T) ok = convert_k();
         }
         tile += T;
       }
     }
   } else {
-    reg_dec<C::kRegMisc>();   // warps 10 and 11
+    // ---------------------------------------------------------------- warps 10, 11: cleaners
+    // value rows that no row of the item sees are zeroed in their slot (the converters do it
+    // for FP8 caches), 64 rows of every tile each
+    reg_dec<C::kRegMisc>();
+    if constexpr (!FP8) {
+      Ring<C::kSlots> rp;
+      Ring<C::kClean> rc;
+      uint32_t tile = 0;
+      bool ok = true;
+      const int half = warp - 10;
+      for (; ok && w.valid; walk_next(a, w)) {
+        if (!w.e.keys) continue;
+        const int ahead = w.e.lw == 0 ? 2 : 1;
+        const int T = w.t1 - w.t0;
+        // Every slot is waited for and released, K tiles too: only who holds a slot back sees
+        // each of its phases.
+        auto next = [&]() -> bool { return warp_wait(&full[rp.slot], rp.phase, abort); };
+        auto done = [&]() {
+          if (lane == 0) mbar_arrive(&empty[rp.slot]);
+          rp.step();
+        };
+        for (int k = 0; ok && k < min(ahead, T); ++k)
+          if ((ok = next())) done();
+        for (int k = 0; ok && k < T; ++k) {
+          if (!(ok = next())) break;
+          const uint2 seen = *reinterpret_cast<const uint2 *>(&meta[(tile + k) % kMetaRing].seen[2 * half]);
+          if ((seen.x & seen.y) != 0xffffffffu) {
+#pragma unroll 1
+            for (int r = lane >> 3; r < kKeys / 2; r += 4)   // eight lanes per 128-byte row
+              if (!(((r < 32 ? seen.x : seen.y) >> (r & 31)) & 1u))
+#pragma unroll
+                for (int hh = 0; hh < C::kHalves; ++hh)
+                  *reinterpret_cast<uint4 *>(sm + C::oRing + rp.slot * C::kTile + hh * C::kHalf +
+                                             (64 * half + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&clean[rc.slot]);
+          rc.step();
+          done();
+          if (k + ahead < T && (ok = next())) done();
+        }
+        tile += T;
+      }
+    }
   }
 
   tc_fence_before();
@@ -1032,7 +1147,7 @@ struct MergeArgs {
   const float *part, *part_ml;
   uint16_t *out;
   float *lse;
-  int part_rows, H_q, G, TT, min_units;
+  int part_rows, H_q, G, TT;
 };
 
 constexpr int kMergeRows = 8;   // rows per CTA; a warp holds 4 groups of 4 dims of them
@@ -1051,27 +1166,28 @@ __global__ void __launch_bounds__(D * 2) paged_merge_kernel(const MergeArgs a) {
   const int qt = t >= a.TT ? 1 : 0;
   const int prow = qt * kRows + (t - qt * a.TT) * a.G + j;
   const int c4 = threadIdx.x >> 3;
-  const long long P = min(static_cast<long long>(gridDim.x), max(1ll, pc.total / a.min_units));
-  const long long end = pc.item_u0 + static_cast<long long>(pc.n) * pc.w;
+  const long long end = pc.item_u0 + (static_cast<long long>(pc.n) << pc.lw);
   // the shares of the item: blockIdx.x .. last
-  long long last = blockIdx.x;
-  while (last + 1 < P && pc.total * (last + 1) / P < end) ++last;
-  auto slot_of = [&](long long c) -> int {   // < 0: an empty piece
+  const int c0 = blockIdx.x;
+  int last = c0;
+  while (last + 1 < pc.P && share_begin(pc.q, pc.r, last + 1) < end) ++last;
+  auto slot_of = [&](int c) -> int {   // < 0: an empty piece
     int t0, t1;
-    piece_of(pc.total * c / P, pc.total * (c + 1) / P, pc.item_u0, pc.n, pc.w, t0, t1);
-    return t1 > t0 ? static_cast<int>(2 * c + (t0 == 0 ? 1 : 0)) : -1;
+    piece_of(share_begin(pc.q, pc.r, c), share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
+    return t1 > t0 ? 2 * c + (t0 == 0 ? 1 : 0) : -1;
   };
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.part);
   float M = -INFINITY;
-  for (long long c = blockIdx.x; c <= last; ++c) {
+#pragma unroll 4
+  for (int c = c0; c <= last; ++c) {
     const int s = slot_of(c);
     if (s >= 0) M = fmaxf(M, ml[static_cast<size_t>(s) * a.part_rows + prow].x);
   }
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (long long c = blockIdx.x; c <= last; ++c) {
+  for (int c = c0; c <= last; ++c) {
     const int s = slot_of(c);
     if (s < 0) continue;
     const float2 v = ml[static_cast<size_t>(s) * a.part_rows + prow];
@@ -1160,7 +1276,7 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.G = G;
   a.TT = TT;
   a.part_rows = pa.part_rows;
-  a.min_units = 2;
+  a.lg_min_units = 1;
   const int cap = pa.max_pages * pa.page_size;
   a.n_sink = std::min(pa.n_sink, cap);
   a.n_stream = pa.n_stream < 0 ? -1 : std::min(pa.n_stream, cap);
@@ -1170,15 +1286,19 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // the warpgroups' register shares add up to what the launch holds; a build that holds less
   // would wait for registers that no warp gives back
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if (fa.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
+  static std::atomic<bool> regs_ok{false};
+  if (!regs_ok) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
+    regs_ok = true;
+  }
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // no more CTAs than the launch can have shares of min_units
   const long long pairs = pa.B + pa.n_tok / (2 * TT);
-  const long long most = pairs * pa.H_kv * 2 * ((cap + kKeys - 1) / kKeys + 1) / a.min_units + 1;
+  const long long most = pairs * pa.H_kv * 2 * ((cap + kKeys - 1) / kKeys + 1) / (1 << a.lg_min_units) + 1;
   const int P = static_cast<int>(std::min(static_cast<long long>(std::min(sms, kPagedMaxCtas)), most));
   {
     ProfScope ps(FP8 ? "paged_attn_fp8" : "paged_attn", s);
@@ -1195,7 +1315,6 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   ma.H_q = pa.H_q;
   ma.G = G;
   ma.TT = TT;
-  ma.min_units = a.min_units;
   const int rows = std::min(2 * TT, pa.n_tok) * G;
   ProfScope ps("paged_attn_merge", s);
   return launch_pdl(paged_merge_kernel<D>, dim3(P, (rows + kMergeRows - 1) / kMergeRows), dim3(D * 2), 0, s, ma);
