@@ -8,7 +8,8 @@
 // the value read back is exactly a bf16: E4M3 has four significant bits and 2^(e-9) >= 2^-125,
 // 448 * 2^119 < 2^127 stay inside bf16's normal range.  A floating-point code keeps the same
 // relative precision under any power of two, so a finer scale would gain nothing but the
-// top of the range.
+// top of the range.  A row that holds a NaN takes the scale byte 255 (E8M0's NaN) and reads
+// back as NaN throughout.
 //
 // Both kernels are bound by HBM: a row is read once and written once.
 #include "common.cuh"
@@ -51,15 +52,15 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
   return r;
 }
 
-// largest finite magnitude (bf16 bits) of one 16-byte piece
+// largest finite magnitude (bf16 bits) of one 16-byte piece; 0xffff if it holds a NaN
 __device__ __forceinline__ uint32_t finite_max8(const uint4 &u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-    m = max(m, lo < 0x7f80u ? lo : 0u);
-    m = max(m, hi < 0x7f80u ? hi : 0u);
+    m = max(m, lo < 0x7f80u ? lo : lo == 0x7f80u ? 0u : 0xffffu);
+    m = max(m, hi < 0x7f80u ? hi : hi == 0x7f80u ? 0u : 0xffffu);
   }
   return m;
 }
@@ -120,13 +121,14 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheWriteArgs
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
       if (slot >= 0) {
-        const int e = row_exponent(m);
+        const bool nan = m == 0xffffu;
+        const int e = nan ? 0 : row_exponent(m);
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         const size_t row = static_cast<size_t>(slot) * a.H_kv + h;
         uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + row * D);
         dst[l] = quantise8(u0, inv);
         dst[l + LPR] = quantise8(u1, inv);
-        if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = static_cast<uint8_t>(e + 127);
+        if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = static_cast<uint8_t>(nan ? 255 : e + 127);
       }
     } else if (slot >= 0) {
       const size_t row = static_cast<size_t>(slot) * a.H_kv + h;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheReadArgs a
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kThreads;
         if (i < pieces) {
-          const float f = __uint_as_float(s[u] << 23);   // 2^(s - 127); s = 0 reads as 0
+          // 2^(s - 127); s = 0 reads as 0, s = 255 as NaN
+          const float f = __uint_as_float(s[u] == 255u ? 0x7fffffffu : s[u] << 23);
           float x[8];
           f16x2_to_f32x2(e4m3x2_to_f16x2(w[u].x), x[0], x[1]);
           f16x2_to_f32x2(e4m3x2_to_f16x2(w[u].x >> 16), x[2], x[3]);

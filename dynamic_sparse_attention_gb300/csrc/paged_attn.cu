@@ -306,14 +306,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t prmt(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;\n" : "=r"(r) : "r"(x), "n"(kSel));
+  return r;
+}
+
 // Four E4M3 codes -> four bf16 times f (a power of two in both halves, 2^(120 + e)): a code's
 // seven magnitude bits at bits 4..10 of a bf16 read as its value times 2^-120 (bias 127 against
-// 7, subnormal codes as bf16 subnormals), so one exact multiply gives code * 2^e.
+// 7, subnormal codes as bf16 subnormals), so one exact multiply gives code * 2^e.  Bytes are
+// spread over halves with their sign replicated, moved up by 4 and cut to sign and magnitude:
+// three integer operations for two codes, one of which can run as a multiply on the FMA pipe
+// (the ALU pipe, at half rate, is what bounds this).
 __device__ __forceinline__ uint2 widen4(uint32_t c, uint32_t f) {
-  const uint32_t x0 = __byte_perm(c, 0u, 0x1404), x1 = __byte_perm(c, 0u, 0x3424);
-  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
-  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
-  return make_uint2(mul_bf16x2(y0, f), mul_bf16x2(y1, f));
+  const uint32_t x0 = (prmt<0x9180>(c) * 16u) & 0x87f087f0u, x1 = (prmt<0xb3a2>(c) * 16u) & 0x87f087f0u;
+  return make_uint2(mul_bf16x2(x0, f), mul_bf16x2(x1, f));
 }
 
 // Lanes `mask` apart exchange: the one with `up` set gives x and takes the other's y for it.
@@ -991,36 +999,41 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         const TileMeta *md = &meta[(tile + k) % kMetaRing];
         const bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
         const int sb = seen ? static_cast<int>(sb_raw) : 127;
-        // 2^e as 2^(120 + e) on the raw bits; scales above 2^7 take a second exact multiply
-        const int e1 = min(sb - 127, 7);
-        const uint32_t f = (static_cast<uint32_t>(e1 + 247) << 7) * 0x00010001u;
-        const int e2 = sb - 127 - e1;
+        // 2^e as 2^(120 + e) on the raw bits (scales above 2^7: see below); a row that is not
+        // seen is multiplied by 0, one with a NaN scale (255) by NaN
+        const int e1 = min(sb - 127, 7), e2 = sb - 127 - e1;
+        const uint32_t f = !seen ? 0u : sb == 255 ? 0x7fff7fffu : (static_cast<uint32_t>(e1 + 247) << 7) * 0x00010001u;
         if (!warp_wait(&empty[rp.slot], rp.phase ^ 1u, abort)) return false;
         const unsigned char *src = sm + C::oRaw + rr.slot * C::kRaw + r * D;
         unsigned char *dst = sm + C::oRing + rp.slot * C::kTile + r * 128;
+        // 16-byte piece p of the row of codes: 128-byte rows hold it at p ^ (r & 7), 64-byte
+        // rows at p ^ ((r >> 1) & 3); piece q of the bf16 row goes to q ^ (r & 7) of its half
+        auto piece = [&](int p) -> uint4 {
+          return *reinterpret_cast<const uint4 *>(src + ((D == 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3)) << 4));
+        };
+        auto put = [&](int q, const uint4 &o) {
+          *reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4)) = o;
+        };
 #pragma unroll
-        for (int p = 0; p < D / 16; ++p) {
-          // 128-byte rows are stored with piece p at p ^ (r & 7), 64-byte rows at p ^ ((r >> 1) & 3)
-          const uint4 c = *reinterpret_cast<const uint4 *>(src + ((D == 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3)) << 4));
-          uint4 o[2];
-          const uint2 y0 = widen4(c.x, f), y1 = widen4(c.y, f), y2 = widen4(c.z, f), y3 = widen4(c.w, f);
-          o[0] = make_uint4(y0.x, y0.y, y1.x, y1.y);
-          o[1] = make_uint4(y2.x, y2.y, y3.x, y3.y);
-          if (__any_sync(kFull, e2 > 0)) {
-            const uint32_t f2 = (static_cast<uint32_t>(e2 + 127) << 7) * 0x00010001u;
+        for (int p0 = 0; p0 < D / 16; p0 += 4) {
+          uint4 c[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              o[h].x = mul_bf16x2(o[h].x, f2);
-              o[h].y = mul_bf16x2(o[h].y, f2);
-              o[h].z = mul_bf16x2(o[h].z, f2);
-              o[h].w = mul_bf16x2(o[h].w, f2);
-            }
+          for (int p = 0; p < 4; ++p) c[p] = piece(p0 + p);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint2 y0 = widen4(c[p].x, f), y1 = widen4(c[p].y, f);
+            const uint2 y2 = widen4(c[p].z, f), y3 = widen4(c[p].w, f);
+            put(2 * (p0 + p), make_uint4(y0.x, y0.y, y1.x, y1.y));
+            put(2 * (p0 + p) + 1, make_uint4(y2.x, y2.y, y3.x, y3.y));
           }
-          if (!seen) o[0] = o[1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = 2 * p + h;                  // 16-byte piece of the bf16 row
-            *reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4)) = o[h];
+        }
+        if (__any_sync(kFull, seen && e2 > 0 && sb != 255)) {
+          // rare: a scale above 2^7 takes a second exact multiply
+          const uint32_t f2 = (static_cast<uint32_t>(e2 + 127) << 7) * 0x00010001u;
+#pragma unroll 1
+          for (int q = 0; seen && e2 > 0 && sb != 255 && q < D / 8; ++q) {
+            uint4 *o = reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4));
+            *o = make_uint4(mul_bf16x2(o->x, f2), mul_bf16x2(o->y, f2), mul_bf16x2(o->z, f2), mul_bf16x2(o->w, f2));
           }
         }
         fence_proxy_async_smem();

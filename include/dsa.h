@@ -411,7 +411,8 @@ int sparse_attn_prefill(const void *q, const void *k, const void *v,
  * new tokens (one token each in a decode step, a prompt, or a mix of both).
  *   k_pages, v_pages [n_pages, page_size, H_kv, D]   bf16, or FP8 E4M3 codes
  *   k_scale, v_scale [n_pages, page_size, H_kv]      FP8 only: one byte s per token and head,
- *                    the row's values are code * 2^(s - 127) (an E8M0 scale)
+ *                    the row's values are code * 2^(s - 127) (an E8M0 scale), all NaN for
+ *                    s = 255; other rows never hold the codes 0x7F and 0xFF
  *   page_table [B, max_pages] int32   page that holds positions i*page_size .. of sequence b;
  *                    entries that no position below kv_len[b] needs may hold anything
  *   q_start [B + 1] int32   rows q_start[b] .. q_start[b+1]-1 of the token tensors (n_tok
@@ -436,9 +437,9 @@ typedef struct {
  * k_new, v_new [n_tok, H_kv, D] bf16 with k_stride / v_stride elements between tokens (a
  * multiple of 8, at least H_kv * D: slices of a fused projection need no copy).  An FP8 cache
  * takes each (token, head) row with a = its largest finite magnitude as codes of x * 2^-e
- * (nearest, ties to even, saturating at 448; NaN stays NaN), e the smallest integer with
- * a * 2^-e <= 448, kept in [-116, 119] (0 for a row of zeros), and stores s = e + 127.  Every
- * value the cache then stands for is exactly a bf16.  shape->H_q is not used but checked.
+ * (nearest, ties to even, saturating at 448), e the smallest integer with a * 2^-e <= 448,
+ * kept in [-116, 119] (0 for a row of zeros), and stores s = e + 127, or s = 255 if the row
+ * holds a NaN.  Every value the cache then stands for is exactly a bf16.  shape->H_q is not used but checked.
  * Errors: INVALID_ARG / UNSUPPORTED (shape, strides), ALIGNMENT, CUDA. */
 int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, long long v_stride,
                    const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,

@@ -9,7 +9,7 @@ from __future__ import annotations
 import numpy as np
 
 E4M3_MAX = 448.0
-E_MIN, E_MAX = -116, 119
+E_MIN, E_MAX, E_NAN = -116, 119, 128
 
 
 def e4m3_grid() -> np.ndarray:
@@ -34,18 +34,22 @@ def e4m3_codes(y: np.ndarray) -> np.ndarray:
 
 
 def quantise(x: np.ndarray):
-    """Rows x [..., D] (float64 values of bf16 elements) -> (codes [..., D], exponents e)."""
+    """Rows x [..., D] (float64 values of bf16 elements) -> (codes [..., D], exponents e; E_NAN
+    for a row that holds a NaN)."""
     a = np.where(np.isfinite(x), np.abs(x), 0.0).max(-1)
     m, p = np.frexp(np.where(a > 0, a, 1.0))          # a = m 2^p, 0.5 <= m < 1
     e = p - 9 + (m > 0.875)                           # smallest e with a <= 448 * 2^e
     e = np.where(a > 0, np.clip(e, E_MIN, E_MAX), 0)
+    nan = np.isnan(x).any(-1)
+    e = np.where(nan, 0, e)
     with np.errstate(invalid="ignore"):
-        return e4m3_codes(np.ldexp(x, -e[..., None])), e
+        return e4m3_codes(np.ldexp(x, -e[..., None])), np.where(nan, E_NAN, e)
 
 
 def dequantise(codes: np.ndarray, e: np.ndarray) -> np.ndarray:
     g = np.append(e4m3_grid(), np.nan)
-    return np.ldexp(g[codes & 127] * np.where(codes > 127, -1.0, 1.0), e[..., None])
+    x = np.ldexp(g[codes & 127] * np.where(codes > 127, -1.0, 1.0), e[..., None])
+    return np.where(e[..., None] == E_NAN, np.nan, x)
 
 
 def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float):
