@@ -16,16 +16,21 @@
 // kernel merges them.
 //
 // One CTA, two streams of scores (i = 0, 1), each with its own TMEM buffers S_i, O_i and its
-// own softmax warpgroup, so that one stream's softmax runs while the tensor core works for
+// own four softmax warps, so that one stream's softmax runs while the tensor core works for
 // the other:
 //   two-tile items: stream i is query tile i, both see every key tile (256 rows per loaded
 //     K/V tile);
 //   one-tile items (a few tokens): both streams hold the same query tile and take the key
 //     tiles alternately; their halves are merged in TMEM at the end of the item.
-// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row, 128 keys), 8 producer
-// (TMA), 9 MMA issuer; FP8 caches add the converter warps 12-15, which widen the E4M3 tiles
-// that TMA brings into a staging ring to bf16 operand tiles (exact: code * 2^e is a bf16).
-//   S_i = Q_i K^T (M = N = 128, K = D), P over the first half of S_i, O_i += P V.
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (TMA), 9 MMA
+// issuer (one thread), 10 scheduler, 11 cleaner (bf16 caches), 12-15 epilogue (results out of
+// TMEM while the softmax warps are at the next item); FP8 caches add the converter warps 16-23,
+// which widen the E4M3 tiles that TMA brings into a staging ring to bf16 operand tiles (exact:
+// code * 2^e is a bf16), four warps the K tiles and four the V tiles.  The scheduler walks the share and hands out its items
+// through a small ring, so that no other role holds that state: beside 224 KB of shared memory
+// next to no L1 is left, and a spilled register costs a round trip to L2.
+//   S_i = Q_i K^T (M = N = 128, K = D), P over S_i (each 32 columns' P in the first 16),
+//   O_i += P V.
 // Each stream issues P V (tile t) and right behind it Q K^T (its next tile): S_i full then
 // also says that P V before it has retired, so moving the softmax reference (O rescaled in
 // TMEM) needs no wait of its own.
@@ -74,8 +79,23 @@ static __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
 
 struct TileMeta {
   uint32_t seen[kKeys / 32];   // bit c: key c of the tile is in a good page and some row sees it
-  int page[8];                 // page of each 16..128-key part (n_pages: none, reads as zero)
 };
+
+// A piece of the CTA's share: key tiles [t0, t0 + T) of one item (kinds: see Walk).
+struct alignas(16) Item {
+  int ns, w0;          // the entry's tiles: [0, ns), then from w0 on
+  int t0, T;
+  int tok0, ntok;      // first token row (global), tokens
+  int p0, p_hi;        // positions of the first and the last token
+  int b, g;            // sequence, KV head
+  int flags;           // kSingle ...
+};
+constexpr int kItems = 4;      // pieces handed out ahead
+constexpr int kSingle = 1;     // one query tile: both streams take turns over the key tiles
+constexpr int kHasKeys = 2;    // some row sees a key
+constexpr int kWhole = 4;      // every tile of the item: the result is final
+constexpr int kStart = 8;      // the item's first tile
+constexpr int kEnd = 16;       // no piece: the share is done
 
 template <int D, bool FP8>
 struct Cfg {
@@ -85,27 +105,38 @@ struct Cfg {
   static constexpr uint32_t kRaw = kKeys * D;               // an FP8 tile
   static constexpr int kSlots = FP8 ? 3 : 5;                // operand ring (K and V tiles in order)
   static constexpr int kRawSlots = FP8 ? 4 : 0;             // staging ring
-  static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kClean = FP8 ? 0 : 4;                // value tiles checked ahead of their use
-  // registers a thread after the split by warpgroup (softmax x 2, warps 8-11, converters);
-  // what the launch holds, threads x kRegLaunch, is what the shares add up to
-  static constexpr int kRegLaunch = FP8 ? 128 : 168;
-  static constexpr int kRegSoft = FP8 ? 184 : 208, kRegMisc = FP8 ? 56 : 88, kRegConv = FP8 ? 88 : 0;
-  static_assert(256 * kRegSoft + 128 * kRegMisc + 128 * kRegConv == kThreads * kRegLaunch, "register split");
+  static constexpr int kClean = FP8 ? 0 : 4;                // value tiles cleaned ahead of their use
+  static constexpr int kSoft = 8;                           // softmax warps
+  static constexpr int kEpi = kSoft + 4, kConv = kEpi + 4;  // first epilogue and converter warps
+  static constexpr int kThreads = (kEpi + 4 + (FP8 ? 8 : 0)) * 32;
+  // registers a thread after the split by warpgroup (softmax x 2, warps 8-11, epilogue,
+  // converters x 2); what the launch holds, threads x kRegLaunch, is what the shares add up to
+  static constexpr int kRegLaunch = FP8 ? 80 : 128;
+  static constexpr int kRegSoft = FP8 ? 96 : 176, kRegMisc = FP8 ? 64 : 72, kRegEpi = FP8 ? 80 : 88,
+                       kRegConv = FP8 ? 72 : 0;
+  static_assert(256 * kRegSoft + 128 * kRegMisc + 128 * kRegEpi + 256 * kRegConv == kThreads * kRegLaunch,
+                "register split");
+  // Scores a thread holds at a time.  bf16: the whole row of the tile.  FP8: 32, read from TMEM
+  // once for the maximum and again for P: the unrolled body beside the converters' did not
+  // fit the instruction cache (3.3 of 10 stall cycles were instruction fetches).
+  static constexpr int kPart = FP8 ? 32 : 128;
   static constexpr uint32_t oQ = 0;
   static constexpr uint32_t oRing = oQ + 2 * kTile;
   static constexpr uint32_t oRaw = oRing + kSlots * kTile;
   static constexpr uint32_t oMeta = oRaw + kRawSlots * kRaw;
-  static constexpr uint32_t oMl = oMeta + kMetaRing * sizeof(TileMeta);
-  static constexpr uint32_t oBar = oMl + kRows * 8;         // stream 1's (m, l) of one-tile items
-  // q_full, q_empty, slot full/empty, raw full/empty, s_full x2, p_full x2, o_final x2,
-  // ml_ready, o1_free, fin, clean
-  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 6 + 3 + kClean;
+  static constexpr uint32_t oMl = oMeta + kMetaRing * sizeof(TileMeta);   // [2 streams][128 rows] (m, l)
+  static constexpr uint32_t oItem = oMl + 2 * kRows * 8;
+  static constexpr uint32_t oBar = oItem + kItems * sizeof(Item);
+  // q_full, q_empty, slot full/empty, raw full/empty, then for both streams s_full, p_full,
+  // o_final, ml_full, drained; fin, clean, item full/empty
+  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 10 + 1 + kClean + 2 * kItems;
+  static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item
   static constexpr uint32_t oMisc = oBar + kBars * 8;
-  static constexpr uint32_t kBytes = oMisc + 96 + 1024;
+  static constexpr uint32_t kBytes = oMisc + 16;
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(kSlots * kTile >= 4096 * 8, "planning scratch");
 };
 
 struct Args {
@@ -245,38 +276,49 @@ __device__ __forceinline__ void walk_next(const Args &a, Walk &w) {
   walk_settle(a, w);
 }
 
-// key tile `k` of an entry -> its first key
-__device__ __forceinline__ int tile_base(const Entry &e, int k) {
-  return (k < e.ns ? k : e.w0 + k - e.ns) * kKeys;
+// first key of tile k of a piece
+__device__ __forceinline__ int tile_base(const Item &it, int k) {
+  const int t = it.t0 + k;
+  return (t < it.ns ? t : it.w0 + t - it.ns) * kKeys;
 }
 
 // ------------------------------------------------------------------ waits
 
-// Bounded wait: gives up when another thread of the CTA did, or after the limit.
-__device__ __forceinline__ bool slow_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  const uint64_t t0 = global_ns();
-  const uint64_t limit = g_wait_limit_ns;
-  const uint32_t hint = limit < 20000ull ? static_cast<uint32_t>(limit) : 20000u;
-  uint32_t spins = 0;
-  while (true) {
-    if (mbar_try_wait_hint(bar, parity, hint)) return true;
-    if (*abort) return false;
-    if ((++spins & 3u) == 0u && global_ns() - t0 > limit) {
-      *abort = 1;
+// What bounds the waits of a CTA: set once one gave up, and the limit in clocks.
+struct WaitCtl {
+  volatile int *abort;   // [0] gave up, [1] limit
+  __device__ __forceinline__ bool over(uint32_t t0) const {
+    return abort[0] || clock_lo() - t0 > static_cast<uint32_t>(abort[1]);
+  }
+  static __device__ __forceinline__ uint32_t clock_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%clock;\n" : "=r"(t));
+    return t;
+  }
+};
+
+// one thread waits
+__device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = WaitCtl::clock_lo();
+  while (!mbar_try_wait(bar, parity))
+    if (w.over(t0)) {
+      w.abort[0] = 1;
       return false;
     }
-  }
+  return true;
 }
 
 // the whole warp waits; the outcome is warp-uniform
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
   if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = slow_wait(bar, parity, abort) ? 1 : 0;
-  ok = __shfl_sync(kFull, ok, 0);
-  // every lane observes the phase itself, so that what was released by it is visible to it
-  if (ok && !mbar_try_wait(bar, parity)) ok = 0;
-  return __all_sync(kFull, ok) != 0;
+  const uint32_t t0 = WaitCtl::clock_lo();
+  while (!__all_sync(kFull, mbar_try_wait(bar, parity)))
+    if (__any_sync(kFull, w.over(t0))) {
+      w.abort[0] = 1;
+      return false;
+    }
+  return true;
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
@@ -345,48 +387,64 @@ template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
+// a share below, at or above what the launch holds
+template <int N, int kLaunch>
+__device__ __forceinline__ void reg_set() {
+  if constexpr (N > kLaunch) reg_inc<N>();
+  else if constexpr (N < kLaunch) reg_dec<N>();
+}
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, FP8>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::oBar);
   uint64_t *q_full = bars, *q_empty = bars + 1;
   uint64_t *full = bars + 2, *empty = full + C::kSlots;
   uint64_t *raw_full = empty + C::kSlots, *raw_empty = raw_full + C::kRawSlots;
   uint64_t *s_full = raw_empty + C::kRawSlots, *p_full = s_full + 2, *o_final = p_full + 2;
-  uint64_t *ml_ready = o_final + 2, *o1_free = ml_ready + 1, *fin = o1_free + 1, *clean = fin + 1;
+  uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *fin = drained + 2;
+  uint64_t *clean = fin + 1, *item_full = clean + C::kClean, *item_empty = item_full + kItems;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
-  volatile int *abort = reinterpret_cast<volatile int *>(sm + C::oMisc + 4);
-  Plan *plan = reinterpret_cast<Plan *>(sm + C::oMisc + 16);
+  const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4)};
+  Plan *plan = reinterpret_cast<Plan *>(sm + C::oMl);   // read before the first piece is handed out
   TileMeta *meta = reinterpret_cast<TileMeta *>(sm + C::oMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(sm) & 1023u) {   // the swizzled tiles need 1024-byte atoms
+    if (tid == 0) atomicExch(&g_paged_error, 1);
+    return;
+  }
 
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], FP8 ? 4 : 1);
-      mbar_init(&empty[i], FP8 ? 1 : 3);   // the MMAs that read it; bf16: and both cleaners
+      mbar_init(&empty[i], FP8 ? 1 : 2);   // the MMAs that read it; bf16: and the cleaner
     }
     for (int i = 0; i < C::kRawSlots; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_final[i], 1);
+      mbar_init(&ml_full[i], 4);
+      mbar_init(&drained[i], 4);
     }
-    mbar_init(ml_ready, 4);
-    mbar_init(o1_free, 4);
     mbar_init(fin, 1);
-    for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 2);
-    *abort = 0;
+    for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], C::kReaders);
+    }
+    abort.abort[0] = 0;
+    // about two clocks a nanosecond; at most 2^31 of them, a second
+    abort.abort[1] = static_cast<int>(min(2ull * g_wait_limit_ns, 0x7fffffffull));
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == C::kSoft + 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -397,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   // units of every sequence (in the still unused ring), their running sum, and the item in
   // which the share begins
   {
-    long long *su = reinterpret_cast<long long *>(sm);   // [B]
+    long long *su = reinterpret_cast<long long *>(sm + C::oRing);   // [B]
     for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
       const int b = b0 + tid;
       long long u = 0;
@@ -444,9 +502,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       // shares: at least min_units each, so that a short launch is not cut finer than pays
       const long long total = run;
       const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total >> a.lg_min_units)));
-      const long long q = total < (1ll << 31) ? static_cast<long long>(static_cast<uint32_t>(total) / static_cast<uint32_t>(P))
-                                              : total / P;
-      const int r = static_cast<int>(total - q * P);
+      // total / P digit by digit (total < 2^46: 4096 sequences of 2^23 tiles, twice, 128 heads
+      // at most, and P < 2^16)
+      const uint32_t up = static_cast<uint32_t>(P), high = static_cast<uint32_t>(total >> 16);
+      const uint32_t mid = ((high % up) << 16) | static_cast<uint32_t>(total & 0xffff);
+      const long long q = (static_cast<long long>(high / up) << 16) + mid / up;
+      const int r = static_cast<int>(mid % up);
       const int c = blockIdx.x;
       const long long u0 = c < P ? share_begin(q, r, c) : total, u1 = c < P ? share_begin(q, r, c + 1) : total;
       // the sequence that holds unit u0: the first with su[b] > u0
@@ -503,82 +564,91 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk w;
-  w.u0 = plan->u0;
-  w.u1 = plan->u1;
-  w.item_u0 = plan->item_u0;
-  w.b = plan->b;
-  w.m = plan->m;
-  w.g = plan->g;
-  w.s = plan->s;
-  w.valid = false;
-  if (w.u0 < w.u1 && w.b < a.B) {
-    w.e = make_entry(a, w.s, w.m);
-    walk_settle(a, w);
-  }
-  if (tid == 0) a.piece[blockIdx.x].valid = 0;   // until this share begins a cut item
+  Item *items = reinterpret_cast<Item *>(sm + C::oItem);
+  // Readers of the item ring: the next piece into `it` (a copy), false at the end
+  Ring<kItems> ri;
+  auto next_item = [&](Item &it) -> bool {
+    if (!warp_wait(&item_full[ri.slot], ri.phase, abort)) return false;
+    it = items[ri.slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[ri.slot]);
+    ri.step();
+    return !(it.flags & kEnd);
+  };
 
-  if (warp < 8) {
-    // ---------------------------------------------------------------- softmax, epilogue
-    reg_inc<C::kRegSoft>();
+  if (warp < C::kSoft) {
+    // ---------------------------------------------------------------- softmax
+    reg_set<C::kRegSoft, C::kRegLaunch>();
     const int i = warp >> 2;                          // stream
     const int row = (warp & 3) * 32 + lane;           // row of the query tile
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = tl + C::cS + i * kKeys;
     const uint32_t o_col = tl + C::cO + i * D;
-    float2 *ml = reinterpret_cast<float2 *>(sm + C::oMl);
-    const int rtok = row / a.G, rhead = row - rtok * a.G;
-    uint32_t s_phase = 0, of_phase = 0, ml_phase = 0;
+    float2 *ml = reinterpret_cast<float2 *>(sm + C::oMl) + i * kRows + row;
+    const int rtok = row / a.G;
+    uint32_t s_phase = 0, d_phase = 1;
     uint32_t tile = 0;                                // key tiles seen so far (meta ring)
     bool ok = true;
-    for (; ok && w.valid; walk_next(a, w)) {
-      const Entry &e = w.e;
-      const bool single = e.lw == 0;
-      const int T = w.t1 - w.t0;
-      const int tok = rtok + (single ? 0 : i * a.TT); // token of the entry
-      const bool row_ok = rtok < a.TT && tok < e.ntok;
+    // The piece is read from its ring entry as it is needed and given back at the end.
+    for (;; ri.step()) {
+      if (!ok || !(ok = warp_wait(&item_full[ri.slot], ri.phase, abort))) break;
+      const Item &it = items[ri.slot];
+      if (it.flags & kEnd) break;
+      const bool single = it.flags & kSingle, keys = it.flags & kHasKeys;
+      const int tok = rtok + (single ? 0 : i * a.TT); // token of the piece's entry
+      const bool row_ok = rtok < a.TT && tok < it.ntok;
       const bool warp_ok = __any_sync(kFull, row_ok);
-      const int p = e.p0 + (row_ok ? tok : e.ntok - 1);
+      const int p = it.p0 + (row_ok ? tok : it.ntok - 1);
       float m_ref = -INFINITY, l = 0.f;               // base-2 units
-      if (e.keys) {
-        for (int k = single ? i : 0; k < T; k += single ? 2 : 1) {
+      if (keys) {
+        const int first = single ? i : 0, step = single ? 2 : 1;
+#pragma unroll 1
+        for (int k = first; k < it.T; k += step) {   // (T and the tile's place: one broadcast load)
           ok = warp_wait(&s_full[i], s_phase, abort);
           if (!ok) break;
           s_phase ^= 1u;
           tc_fence_after();
           if (warp_ok) {
-            const int base = tile_base(e, w.t0 + k);
-            const TileMeta *md = &meta[(tile + k) % kMetaRing];
-            uint32_t s[kKeys];
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_col + c, s + c);
-            const uint4 seen = *reinterpret_cast<const uint4 *>(md->seen);
+            const int base = tile_base(it, k);
+            const uint4 seen = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
             const int hi = p - base;                  // keys c <= hi are not after the row
             const int lo = a.n_stream < 0 ? 0 : p - a.n_stream + 1 - base;   // c >= lo: in its window
             const int sk = a.n_sink - base;           // c < sk: a first token
-            const bool trim = hi < kKeys - 1 || (lo > 0 && sk < kKeys) ||
-                              (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
-            tmem_wait_ld();
-            if (__any_sync(kFull, trim)) {
-              const uint32_t sw[4] = {seen.x, seen.y, seen.z, seen.w};
+            const bool trim = __any_sync(kFull, hi < kKeys - 1 || (lo > 0 && sk < kKeys) ||
+                                                    (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu);
+            // scores of part `part`, minus infinity where the row does not see the key
+            uint32_t s[C::kPart];
+            auto scores = [&](int part) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                // bits below x of the q-th 32 keys
-                auto below = [&](int x) -> uint32_t {
-                  const int y = x - 32 * q;
-                  return y <= 0 ? 0u : (y >= 32 ? 0xffffffffu : (1u << y) - 1u);
-                };
-                const uint32_t v = sw[q] & below(hi + 1) & (~below(lo) | below(sk));
+              for (int c = 0; c < C::kPart; c += 32) tmem_ld32(s_col + C::kPart * part + c, s + c);
+              tmem_wait_ld();
+              if (trim) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  s[32 * q + c] = (v >> c) & 1u ? s[32 * q + c] : __float_as_uint(-INFINITY);
+                for (int c = 0; c < C::kPart; c += 32) {
+                  const int q = C::kPart / 32 * part + c / 32;   // which 32 keys of the tile
+                  auto below = [&](int x) -> uint32_t {          // bits below x of them
+                    const int y = x - 32 * q;
+                    return y <= 0 ? 0u : (y >= 32 ? 0xffffffffu : (1u << y) - 1u);
+                  };
+                  const uint32_t sw = q == 0 ? seen.x : q == 1 ? seen.y : q == 2 ? seen.z : seen.w;
+                  const uint32_t v = sw & below(hi + 1) & (~below(lo) | below(sk));
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) s[c + x] = (v >> x) & 1u ? s[c + x] : __float_as_uint(-INFINITY);
+                }
               }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            };
+            constexpr int kParts = kKeys / C::kPart;
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int part = 0; part < kParts; ++part) {
+              scores(part);
+              float mx[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 2)
-              mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            const float mt = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.sl2;
+              for (int c = 0; c < C::kPart; c += 2)
+                mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              mt = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+            }
+            mt *= a.sl2;
             const bool move = mt > m_ref + kSlack;
             if (__any_sync(kFull, move)) {
               float f = 1.f;
@@ -587,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 l *= f;
                 m_ref = mt;
               }
-              if (k > (single ? i : 0)) {             // O holds earlier tiles of this piece
+              if (k > first) {                        // O holds earlier tiles of this piece
                 const float2 f2 = make_float2(f, f);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
@@ -607,18 +677,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
             const float2 nm2 = make_float2(nm, nm), sl22 = make_float2(a.sl2, a.sl2);
             float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int part = kParts - 1; part >= 0; --part) {   // the last part is still here
+              if (kParts > 1 && part < kParts - 1) scores(part);
 #pragma unroll
-            for (int c0 = 0; c0 < kKeys; c0 += 32) {
-              uint32_t pk[16];
+              for (int c0 = 0; c0 < C::kPart; c0 += 32) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                const float2 y = ffma2(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), sl22, nm2);
-                const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                if ((c >> 1) & 1) acc1 = fadd2(acc1, x);
-                else acc0 = fadd2(acc0, x);
-                pk[c >> 1] = pack_bf16x2(x.x, x.y);
+                for (int c = 0; c < 32; c += 2) {
+                  const float2 y = ffma2(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), sl22, nm2);
+                  const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                  if ((c >> 1) & 1) acc1 = fadd2(acc1, x);
+                  else acc0 = fadd2(acc0, x);
+                  pk[c >> 1] = pack_bf16x2(x.x, x.y);
+                }
+                tmem_st16(s_col + C::kPart * part + c0, pk);
               }
-              tmem_st16(s_col + c0 / 2, pk);
             }
             const float2 as = fadd2(acc0, acc1);
             l += as.x + as.y;
@@ -629,129 +703,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           if (lane == 0) mbar_arrive(&p_full[i]);
         }
         if (!ok) break;
-        tile += T;
+        tile += it.T;
       }
-      // ---------------- end of the piece: O_i complete after the stream's last P V
-      const int mine = !e.keys ? 0 : single ? (T - i + 1) / 2 : T;   // tiles of this stream
-      if (mine > 0) {
-        ok = warp_wait(&o_final[i], of_phase, abort);
-        if (!ok) break;
-        of_phase ^= 1u;
-        tc_fence_after();
-      }
-      if (single && i == 1) {
-        // hand (m, l) to stream 0, which merges the halves, and wait until it has read O_1
-        ml[row] = make_float2(m_ref, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ml_ready);
-        ok = warp_wait(o1_free, ml_phase, abort);
-        ml_phase ^= 1u;
-        continue;
-      }
-      float f0 = 1.f, f1 = 0.f, m = m_ref;
-      bool two = false;
-      if (single) {
-        ok = warp_wait(ml_ready, ml_phase, abort);
-        if (!ok) break;
-        ml_phase ^= 1u;
-        tc_fence_after();
-        const float2 o = ml[row];
-        two = e.keys && T > 1;                        // stream 1 had a tile: O_1 is defined
-        m = fmaxf(m_ref, o.x);
-        f0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
-        f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - m);
-        l = l * f0 + o.y * f1;
-      }
-      const bool whole = w.t0 == 0 && w.t1 == e.n;
-      const bool some = mine > 0;
-      const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // NaN stays NaN
-      const float g0 = f0 * inv, g1 = f1 * inv;
-      const int head = w.g * a.G + rhead;
-      const size_t orow = static_cast<size_t>(e.tok0 + tok) * a.H_q + head;
-      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      const int prow = (single ? 0 : i * kRows) + row;
-      if (warp_ok) {
-        long long quad_row[4];                        // output rows of the lane's quad (-1: none)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          quad_row[x] = __shfl_sync(kFull, row_ok ? static_cast<long long>(orow) : -1ll, (lane & ~3) + x);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (some) tmem_ld32(o_col + c, o);
-          if (two) {
-            uint32_t o1[32];
-            tmem_ld32(o_col + D + c, o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              o[x] = __float_as_uint((f0 == 0.f ? 0.f : __uint_as_float(o[x]) * g0) +
-                                     (f1 == 0.f ? 0.f : __uint_as_float(o1[x]) * g1));
-          } else {
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              o[x] = !some || l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[x]) * g0);
-          }
-          if (whole) {
-            // 4 x 4 transpose of 16-byte pieces over four lanes: store j then covers 64
-            // contiguous bytes of row j of the quad instead of 16 bytes of every row
-            uint4 y[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              y[x].x = pack_bf16x2(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1]));
-              y[x].y = pack_bf16x2(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3]));
-              y[x].z = pack_bf16x2(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5]));
-              y[x].w = pack_bf16x2(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7]));
-            }
-            swap4(y[0], y[1], lane & 1, 1);
-            swap4(y[2], y[3], lane & 1, 1);
-            swap4(y[0], y[2], lane & 2, 2);
-            swap4(y[1], y[3], lane & 2, 2);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (quad_row[x] >= 0)
-                *reinterpret_cast<uint4 *>(a.out + quad_row[x] * D + c + 8 * (lane & 3)) = y[x];
-          } else if (row_ok) {
-            float4 *dst = reinterpret_cast<float4 *>(a.part) +
-                          (static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + prow;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              dst[static_cast<size_t>(x) * a.part_rows] =
-                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-          }
-        }
-        if (row_ok) {
-          if (whole) {
-            if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-          } else {
-            reinterpret_cast<float2 *>(a.part_ml)[static_cast<size_t>(slot) * a.part_rows + prow] = make_float2(m, l);
-          }
-        }
-      }
-      tc_fence_before();
+      // (m, l) to the epilogue, once it has drained the piece before
+      if (!(ok = warp_wait(&drained[i], d_phase, abort))) break;
+      d_phase ^= 1u;
+      *ml = make_float2(m_ref, l);
       __syncwarp();
-      if (single && lane == 0) mbar_arrive(o1_free);
-      // the share in which a cut item begins describes it for the merge
-      if (i == 0 && row == 0 && w.t0 == 0 && !whole) {
-        PagedPiece d;
-        d.item_u0 = w.item_u0;
-        d.q = plan->q;
-        d.r = plan->r;
-        d.P = plan->P;
-        d.n = e.n;
-        d.lw = e.lw;
-        d.tok0 = e.tok0;
-        d.ntok = e.ntok;
-        d.g = w.g;
-        d.valid = 1;
-        a.piece[blockIdx.x] = d;
+      if (lane == 0) {
+        mbar_arrive(&ml_full[i]);
+        mbar_arrive(&item_empty[ri.slot]);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == C::kSoft) {
     // ---------------------------------------------------------------- producer
-    reg_dec<C::kRegMisc>();
+    reg_set<C::kRegMisc, C::kRegLaunch>();
     constexpr int NS = FP8 ? C::kRawSlots : C::kSlots;
     constexpr uint32_t kBytes = FP8 ? C::kRaw : C::kTile;
     uint64_t *rf = FP8 ? raw_full : full, *re = FP8 ? raw_empty : empty;
@@ -762,29 +728,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     uint32_t q_phase = 0;
     uint32_t tile = 0;
     bool ok = true, q_open = false;
-    // one K or V tile into the next ring slot
-    auto load = [&](const CUtensorMap *map, int k, int g) -> bool {
-      if (!warp_wait(&re[rp.slot], rp.phase ^ 1u, abort)) return false;
-      const TileMeta *md = &meta[(tile + k) % kMetaRing];
-      unsigned char *dst = ring + rp.slot * kBytes;
-      const int base = tile_base(w.e, w.t0 + k);
-      if (lane == 0) mbar_arrive_expect_tx(&rf[rp.slot], kBytes);
-      __syncwarp();
-      const int boxes = FP8 ? parts : parts * C::kHalves;
-      if (lane < boxes) {
-        const int part = FP8 ? lane : lane / C::kHalves, hh = FP8 ? 0 : lane - part * C::kHalves;
-        tma_load_4d(dst + (FP8 ? part * R * D : hh * C::kHalf + part * R * 128), map, &rf[rp.slot], 64 * hh, g,
-                    base & (a.page_size - 1) & ~(R - 1), md->page[part]);
-      }
-      __syncwarp();
-      rp.step();
-      return true;
-    };
-    for (; ok && w.valid; walk_next(a, w)) {
-      const Entry &e = w.e;
-      if (!e.keys) continue;
-      const bool single = e.lw == 0;
-      const int T = w.t1 - w.t0;
+    Item it;
+    // one K or V tile into the next ring slot; lane x of `boxes` brings box x, of the part of
+    // the tile that lies in `page`
+    const int boxes = FP8 ? parts : parts * C::kHalves;
+    const int part = FP8 ? lane : lane / C::kHalves, hh = FP8 ? 0 : lane - part * C::kHalves;
+    while (ok && next_item(it)) {
+      if (!(it.flags & kHasKeys)) continue;
+      const bool single = it.flags & kSingle;
+      const int T = it.T;
       // the item's query tiles, once the MMAs of the one before have read theirs
       if (q_open) {
         ok = warp_wait(q_empty, q_phase, abort);
@@ -797,55 +749,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nt * C::kHalves * a.TT * a.G * 128));
         for (int t = 0; t < nt; ++t)
           for (int hh = 0; hh < C::kHalves; ++hh)
-            tma_load_4d(sm + C::oQ + t * C::kTile + hh * C::kHalf, &a.tq, q_full, 64 * hh, w.g * a.G,
-                        e.tok0 + t * a.TT, 0);
+            tma_load_4d(sm + C::oQ + t * C::kTile + hh * C::kHalf, &a.tq, q_full, 64 * hh, it.g * a.G,
+                        it.tok0 + t * a.TT, 0);
       }
       __syncwarp();
-      const int32_t *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
-      // this lane's page of tile k
+      const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+      // the page of this lane's part of tile k (n_pages: none, reads as zero)
       auto page_of = [&](int k) -> int {
         int page = a.n_pages;
-        const int pos = tile_base(e, w.t0 + k) + lane * R;
-        if (k < T && lane < parts && pos <= e.p_hi) {   // p_hi < capacity: inside the table
+        const int pos = tile_base(it, k) + part * R;
+        if (k < T && part < parts && pos <= it.p_hi) {   // p_hi < capacity: inside the table
           page = table[pos >> a.lg_page];
           DSA_CHECK(page >= 0 && page < a.n_pages);
           if (page < 0 || page >= a.n_pages) page = a.n_pages;
         }
         return page;
       };
+      int pg0 = a.n_pages, pg1 = a.n_pages;           // pages of the last two K tiles
       int page_next = page_of(0);
-      // pages and visible keys of tile k; the next tile's pages are requested meanwhile
-      auto describe = [&](int k) {
-        TileMeta *md = &meta[(tile + k) % kMetaRing];
-        const int base = tile_base(e, w.t0 + k);
-        const int page = page_next;
-        page_next = page_of(k + 1);
-        if (lane < 8) md->page[lane] = page;
-        const int lo = a.n_stream < 0 ? 0 : a.n_stream == 0 ? 0x7fffffff : max(e.p0, 0) - a.n_stream + 1;
+      const int ahead = single ? 2 : 1;               // K tiles in flight before the first V
+      const int lo = a.n_stream < 0 ? 0 : a.n_stream == 0 ? 0x7fffffff : max(it.p0, 0) - a.n_stream + 1;
+#pragma unroll 1
+      for (int x = 0; ok && x < 2 * (T + ahead); ++x) {
+        const bool value = !(x & 1);                  // V of tile x / 2 - ahead, then K of tile x / 2
+        const int k = value ? (x >> 1) - ahead : x >> 1;
+        if (k < 0 || k >= T) continue;
+        const int base = tile_base(it, k);
+        // (behind the last K the pages shift by none: the shift is made when K is loaded)
+        int page = single && (x >> 1) < T + 1 ? pg1 : pg0;
+        if (!value) {
+          page = page_next;
+          page_next = page_of(k + 1);                 // requested meanwhile
+          pg1 = pg0;
+          pg0 = page;
+          // the tile's visible keys
+          uint32_t *seen = meta[(tile + k) % kMetaRing].seen;
 #pragma unroll
-        for (int q = 0; q < kKeys / 32; ++q) {
-          const int c = 32 * q + lane, j = base + c;
-          const bool good = __shfl_sync(kFull, page, c / R) != a.n_pages;
-          const uint32_t v = __ballot_sync(kFull, good && j <= e.p_hi && (j >= lo || j < a.n_sink));
-          if (lane == 0) md->seen[q] = v;
+          for (int q = 0; q < kKeys / 32; ++q) {
+            const int c = 32 * q + lane, j = base + c;
+            const bool good = __shfl_sync(kFull, page, (c / R) * (FP8 ? 1 : C::kHalves)) != a.n_pages;
+            const uint32_t v = __ballot_sync(kFull, good && j <= it.p_hi && (j >= lo || j < a.n_sink));
+            if (lane == 0) seen[q] = v;
+          }
         }
+        if (!(ok = warp_wait(&re[rp.slot], rp.phase ^ 1u, abort))) break;
+        unsigned char *dst = ring + rp.slot * kBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&rf[rp.slot], kBytes);
         __syncwarp();
-      };
-      const int ahead = single ? 2 : 1;
-      for (int k = 0; ok && k < min(ahead, T); ++k) {
-        describe(k);
-        ok = load(&a.tk, k, w.g);
-      }
-      for (int k = 0; ok && k < T; ++k) {
-        ok = load(&a.tv, k, w.g);
-        if (ok && k + ahead < T) {
-          describe(k + ahead);
-          ok = load(&a.tk, k + ahead, w.g);
-        }
+        if (lane < boxes)
+          tma_load_4d(dst + (FP8 ? part * R * D : hh * C::kHalf + part * R * 128), value ? &a.tv : &a.tk, &rf[rp.slot],
+                      64 * hh, it.g, base & (a.page_size - 1) & ~(R - 1), page);
+        __syncwarp();
+        rp.step();
       }
       tile += T;
     }
-    if (!ok || *abort) {
+    if (!ok || abort.abort[0]) {
       // let this CTA's copies land before it exits
       if (lane == 0) {
         if (q_open) drain_wait(q_full, q_phase, 200000000ull);
@@ -856,143 +815,235 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == C::kSoft + 1) {
     // ---------------------------------------------------------------- MMA issuer
-    reg_dec<C::kRegMisc>();
+    reg_set<C::kRegMisc, C::kRegLaunch>();
     constexpr uint32_t id_qk = idesc_bf16_f32(kRows, kKeys, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(kRows, D, false, true);
-    const uint32_t sQ = smem_u32(sm + C::oQ);
-    const uint32_t sR = smem_u32(sm + C::oRing);
+    // descriptors of the first tiles; the address field counts 16 bytes
+    const uint64_t dq = sdesc_sw128(smem_u32(sm + C::oQ), 16, 1024);
+    const uint64_t dk = sdesc_sw128(smem_u32(sm + C::oRing), 16, 1024);
+    const uint64_t dv = sdesc_sw128(smem_u32(sm + C::oRing), C::kHalf, 1024);
     Ring<C::kSlots> rp;
-    uint32_t q_phase = 0, p_phase[2] = {0, 0};
-    uint32_t tile = 0;
-    bool ok = true;
-    // S_i = Q K^T with the K tile of ring slot `slot`
-    auto qk = [&](int i, int qt, int slot) {
-      if (lane == 0) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-          tc_mma(tmem + C::cS + i * kKeys, sdesc_sw128(sQ + qt * C::kTile + off, 16, 1024),
-                 sdesc_sw128(sR + slot * C::kTile + off, 16, 1024), id_qk, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&s_full[i]);
-      }
-    };
-    auto pv = [&](int i, int slot, bool first) {
-      if (lane == 0) {
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc_mma_ts(tmem + C::cO + i * D, tmem + C::cS + i * kKeys + kk * 8,
-                    sdesc_sw128(sR + slot * C::kTile + kk * 2048, C::kHalf, 1024), id_pv,
-                    (!first || kk > 0) ? 1u : 0u);
-      }
-    };
-    // the next ring slot, once filled
-    auto next = [&](int &slot) -> bool {
-      if (!warp_wait(&full[rp.slot], rp.phase, abort)) return false;
-      tc_fence_after();
-      slot = rp.slot;
-      rp.step();
-      return true;
-    };
-    // a value tile, once filled and (bf16 caches) rid of rows that no row of the item sees
     Ring<FP8 ? 1 : C::kClean> rc;
-    auto next_v = [&](int &slot) -> bool {
-      if (!next(slot)) return false;
-      if constexpr (!FP8) {
-        if (!warp_wait(&clean[rc.slot], rc.phase, abort)) return false;
-        rc.step();
+    uint32_t q_phase = 0, p_phase[2] = {0, 0}, d_phase = 0;
+    bool ok = true;
+    Item it;
+    while (ok && next_item(it)) {
+      // O_i of the piece before has been read (every piece is waited for, so that no phase is
+      // missed); waited for right before the first P V into it
+      d_phase ^= 1u;
+      const bool single = it.flags & kSingle;
+      if (!(it.flags & kHasKeys)) {
+        ok = warp_wait(&drained[0], d_phase, abort) && warp_wait(&drained[1], d_phase, abort);
+        continue;
       }
-      return true;
-    };
-    auto wait_p = [&](int i) -> bool {
-      if (!warp_wait(&p_full[i], p_phase[i], abort)) return false;
-      p_phase[i] ^= 1u;
-      tc_fence_after();
-      return true;
-    };
-    auto release = [&](int slot) {
-      if (lane == 0) tc_commit(&empty[slot]);
-    };
-    // the query tiles may be overwritten once the item's last Q K^T has read them
-    auto q_done = [&]() {
-      if (lane == 0) tc_commit(q_empty);
-    };
-    for (; ok && w.valid; walk_next(a, w)) {
-      const Entry &e = w.e;
-      if (!e.keys) continue;
-      const bool single = e.lw == 0;
-      const int T = w.t1 - w.t0;
       if (!(ok = warp_wait(q_full, q_phase, abort))) break;
       q_phase ^= 1u;
       tc_fence_after();
-      int ks, vs;
-      if (single) {
-        for (int k = 0; ok && k < min(2, T); ++k)
-          if ((ok = next(ks))) {
-            qk(k, 0, ks);
-            release(ks);
-            if (k + 1 == T) q_done();
+      // X score tiles; tile x belongs to stream x & 1, and to key tile x / 2 (two query tiles) or
+      // x.  In turn: P V of tile y - 2, then Q K^T of tile y over its scores.
+      const int X = single ? it.T : 2 * it.T;
+      int ks = 0, vs = 0;
+#pragma unroll 1
+      for (int y = 0; y < X + 2; ++y) {
+        const int i = y & 1;
+        const bool fresh = single || i == 0, done = single || i == 1;   // first, last use of a key tile
+        if (y >= 2) {
+          const int x = y - 2;
+          if (fresh) {
+            // a V tile is ready once filled and (bf16 caches) rid of rows that no row sees
+            ok = FP8 ? warp_wait(&full[rp.slot], rp.phase, abort) : warp_wait(&clean[rc.slot], rc.phase, abort);
+            if (!ok) break;
+            rc.step();
+            vs = rp.slot;
+            rp.step();
           }
-        for (int k = 0; ok && k < T; ++k) {
-          const int i = k & 1;
-          if (!(ok = next_v(vs))) break;
-          if (!(ok = wait_p(i))) break;
-          pv(i, vs, k < 2);
-          release(vs);
-          if (k + 2 >= T) {
-            if (lane == 0) tc_commit(&o_final[i]);
-          } else {
-            if (!(ok = next(ks))) break;
-            qk(i, 0, ks);
-            release(ks);
-            if (k + 3 == T) q_done();
+          if (!(ok = warp_wait(&p_full[i], p_phase[i], abort))) break;
+          p_phase[i] ^= 1u;
+          // the first P V of the piece; a lone tile's piece waits for both streams here
+          if (x < 2 && !(ok = warp_wait(&drained[i], d_phase, abort))) break;
+          if (X == 1 && !(ok = warp_wait(&drained[1], d_phase, abort))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t bd = dv + static_cast<uint32_t>(vs) * (C::kTile >> 4);
+            const uint32_t p = tmem + C::cS + i * kKeys, d = tmem + C::cO + i * D;
+#pragma unroll 1
+            for (uint32_t kk = 0; kk < kKeys / 16; kk += 2) {
+              tc_mma_ts(d, p + kk * 16, bd + kk * 128, id_pv, (x >= 2 || kk > 0) ? 1u : 0u);
+              tc_mma_ts(d, p + kk * 16 + 8, bd + kk * 128 + 128, id_pv, 1u);
+            }
+            if (done) tc_commit(&empty[vs]);
+            if (y >= X) tc_commit(&o_final[i]);
           }
+          __syncwarp();
         }
-      } else {
-        if ((ok = next(ks))) {
-          qk(0, 0, ks);
-          qk(1, 1, ks);
-          release(ks);
-          if (T == 1) q_done();
-        }
-        for (int k = 0; ok && k < T; ++k) {
-          const bool more = k + 1 < T;
-          if (!(ok = next_v(vs))) break;
-          if (!(ok = wait_p(0))) break;
-          pv(0, vs, k == 0);
-          if (more) {
-            if (!(ok = next(ks))) break;
-            qk(0, 0, ks);
-          } else if (lane == 0) {
-            tc_commit(&o_final[0]);
+        if (y < X) {
+          if (fresh) {
+            if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
+            ks = rp.slot;
+            rp.step();
           }
-          if (!(ok = wait_p(1))) break;
-          pv(1, vs, k == 0);
-          release(vs);
-          if (more) {
-            qk(1, 1, ks);
-            release(ks);
-            if (k + 2 == T) q_done();
-          } else if (lane == 0) {
-            tc_commit(&o_final[1]);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t ad = dq + (single ? 0u : static_cast<uint32_t>(i)) * (C::kTile >> 4);
+            const uint64_t bd = dk + static_cast<uint32_t>(ks) * (C::kTile >> 4);
+#pragma unroll 1
+            for (uint32_t h = 0; h < C::kHalves; ++h)
+#pragma unroll
+              for (uint32_t kk = 0; kk < 4; ++kk)
+                tc_mma(tmem + C::cS + i * kKeys, ad + h * (C::kHalf >> 4) + kk * 2, bd + h * (C::kHalf >> 4) + kk * 2,
+                       id_qk, (h | kk) ? 1u : 0u);
+            tc_commit(&s_full[i]);
+            if (done) tc_commit(&empty[ks]);
+            if (y == X - 1) tc_commit(q_empty);
           }
+          __syncwarp();
         }
       }
-      tile += T;
     }
     if (lane == 0) tc_commit(fin);
     __syncwarp();
-  } else if (FP8 && warp >= 12) {
+  } else if (warp >= C::kEpi && warp < C::kEpi + 4) {
+    // ---------------------------------------------------------------- epilogue
+    // O out of TMEM, normalised into out (or, of a cut item, as it is into the workspace)
+    reg_set<C::kRegEpi, C::kRegLaunch>();
+    const int row = (warp & 3) * 32 + lane;           // row of the query tile
+    const uint32_t o_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::cO;
+    const float2 *ml = reinterpret_cast<const float2 *>(sm + C::oMl) + row;
+    const int rtok = row / a.G, rhead = row - rtok * a.G;
+    uint32_t ml_phase = 0, of_phase[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    while (ok && next_item(it)) {
+      const bool single = it.flags & kSingle, keys = it.flags & kHasKeys, whole = it.flags & kWhole;
+      const int slot = 2 * blockIdx.x + (it.flags & kStart ? 1 : 0);
+      // (m, l) of stream i, and O_i complete; false: gave up
+      auto wait_o = [&](int i, bool any) -> bool {
+        if (!warp_wait(&ml_full[i], ml_phase, abort)) return false;
+        if (any) {
+          if (!warp_wait(&o_final[i], of_phase[i], abort)) return false;
+          of_phase[i] ^= 1u;
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto release = [&](int i) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&drained[i]);
+      };
+#pragma unroll 1
+      for (int i = 0; i < (single ? 1 : 2); ++i) {
+        const int tok = rtok + i * a.TT;              // token of the piece's entry
+        const bool row_ok = rtok < a.TT && tok < it.ntok;
+        if (!(ok = wait_o(i, keys))) break;
+        float m = ml[i * kRows].x, l = ml[i * kRows].y, f0 = 1.f, f1 = 0.f;
+        bool two = false;
+        if (single) {                                 // the other half of the key tiles
+          two = keys && it.T > 1;
+          if (!(ok = wait_o(1, two))) break;
+          const float2 o = ml[kRows];
+          const float mm = fmaxf(m, o.x);
+          f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
+          f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mm);
+          l = l * f0 + o.y * f1;
+          m = mm;
+        }
+        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // NaN stays NaN
+        const float g0 = f0 * inv, g1 = f1 * inv;
+        const bool none = !keys || f0 == 0.f || l == 0.f;
+        const size_t orow = static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + rhead;
+        const int prow = i * kRows + row;
+        if (__any_sync(kFull, row_ok)) {
+          const uint32_t o_col = o_base + i * D;
+          // 16 columns of O (the streams' halves merged, normalised if the result is final)
+          auto columns = [&](int c, float *x) {
+            uint32_t o[16];
+            if (keys) tmem_ld16(o_col + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) x[q] = none ? 0.f : __uint_as_float(o[q]) * g0;
+            if (two) {
+              tmem_ld16(o_col + D + c, o);
+              tmem_wait_ld();
+              if (f1 != 0.f) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) x[q] = fmaf(__uint_as_float(o[q]), g1, x[q]);
+              }
+            }
+          };
+          if (whole) {
+            const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              // 4 x 4 transpose of 16-byte pieces over four lanes: store j then covers 64
+              // contiguous bytes of row j of the quad instead of 16 bytes of every row
+              uint4 y[4];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float x[16];
+                columns(c + 16 * q, x);
+                y[2 * q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                      pack_bf16x2(x[6], x[7]));
+                y[2 * q + 1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]),
+                                          pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+              }
+              swap4(y[0], y[1], lane & 1, 1);
+              swap4(y[2], y[3], lane & 1, 1);
+              swap4(y[0], y[2], lane & 2, 2);
+              swap4(y[1], y[3], lane & 2, 2);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const long long r = __shfl_sync(kFull, mine_row, (lane & ~3) + x);   // -1: no such row
+                if (r >= 0) *reinterpret_cast<uint4 *>(a.out + r * D + c + 8 * (lane & 3)) = y[x];
+              }
+            }
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(a.part) + static_cast<size_t>(slot) * (D / 4) * a.part_rows + prow;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float x[16];
+              columns(c, x);
+              if (row_ok) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  dst[static_cast<size_t>(q) * a.part_rows] =
+                      make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+              }
+              dst += static_cast<size_t>(4) * a.part_rows;
+            }
+          }
+          if (row_ok) {
+            if (!whole)
+              reinterpret_cast<float2 *>(a.part_ml)[static_cast<size_t>(slot) * a.part_rows + prow] = make_float2(m, l);
+            else if (a.lse)
+              a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          }
+        }
+        release(i);
+        if (single) release(1);
+      }
+      ml_phase ^= 1u;
+    }
+  } else if (FP8 && warp >= C::kConv) {
     // ---------------------------------------------------------------- converters
     if constexpr (FP8) {
-      reg_dec<C::kRegConv>();
-      const int r = (warp - 12) * 32 + lane;          // the thread's row of every tile
+      reg_set<C::kRegConv, C::kRegLaunch>();
+      Item it;
+      const int r = (warp & 3) * 32 + lane;           // the thread's row of every tile
+      const bool values = warp >= C::kConv + 4;       // V tiles, or K tiles
       Ring<C::kRawSlots> rr;
       Ring<C::kSlots> rp;
       uint32_t tile = 0;
       bool ok = true;
+      auto skip = [&]() -> bool {
+        if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
+        if (lane == 0) mbar_arrive(&raw_empty[rr.slot]);
+        rr.step();
+        rp.step();
+        return true;
+      };
       // tile k (already described) with this row's scale byte sb
       auto convert = [&](int k, uint32_t sb_raw) -> bool {
         if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
@@ -1046,111 +1097,169 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         rp.step();
         return true;
       };
-      for (; ok && w.valid; walk_next(a, w)) {
-        if (!w.e.keys) continue;
-        const int ahead = w.e.lw == 0 ? 2 : 1;
-        const int T = w.t1 - w.t0;
-        // the row's page two tiles ahead and its scale bytes one tile ahead of the conversion
-        // of K, so that neither load's latency is waited for; a V byte waits (in `vq`, oldest
-        // lowest) for its tile's turn
-        const int32_t *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+      while (ok && next_item(it)) {
+        if (!(it.flags & kHasKeys)) continue;
+        const int ahead = it.flags & kSingle ? 2 : 1;
+        const int T = it.T;
+        // the row's page two tiles ahead and its scale byte one tile ahead of the conversion,
+        // so that neither load's latency is waited for
+        const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+        const uint8_t *scales = values ? a.v_scale : a.k_scale;
         auto page_of = [&](int k) -> int {
-          const int pos = tile_base(w.e, w.t0 + k) + r;
-          if (k >= T || pos > w.e.p_hi) return -1;
+          const int pos = tile_base(it, k) + r;
+          if (k >= T || pos > it.p_hi) return -1;
           const int page = table[pos >> a.lg_page];
           return page >= 0 && page < a.n_pages ? page : -1;
         };
-        auto scales_of = [&](int k, int page, uint32_t &ks, uint32_t &vs) {
-          ks = vs = 127;
-          if (page < 0) return;
-          const size_t at = (static_cast<size_t>(page) * a.page_size +
-                             ((tile_base(w.e, w.t0 + k) + r) & (a.page_size - 1))) * a.H_kv + w.g;
-          ks = a.k_scale[at];
-          vs = a.v_scale[at];
+        auto scale_of = [&](int k, int page) -> uint32_t {
+          if (page < 0) return 127;
+          return scales[(static_cast<size_t>(page) * a.page_size + ((tile_base(it, k) + r) & (a.page_size - 1))) * a.H_kv +
+                        it.g];
         };
-        int front = 0, nv = 0;
-        uint32_t ks, vs, vq = 0;
         int page = page_of(0);
         int page_next = page_of(1);
-        scales_of(0, page, ks, vs);
-        auto convert_k = [&]() -> bool {
-          uint32_t ks1, vs1;
-          scales_of(front + 1, page_next, ks1, vs1);
-          page_next = page_of(front + 2);
-          if (!convert(front, ks)) return false;
-          vq |= vs << (8 * nv++);
-          ks = ks1;
-          vs = vs1;
-          ++front;
+        uint32_t sb = scale_of(0, page);
+        int mine = 0;                                 // tiles of this warp's kind so far
+        // one operand tile in ring order: this warp's kind is converted, the other kind's slots
+        // are only seen and given back (see the cleaner)
+        auto step = [&](bool value) -> bool {
+          if (value != values) return skip();
+          const uint32_t sb1 = scale_of(mine + 1, page_next);
+          page_next = page_of(mine + 2);
+          if (!convert(mine, sb)) return false;
+          sb = sb1;
+          ++mine;
           return true;
         };
-        for (int k = 0; ok && k < min(ahead, T); ++k) ok = convert_k();
-        for (int k = 0; ok && k < T; ++k) {
-          ok = convert(k, vq & 0xffu);
-          vq >>= 8;
-          --nv;
-          if (ok && k + ahead < T) ok = convert_k();
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * (T + ahead); ++x) {   // the producer's order
+          const int k = x & 1 ? x >> 1 : (x >> 1) - ahead;
+          if (k >= 0 && k < T) ok = step(!(x & 1));
         }
         tile += T;
       }
     }
+  } else if (warp == C::kSoft + 2) {
+    // ---------------------------------------------------------------- scheduler
+    reg_set<C::kRegMisc, C::kRegLaunch>();
+    if (lane == 0) {
+      a.piece[blockIdx.x].valid = 0;   // until this share begins a cut item
+      Walk w;
+      w.u0 = plan->u0;
+      w.u1 = plan->u1;
+      w.item_u0 = plan->item_u0;
+      w.b = plan->b;
+      w.m = plan->m;
+      w.g = plan->g;
+      w.s = plan->s;
+      w.valid = false;
+      PagedPiece d;
+      d.q = plan->q;
+      d.r = plan->r;
+      d.P = plan->P;
+      if (w.u0 < w.u1 && w.b < a.B) {
+        w.e = make_entry(a, w.s, w.m);
+        walk_settle(a, w);
+      }
+      while (true) {
+        if (!one_wait(&item_empty[ri.slot], ri.phase ^ 1u, abort)) break;
+        Item it;
+        if (w.valid) {
+          const bool start = w.t0 == 0, whole = start && w.t1 == w.e.n;
+          it.tok0 = w.e.tok0;
+          it.ntok = w.e.ntok;
+          it.p0 = w.e.p0;
+          it.p_hi = w.e.p_hi;
+          it.ns = w.e.ns;
+          it.w0 = w.e.w0;
+          it.t0 = w.t0;
+          it.T = w.t1 - w.t0;
+          it.b = w.b;
+          it.g = w.g;
+          it.flags = (w.e.lw == 0 ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
+                     (start ? kStart : 0);
+          if (start && !whole) {       // a cut item, described for the merge where it begins
+            d.item_u0 = w.item_u0;
+            d.n = w.e.n;
+            d.lw = w.e.lw;
+            d.tok0 = w.e.tok0;
+            d.ntok = w.e.ntok;
+            d.g = w.g;
+            d.valid = 1;
+            a.piece[blockIdx.x] = d;
+          }
+        } else {
+          it.flags = kEnd;
+        }
+        items[ri.slot] = it;
+        mbar_arrive(&item_full[ri.slot]);
+        ri.step();
+        if (!w.valid) break;
+        walk_next(a, w);
+      }
+    }
+    __syncwarp();
   } else {
-    // ---------------------------------------------------------------- warps 10, 11: cleaners
+    // ---------------------------------------------------------------- cleaner
     // value rows that no row of the item sees are zeroed in their slot (the converters do it
-    // for FP8 caches), 64 rows of every tile each
-    reg_dec<C::kRegMisc>();
+    // for FP8 caches)
+    reg_set<C::kRegMisc, C::kRegLaunch>();
     if constexpr (!FP8) {
       Ring<C::kSlots> rp;
       Ring<C::kClean> rc;
       uint32_t tile = 0;
       bool ok = true;
-      const int half = warp - 10;
-      for (; ok && w.valid; walk_next(a, w)) {
-        if (!w.e.keys) continue;
-        const int ahead = w.e.lw == 0 ? 2 : 1;
-        const int T = w.t1 - w.t0;
+      Item it;
+      while (ok && next_item(it)) {
+        if (!(it.flags & kHasKeys)) continue;
+        const int ahead = it.flags & kSingle ? 2 : 1;
         // Every slot is waited for and released, K tiles too: only who holds a slot back sees
         // each of its phases.
-        auto next = [&]() -> bool { return warp_wait(&full[rp.slot], rp.phase, abort); };
-        auto done = [&]() {
+#pragma unroll 1
+        for (int x = 0; x < 2 * (it.T + ahead); ++x) {   // the producer's order
+          const bool value = !(x & 1);
+          const int k = value ? (x >> 1) - ahead : x >> 1;
+          if (k < 0 || k >= it.T) continue;
+          if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
+          if (value) {
+            const uint4 s4 = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
+            if ((s4.x & s4.y & s4.z & s4.w) != 0xffffffffu) {
+              const int at = lane >> 3;               // eight lanes per 128-byte row
+#pragma unroll 1
+              for (int r0 = 0; r0 < kKeys; r0 += 32) {
+                const uint32_t sw = r0 == 0 ? s4.x : r0 == 32 ? s4.y : r0 == 64 ? s4.z : s4.w;
+                if (sw == 0xffffffffu) continue;
+#pragma unroll 1
+                for (int r = 0; r < 32; r += 4)
+                  if (!((sw >> (r + at)) & 1u))
+#pragma unroll
+                    for (int hh = 0; hh < C::kHalves; ++hh)
+                      *reinterpret_cast<uint4 *>(sm + C::oRing + rp.slot * C::kTile + hh * C::kHalf +
+                                                 (r0 + r + at) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&clean[rc.slot]);
+            rc.step();
+          }
           if (lane == 0) mbar_arrive(&empty[rp.slot]);
           rp.step();
-        };
-        for (int k = 0; ok && k < min(ahead, T); ++k)
-          if ((ok = next())) done();
-        for (int k = 0; ok && k < T; ++k) {
-          if (!(ok = next())) break;
-          const uint2 seen = *reinterpret_cast<const uint2 *>(&meta[(tile + k) % kMetaRing].seen[2 * half]);
-          if ((seen.x & seen.y) != 0xffffffffu) {
-#pragma unroll 1
-            for (int r = lane >> 3; r < kKeys / 2; r += 4)   // eight lanes per 128-byte row
-              if (!(((r < 32 ? seen.x : seen.y) >> (r & 31)) & 1u))
-#pragma unroll
-                for (int hh = 0; hh < C::kHalves; ++hh)
-                  *reinterpret_cast<uint4 *>(sm + C::oRing + rp.slot * C::kTile + hh * C::kHalf +
-                                             (64 * half + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(&clean[rc.slot]);
-          rc.step();
-          done();
-          if (k + ahead < T && (ok = next())) done();
         }
-        tile += T;
+        tile += it.T;
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::kSoft + 1) {
     tc_fence_after();
     if (lane == 0) drain_wait(fin, 0, 1000000000ull);   // every MMA retired before TMEM is freed
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (tid == 0 && *abort) atomicExch(&g_paged_error, 1);
+  if (tid == 0 && abort.abort[0]) atomicExch(&g_paged_error, 1);
 }
 
 // ------------------------------------------------------------------ merge
