@@ -327,6 +327,35 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
     if (global_ns() - t0 > limit_ns) return;
 }
 
+// The tensor-core instructions of the MMA warp, executed by the whole warp with the leader's
+// predicate inside: the warp stays converged, so descriptors and addresses live in uniform
+// registers.  (In a branch that only lane 0 takes, every operand is moved there first, about
+// 125 clocks an instruction against the 64 that the tensor core needs for it.)
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// arrive on `bar` when every tensor-core instruction issued so far has completed
+__device__ __forceinline__ void commit_if(uint32_t pred, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(pred)
+      : "memory");
+}
+
 // a ring position: slot and phase parity
 template <int N>
 struct Ring {
@@ -826,6 +855,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     const uint64_t dv = sdesc_sw128(smem_u32(sm + C::oRing), C::kHalf, 1024);
     Ring<C::kSlots> rp;
     Ring<FP8 ? 1 : C::kClean> rc;
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const uint32_t tmem_u = __shfl_sync(kFull, tmem, 0);
     uint32_t q_phase = 0, p_phase[2] = {0, 0}, d_phase = 0;
     bool ok = true;
     Item it;
@@ -856,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             ok = FP8 ? warp_wait(&full[rp.slot], rp.phase, abort) : warp_wait(&clean[rc.slot], rc.phase, abort);
             if (!ok) break;
             rc.step();
-            vs = rp.slot;
+            vs = __shfl_sync(kFull, rp.slot, 0);
             rp.step();
           }
           if (!(ok = warp_wait(&p_full[i], p_phase[i], abort))) break;
@@ -865,40 +896,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           if (x < 2 && !(ok = warp_wait(&drained[i], d_phase, abort))) break;
           if (X == 1 && !(ok = warp_wait(&drained[1], d_phase, abort))) break;
           tc_fence_after();
-          if (lane == 0) {
+          {
             const uint64_t bd = dv + static_cast<uint32_t>(vs) * (C::kTile >> 4);
-            const uint32_t p = tmem + C::cS + i * kKeys, d = tmem + C::cO + i * D;
-#pragma unroll 1
-            for (uint32_t kk = 0; kk < kKeys / 16; kk += 2) {
-              tc_mma_ts(d, p + kk * 16, bd + kk * 128, id_pv, (x >= 2 || kk > 0) ? 1u : 0u);
-              tc_mma_ts(d, p + kk * 16 + 8, bd + kk * 128 + 128, id_pv, 1u);
-            }
-            if (done) tc_commit(&empty[vs]);
-            if (y >= X) tc_commit(&o_final[i]);
+            const uint32_t pc = tmem_u + C::cS + i * kKeys, d = tmem_u + C::cO + i * D;
+#pragma unroll
+            for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(leader, d, pc + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, (x >= 2 || kk > 0) ? 1u : 0u);
+            commit_if(leader & (done ? 1u : 0u), &empty[vs]);
+            commit_if(leader & (y >= X ? 1u : 0u), &o_final[i]);
           }
-          __syncwarp();
         }
         if (y < X) {
           if (fresh) {
             if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
-            ks = rp.slot;
+            ks = __shfl_sync(kFull, rp.slot, 0);
             rp.step();
           }
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t ad = dq + (single ? 0u : static_cast<uint32_t>(i)) * (C::kTile >> 4);
-            const uint64_t bd = dk + static_cast<uint32_t>(ks) * (C::kTile >> 4);
-#pragma unroll 1
-            for (uint32_t h = 0; h < C::kHalves; ++h)
+          const uint64_t ad = dq + (single ? 0u : static_cast<uint32_t>(i)) * (C::kTile >> 4);
+          const uint64_t bd = dk + static_cast<uint32_t>(ks) * (C::kTile >> 4);
 #pragma unroll
-              for (uint32_t kk = 0; kk < 4; ++kk)
-                tc_mma(tmem + C::cS + i * kKeys, ad + h * (C::kHalf >> 4) + kk * 2, bd + h * (C::kHalf >> 4) + kk * 2,
-                       id_qk, (h | kk) ? 1u : 0u);
-            tc_commit(&s_full[i]);
-            if (done) tc_commit(&empty[ks]);
-            if (y == X - 1) tc_commit(q_empty);
+          for (uint32_t kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (C::kHalf >> 4) + (kk & 3) * 2;
+            mma_ss(leader, tmem_u + C::cS + i * kKeys, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
           }
-          __syncwarp();
+          commit_if(leader, &s_full[i]);
+          commit_if(leader & (done ? 1u : 0u), &empty[ks]);
+          commit_if(leader & (y == X - 1 ? 1u : 0u), q_empty);
         }
       }
     }
