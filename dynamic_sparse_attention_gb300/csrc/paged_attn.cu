@@ -22,13 +22,17 @@
 //     K/V tile);
 //   one-tile items (a few tokens): both streams hold the same query tile and take the key
 //     tiles alternately; their halves are merged in TMEM at the end of the item.
-// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (TMA), 9 MMA
-// issuer (one thread), 10 scheduler, 11 cleaner (bf16 caches), 12-15 epilogue (results out of
-// TMEM while the softmax warps are at the next item); FP8 caches add the converter warps 16-23,
-// which widen the E4M3 tiles that TMA brings into a staging ring to bf16 operand tiles (exact:
-// code * 2^e is a bf16), four warps the K tiles and four the V tiles.  The scheduler walks the share and hands out its items
-// through a small ring, so that no other role holds that state: beside 224 KB of shared memory
-// next to no L1 is left, and a spilled register costs a round trip to L2.
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (schedule and
+// TMA), 9 and 10 MMA issuers of stream 0 and 1 (one issuer for both spent 1,800 clocks a turn
+// on waits, 16 MMAs and commits against 1,024 in the tensor core), 11 cleaner (bf16 caches),
+// 12-15 epilogue (results out of TMEM while the softmax warps are at the next item); FP8 caches
+// add the converter warps 16-23, which widen the E4M3 tiles that TMA brings into a staging ring
+// to bf16 operand tiles (exact: code * 2^e is a bf16), four warps the K tiles and four the V
+// tiles.  The producer walks the share and hands out its items through a small ring, so that no
+// other role holds that state: beside 224 KB of shared memory next to no L1 is left, and a
+// spilled register costs a round trip to L2.  Every role is one compact loop: instruction
+// fetches bound this kernel before its pipes do (with each role's code unrolled and inlined per
+// case, 150 KB in all, the FP8 cases took two to three times as long).
 //   S_i = Q_i K^T (M = N = 128, K = D), P over S_i (each 32 columns' P in the first 16),
 //   O_i += P V.
 // Each stream issues P V (tile t) and right behind it Q K^T (its next tile): S_i full then
@@ -128,9 +132,9 @@ struct Cfg {
   static constexpr uint32_t oItem = oMl + 2 * kRows * 8;
   static constexpr uint32_t oBar = oItem + kItems * sizeof(Item);
   // q_full, q_empty, slot full/empty, raw full/empty, then for both streams s_full, p_full,
-  // o_final, ml_full, drained; fin, clean, item full/empty
-  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 10 + 1 + kClean + 2 * kItems;
-  static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item
+  // o_final, ml_full, drained, turn; fin, clean, item full/empty
+  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems;
+  static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item (not the producer)
   static constexpr uint32_t oMisc = oBar + kBars * 8;
   static constexpr uint32_t kBytes = oMisc + 16;
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
@@ -216,7 +220,7 @@ __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) 
   return e;
 }
 
-// What a CTA's planning leaves for its warps: the share [u0, u1), the item it begins in (first
+// What a CTA's planning leaves for its producer: the share [u0, u1), the item it begins in (first
 // unit, sequence, pair, KV head) and how the launch's units are dealt out.
 struct Plan {
   long long item_u0, u0, u1, q;
@@ -296,18 +300,6 @@ struct WaitCtl {
     return t;
   }
 };
-
-// one thread waits
-__device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = WaitCtl::clock_lo();
-  while (!mbar_try_wait(bar, parity))
-    if (w.over(t0)) {
-      w.abort[0] = 1;
-      return false;
-    }
-  return true;
-}
 
 // the whole warp waits; the outcome is warp-uniform
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
@@ -432,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   uint64_t *full = bars + 2, *empty = full + C::kSlots;
   uint64_t *raw_full = empty + C::kSlots, *raw_empty = raw_full + C::kRawSlots;
   uint64_t *s_full = raw_empty + C::kRawSlots, *p_full = s_full + 2, *o_final = p_full + 2;
-  uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *fin = drained + 2;
+  uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *turn = drained + 2, *fin = turn + 2;
   uint64_t *clean = fin + 1, *item_full = clean + C::kClean, *item_empty = item_full + kItems;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
   const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4)};
@@ -446,10 +438,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], FP8 ? 4 : 1);
-      mbar_init(&empty[i], FP8 ? 1 : 2);   // the MMAs that read it; bf16: and the cleaner
+      mbar_init(&empty[i], FP8 ? 2 : 3);   // both MMA issuers; bf16: and the cleaner
     }
     for (int i = 0; i < C::kRawSlots; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -461,8 +453,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       mbar_init(&o_final[i], 1);
       mbar_init(&ml_full[i], 4);
       mbar_init(&drained[i], 4);
+      mbar_init(&turn[i], 1);
     }
-    mbar_init(fin, 1);
+    mbar_init(fin, 2);
     for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
@@ -758,11 +751,64 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     uint32_t tile = 0;
     bool ok = true, q_open = false;
     Item it;
-    // one K or V tile into the next ring slot; lane x of `boxes` brings box x, of the part of
-    // the tile that lies in `page`
+    Walk w;
+    w.u0 = plan->u0;
+    w.u1 = plan->u1;
+    w.item_u0 = plan->item_u0;
+    w.b = plan->b;
+    w.m = plan->m;
+    w.g = plan->g;
+    w.s = plan->s;
+    w.valid = false;
+    const long long plan_q = plan->q;
+    const int plan_r = plan->r, plan_P = plan->P;
+    if (lane == 0) a.piece[blockIdx.x].valid = 0;     // until this share begins a cut item
+    if (w.u0 < w.u1 && w.b < a.B) {
+      w.e = make_entry(a, w.s, w.m);
+      walk_settle(a, w);
+    }
+    // the next piece of the share to every role (and into `it`); false at the end
+    auto hand_out = [&]() -> bool {
+      if (!(ok = warp_wait(&item_empty[ri.slot], ri.phase ^ 1u, abort))) return false;
+      const bool start = w.t0 == 0, whole = start && w.t1 == w.e.n;
+      it.tok0 = w.e.tok0;
+      it.ntok = w.e.ntok;
+      it.p0 = w.e.p0;
+      it.p_hi = w.e.p_hi;
+      it.ns = w.e.ns;
+      it.w0 = w.e.w0;
+      it.t0 = w.t0;
+      it.T = w.t1 - w.t0;
+      it.b = w.b;
+      it.g = w.g;
+      it.flags = !w.valid ? kEnd : (w.e.lw == 0 ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
+                                       (start ? kStart : 0);
+      if (lane == 0) {
+        items[ri.slot] = it;
+        mbar_arrive(&item_full[ri.slot]);
+        if (w.valid && start && !whole) {             // a cut item, described for the merge where it begins
+          PagedPiece d;
+          d.item_u0 = w.item_u0;
+          d.q = plan_q;
+          d.r = plan_r;
+          d.P = plan_P;
+          d.n = w.e.n;
+          d.lw = w.e.lw;
+          d.tok0 = w.e.tok0;
+          d.ntok = w.e.ntok;
+          d.g = w.g;
+          d.valid = 1;
+          a.piece[blockIdx.x] = d;
+        }
+      }
+      __syncwarp();
+      ri.step();
+      return w.valid;
+    };
+    // lane x of `boxes` brings box x of a tile, of the part that lies in one page
     const int boxes = FP8 ? parts : parts * C::kHalves;
     const int part = FP8 ? lane : lane / C::kHalves, hh = FP8 ? 0 : lane - part * C::kHalves;
-    while (ok && next_item(it)) {
+    for (; ok && hand_out(); walk_next(a, w)) {
       if (!(it.flags & kHasKeys)) continue;
       const bool single = it.flags & kSingle;
       const int T = it.T;
@@ -844,89 +890,112 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         }
       }
     }
-  } else if (warp == C::kSoft + 1) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (warp <= C::kSoft + 2) {
+    // ---------------------------------------------------------------- MMA issuers
     reg_set<C::kRegMisc, C::kRegLaunch>();
     constexpr uint32_t id_qk = idesc_bf16_f32(kRows, kKeys, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(kRows, D, false, true);
+    const int i = __shfl_sync(kFull, warp - C::kSoft - 1, 0);   // stream
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    const uint32_t s_tm = tm + C::cS + i * kKeys, o_tm = tm + C::cO + i * D;
     // descriptors of the first tiles; the address field counts 16 bytes
     const uint64_t dq = sdesc_sw128(smem_u32(sm + C::oQ), 16, 1024);
     const uint64_t dk = sdesc_sw128(smem_u32(sm + C::oRing), 16, 1024);
     const uint64_t dv = sdesc_sw128(smem_u32(sm + C::oRing), C::kHalf, 1024);
+    const uint32_t leader = lane == 0 ? 1u : 0u;
     Ring<C::kSlots> rp;
     Ring<FP8 ? 1 : C::kClean> rc;
-    const uint32_t leader = lane == 0 ? 1u : 0u;
-    const uint32_t tmem_u = __shfl_sync(kFull, tmem, 0);
-    uint32_t q_phase = 0, p_phase[2] = {0, 0}, d_phase = 0;
+    uint32_t q_phase = 0, p_phase = 0, d_phase = 0, t_phase = i ^ 1;
     bool ok = true;
+    // The streams take turns: P V and the Q K^T behind it of one, then of the other.  Left to
+    // themselves they fall into step, and then share the tensor core during one half of the
+    // time and the exponential unit during the other.
+    auto take_turn = [&]() -> bool {
+      if (!warp_wait(&turn[i], t_phase, abort)) return false;
+      t_phase ^= 1u;
+      return true;
+    };
+    auto pass_turn = [&]() {
+      if (lane == 0) mbar_arrive(&turn[i ^ 1]);
+      __syncwarp();
+    };
     Item it;
     while (ok && next_item(it)) {
       // O_i of the piece before has been read (every piece is waited for, so that no phase is
-      // missed); waited for right before the first P V into it
+      // missed)
       d_phase ^= 1u;
       const bool single = it.flags & kSingle;
+      const int T = it.T, ahead = single ? 2 : 1;
       if (!(it.flags & kHasKeys)) {
-        ok = warp_wait(&drained[0], d_phase, abort) && warp_wait(&drained[1], d_phase, abort);
+        ok = warp_wait(&drained[i], d_phase, abort);
         continue;
       }
       if (!(ok = warp_wait(q_full, q_phase, abort))) break;
       q_phase ^= 1u;
-      tc_fence_after();
-      // X score tiles; tile x belongs to stream x & 1, and to key tile x / 2 (two query tiles) or
-      // x.  In turn: P V of tile y - 2, then Q K^T of tile y over its scores.
-      const int X = single ? it.T : 2 * it.T;
-      int ks = 0, vs = 0;
+      const int last = single ? T - 1 - ((T - 1 - i) & 1) : T - 1;   // the stream's last key tile
+      if (last < 0) {                                 // it has none: one key tile, stream 1
+        ok = warp_wait(&drained[i], d_phase, abort);
+        if (lane == 0) mbar_arrive(q_empty);
+      }
+      const uint64_t ad = dq + (single ? 0u : static_cast<uint32_t>(i)) * (C::kTile >> 4);
+      // the slots in ring order (the producer's): P V of tile k, then Q K^T of the stream's next
 #pragma unroll 1
-      for (int y = 0; y < X + 2; ++y) {
-        const int i = y & 1;
-        const bool fresh = single || i == 0, done = single || i == 1;   // first, last use of a key tile
-        if (y >= 2) {
-          const int x = y - 2;
-          if (fresh) {
-            // a V tile is ready once filled and (bf16 caches) rid of rows that no row sees
-            ok = FP8 ? warp_wait(&full[rp.slot], rp.phase, abort) : warp_wait(&clean[rc.slot], rc.phase, abort);
-            if (!ok) break;
-            rc.step();
-            vs = __shfl_sync(kFull, rp.slot, 0);
-            rp.step();
-          }
-          if (!(ok = warp_wait(&p_full[i], p_phase[i], abort))) break;
-          p_phase[i] ^= 1u;
-          // the first P V of the piece; a lone tile's piece waits for both streams here
-          if (x < 2 && !(ok = warp_wait(&drained[i], d_phase, abort))) break;
-          if (X == 1 && !(ok = warp_wait(&drained[1], d_phase, abort))) break;
-          tc_fence_after();
-          {
-            const uint64_t bd = dv + static_cast<uint32_t>(vs) * (C::kTile >> 4);
-            const uint32_t pc = tmem_u + C::cS + i * kKeys, d = tmem_u + C::cO + i * D;
-#pragma unroll
-            for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(leader, d, pc + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, (x >= 2 || kk > 0) ? 1u : 0u);
-            commit_if(leader & (done ? 1u : 0u), &empty[vs]);
-            commit_if(leader & (y >= X ? 1u : 0u), &o_final[i]);
-          }
+      for (int x = 0; ok && x < 2 * (T + ahead); ++x) {
+        const bool value = !(x & 1);
+        const int k = value ? (x >> 1) - ahead : x >> 1;
+        if (k < 0 || k >= T) continue;
+        const int slot = __shfl_sync(kFull, rp.slot, 0);
+        // a V tile is ready once filled and (bf16 caches) rid of rows that no row sees
+        if (!FP8 && value) {
+          ok = warp_wait(&clean[rc.slot], rc.phase, abort);
+          rc.step();
+        } else {
+          ok = warp_wait(&full[slot], rp.phase, abort);
         }
-        if (y < X) {
-          if (fresh) {
-            if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
-            ks = __shfl_sync(kFull, rp.slot, 0);
-            rp.step();
-          }
+        if (!ok) break;
+        rp.step();
+        if (single && ((k ^ i) & 1)) {                // the other stream's: only seen and given back
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          __syncwarp();
+          continue;
+        }
+        if (value) {
+          const bool first = single ? k == i : k == 0;
+          if (!(ok = warp_wait(&p_full[i], p_phase, abort))) break;
+          p_phase ^= 1u;
+          if (first && !(ok = warp_wait(&drained[i], d_phase, abort))) break;
+          if (!(ok = take_turn())) break;
           tc_fence_after();
-          const uint64_t ad = dq + (single ? 0u : static_cast<uint32_t>(i)) * (C::kTile >> 4);
-          const uint64_t bd = dk + static_cast<uint32_t>(ks) * (C::kTile >> 4);
+          const uint64_t bd = dv + static_cast<uint32_t>(slot) * (C::kTile >> 4);
+          const uint32_t acc = first ? 0u : 1u;
+#pragma unroll
+          for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(leader, o_tm, s_tm + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, kk > 0 ? 1u : acc);
+          commit_if(leader, &empty[slot]);
+          if (k == last) {
+            commit_if(leader, &o_final[i]);
+            pass_turn();
+          }
+        } else {
+          tc_fence_after();
+          const uint64_t bd = dk + static_cast<uint32_t>(slot) * (C::kTile >> 4);
 #pragma unroll
           for (uint32_t kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (C::kHalf >> 4) + (kk & 3) * 2;
-            mma_ss(leader, tmem_u + C::cS + i * kKeys, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+            mma_ss(leader, s_tm, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
           }
           commit_if(leader, &s_full[i]);
-          commit_if(leader & (done ? 1u : 0u), &empty[ks]);
-          commit_if(leader & (y == X - 1 ? 1u : 0u), q_empty);
+          commit_if(leader, &empty[slot]);
+          if (k == last) commit_if(leader, q_empty);
+          if (k >= ahead) pass_turn();
         }
       }
+      if (ok && single && i == 1 && (T & 1)) {        // stream 0 had one tile more
+        ok = take_turn();
+        pass_turn();
+      }
     }
-    if (lane == 0) tc_commit(fin);
+    commit_if(leader, fin);
     __syncwarp();
   } else if (warp >= C::kEpi && warp < C::kEpi + 4) {
     // ---------------------------------------------------------------- epilogue
@@ -1163,66 +1232,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         tile += T;
       }
     }
-  } else if (warp == C::kSoft + 2) {
-    // ---------------------------------------------------------------- scheduler
-    reg_set<C::kRegMisc, C::kRegLaunch>();
-    if (lane == 0) {
-      a.piece[blockIdx.x].valid = 0;   // until this share begins a cut item
-      Walk w;
-      w.u0 = plan->u0;
-      w.u1 = plan->u1;
-      w.item_u0 = plan->item_u0;
-      w.b = plan->b;
-      w.m = plan->m;
-      w.g = plan->g;
-      w.s = plan->s;
-      w.valid = false;
-      PagedPiece d;
-      d.q = plan->q;
-      d.r = plan->r;
-      d.P = plan->P;
-      if (w.u0 < w.u1 && w.b < a.B) {
-        w.e = make_entry(a, w.s, w.m);
-        walk_settle(a, w);
-      }
-      while (true) {
-        if (!one_wait(&item_empty[ri.slot], ri.phase ^ 1u, abort)) break;
-        Item it;
-        if (w.valid) {
-          const bool start = w.t0 == 0, whole = start && w.t1 == w.e.n;
-          it.tok0 = w.e.tok0;
-          it.ntok = w.e.ntok;
-          it.p0 = w.e.p0;
-          it.p_hi = w.e.p_hi;
-          it.ns = w.e.ns;
-          it.w0 = w.e.w0;
-          it.t0 = w.t0;
-          it.T = w.t1 - w.t0;
-          it.b = w.b;
-          it.g = w.g;
-          it.flags = (w.e.lw == 0 ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
-                     (start ? kStart : 0);
-          if (start && !whole) {       // a cut item, described for the merge where it begins
-            d.item_u0 = w.item_u0;
-            d.n = w.e.n;
-            d.lw = w.e.lw;
-            d.tok0 = w.e.tok0;
-            d.ntok = w.e.ntok;
-            d.g = w.g;
-            d.valid = 1;
-            a.piece[blockIdx.x] = d;
-          }
-        } else {
-          it.flags = kEnd;
-        }
-        items[ri.slot] = it;
-        mbar_arrive(&item_full[ri.slot]);
-        ri.step();
-        if (!w.valid) break;
-        walk_next(a, w);
-      }
-    }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- cleaner
     // value rows that no row of the item sees are zeroed in their slot (the converters do it
