@@ -1200,12 +1200,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         const uint8_t *scales = values ? a.v_scale : a.k_scale;
         auto page_of = [&](int k) -> int {
           const int pos = tile_base(it, k) + r;
-          if (k >= T || pos > it.p_hi) return -1;
-          const int page = table[pos >> a.lg_page];
-          return page >= 0 && page < a.n_pages ? page : -1;
+          return k < T && pos <= it.p_hi ? table[pos >> a.lg_page] : -1;   // checked when used
         };
         auto scale_of = [&](int k, int page) -> uint32_t {
-          if (page < 0) return 127;
+          if (page < 0 || page >= a.n_pages) return 127;
           return scales[(static_cast<size_t>(page) * a.page_size + ((tile_base(it, k) + r) & (a.page_size - 1))) * a.H_kv +
                         it.g];
         };
