@@ -1303,64 +1303,81 @@ struct MergeArgs {
   int part_rows, H_q, G, TT;
 };
 
-constexpr int kMergeRows = 8;   // rows per CTA; a warp holds 4 groups of 4 dims of them
+constexpr int kMergeWarps = 8;
 
-// CTA (c, y) merges rows 8 y .. of the item that share c begins and a boundary cuts: the
-// pieces of shares c, c + 1, ... until the item ends, weighted by exp2(m - max m).  Lanes run
-// over the rows first, so partials are read in whole lines.
+// CTA (c, y) merges rows of the item that share c begins and a boundary cuts, a row per warp at
+// a time: the pieces of shares c, c + 1, ... until the item ends, weighted by exp2(m - max m).
+// Each lane fetches one piece's (m, l), so that all weights of a row cost one round of loads;
+// then D / 4 lanes add up the pieces' O (with D = 64 the half-warps take alternate pieces).
 template <int D>
-__global__ void __launch_bounds__(D * 2) paged_merge_kernel(const MergeArgs a) {
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const MergeArgs a) {
+  const int lane = threadIdx.x & 31;
   grid_dep_wait();
   const PagedPiece pc = a.piece[blockIdx.x];
-  const int x = blockIdx.y * kMergeRows + (threadIdx.x & 7);
-  if (!pc.valid || static_cast<int>(blockIdx.y) * kMergeRows >= pc.ntok * a.G) return;
-  const bool in = x < pc.ntok * a.G;
-  const int t = (in ? x : 0) / a.G, j = (in ? x : 0) - t * a.G;
-  const int qt = t >= a.TT ? 1 : 0;
-  const int prow = qt * kRows + (t - qt * a.TT) * a.G + j;
-  const int c4 = threadIdx.x >> 3;
+  if (!pc.valid) return;
   const long long end = pc.item_u0 + (static_cast<long long>(pc.n) << pc.lw);
-  // the shares of the item: blockIdx.x .. last
-  const int c0 = blockIdx.x;
-  int last = c0;
-  while (last + 1 < pc.P && share_begin(pc.q, pc.r, last + 1) < end) ++last;
-  auto slot_of = [&](int c) -> int {   // < 0: an empty piece
-    int t0, t1;
-    piece_of(share_begin(pc.q, pc.r, c), share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
-    return t1 > t0 ? 2 * c + (t0 == 0 ? 1 : 0) : -1;
-  };
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.part);
-  float M = -INFINITY;
+  constexpr int kStep = 128 / D;                      // pieces added per step
+  const int c4 = lane % (D / 4), odd = lane / (D / 4);
+  for (int x = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); x < pc.ntok * a.G; x += gridDim.y * kMergeWarps) {
+    const int t = x / a.G, j = x - t * a.G;
+    const int qt = t >= a.TT ? 1 : 0;
+    const int prow = qt * kRows + (t - qt * a.TT) * a.G + j;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c0 = blockIdx.x; c0 < pc.P; c0 += 32) {   // 32 shares at a time
+      const int c = c0 + lane;
+      int slot = -1;                                  // this lane's share has no piece
+      if (c < pc.P && share_begin(pc.q, pc.r, c) < end) {
+        int t0, t1;
+        piece_of(share_begin(pc.q, pc.r, c), share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
+        if (t1 > t0) slot = 2 * c + (t0 == 0 ? 1 : 0);
+      }
+      const uint32_t have = __ballot_sync(kFull, slot >= 0);
+      if (!have) break;
+      const float2 v = slot >= 0 ? ml[static_cast<size_t>(slot) * a.part_rows + prow] : make_float2(-INFINITY, 0.f);
+      const float m = fmaxf(M, warp_max(v.x));
+      const float old = M == -INFINITY ? 0.f : fast_exp2(M - m);
+      const float w = v.x == -INFINITY ? 0.f : fast_exp2(v.x - m);   // 0 for a piece without keys
+      L = L * old + warp_sum(v.y * w);
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
+      M = m;
+      const int n = 32 - __clz(have);                 // shares of an item lie side by side
 #pragma unroll 4
-  for (int c = c0; c <= last; ++c) {
-    const int s = slot_of(c);
-    if (s >= 0) M = fmaxf(M, ml[static_cast<size_t>(s) * a.part_rows + prow].x);
+      for (int p = 0; p < n; p += kStep) {
+        const int src = (p + odd) & 31;
+        const float f = __shfl_sync(kFull, w, src);
+        const int s = __shfl_sync(kFull, slot, src);
+        if (p + odd < n && f != 0.f) {
+          const float4 o = po[(static_cast<size_t>(s) * (D / 4) + c4) * a.part_rows + prow];
+          acc.x = fmaf(o.x, f, acc.x);
+          acc.y = fmaf(o.y, f, acc.y);
+          acc.z = fmaf(o.z, f, acc.z);
+          acc.w = fmaf(o.w, f, acc.w);
+        }
+      }
+    }
+    if (D == 64) {
+      acc.x += __shfl_xor_sync(kFull, acc.x, 16);
+      acc.y += __shfl_xor_sync(kFull, acc.y, 16);
+      acc.z += __shfl_xor_sync(kFull, acc.z, 16);
+      acc.w += __shfl_xor_sync(kFull, acc.w, 16);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t orow = static_cast<size_t>(pc.tok0 + t) * a.H_q + pc.g * a.G + j;
+    if (odd == 0) {
+      uint2 w;
+      w.x = L == 0.f ? 0u : pack_bf16x2(acc.x * inv, acc.y * inv);
+      w.y = L == 0.f ? 0u : pack_bf16x2(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2 *>(a.out + orow * D + 4 * c4) = w;
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= last; ++c) {
-    const int s = slot_of(c);
-    if (s < 0) continue;
-    const float2 v = ml[static_cast<size_t>(s) * a.part_rows + prow];
-    const float4 o = po[(static_cast<size_t>(s) * (D / 4) + c4) * a.part_rows + prow];
-    if (v.x == -INFINITY) continue;
-    const float f = fast_exp2(v.x - M);
-    L = fmaf(v.y, f, L);
-    acc.x = fmaf(o.x, f, acc.x);
-    acc.y = fmaf(o.y, f, acc.y);
-    acc.z = fmaf(o.z, f, acc.z);
-    acc.w = fmaf(o.w, f, acc.w);
-  }
-  if (!in) return;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t orow = static_cast<size_t>(pc.tok0 + t) * a.H_q + pc.g * a.G + j;
-  uint2 w;
-  w.x = L == 0.f ? 0u : pack_bf16x2(acc.x * inv, acc.y * inv);
-  w.y = L == 0.f ? 0u : pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2 *>(a.out + orow * D + 4 * c4) = w;
-  if (c4 == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host side
@@ -1470,7 +1487,8 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   ma.TT = TT;
   const int rows = std::min(2 * TT, pa.n_tok) * G;
   ProfScope ps("paged_attn_merge", s);
-  return launch_pdl(paged_merge_kernel<D>, dim3(P, (rows + kMergeRows - 1) / kMergeRows), dim3(D * 2), 0, s, ma);
+  const int y = std::min(16, (rows + kMergeWarps - 1) / kMergeWarps);
+  return launch_pdl(paged_merge_kernel<D>, dim3(P, y), dim3(kMergeWarps * 32), 0, s, ma);
 }
 
 }  // namespace
