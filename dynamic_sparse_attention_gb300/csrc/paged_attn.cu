@@ -1380,6 +1380,67 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Mer
   }
 }
 
+// The same for launches whose items have more rows than one tile: those have few pieces each
+// and many rows, so a warp takes 32 rows (a lane each) and 16 dims, reads whole lines of the
+// partials and writes whole sectors.  Reading them a row per warp took 22 us of a 240 us launch
+// (8K tokens, window 1024).
+template <int D>
+__global__ void __launch_bounds__(D * 2) paged_merge_rows_kernel(const MergeArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  const PagedPiece pc = a.piece[blockIdx.x];
+  if (!pc.valid) return;
+  const int prow = blockIdx.y * 32 + lane;
+  const int qt = prow / kRows, r = prow - qt * kRows;
+  const int t = qt * a.TT + r / a.G, j = r % a.G;
+  const bool in = r < a.TT * a.G && t < pc.ntok;
+  if (!__any_sync(kFull, in)) return;
+  const long long end = pc.item_u0 + (static_cast<long long>(pc.n) << pc.lw);
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + prow;
+  const float4 *po = reinterpret_cast<const float4 *>(a.part) + static_cast<size_t>(4 * warp) * a.part_rows + prow;
+  float M = -INFINITY, L = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int c = blockIdx.x; c < pc.P; ++c) {
+    const long long u0 = share_begin(pc.q, pc.r, c);
+    if (u0 >= end) break;
+    int t0, t1;
+    piece_of(u0, share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
+    if (t1 <= t0 || !in) continue;
+    const int slot = 2 * c + (t0 == 0 ? 1 : 0);
+    const float2 v = ml[static_cast<size_t>(slot) * a.part_rows];
+    float4 o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = po[(static_cast<size_t>(slot) * (D / 4) + q) * a.part_rows];
+    if (v.x == -INFINITY) continue;                   // no keys for this row in the piece
+    const float m = fmaxf(M, v.x);
+    const float old = M == -INFINITY ? 0.f : fast_exp2(M - m), w = fast_exp2(v.x - m);
+    M = m;
+    L = L * old + v.y * w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc[q].x = acc[q].x * old + o[q].x * w;
+      acc[q].y = acc[q].y * old + o[q].y * w;
+      acc[q].z = acc[q].z * old + o[q].z * w;
+      acc[q].w = acc[q].w * old + o[q].w * w;
+    }
+  }
+  if (!in) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t orow = static_cast<size_t>(pc.tok0 + t) * a.H_q + pc.g * a.G + j;
+  uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + 16 * warp);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float4 x = acc[2 * q], y = acc[2 * q + 1];
+    dst[q] = L == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                      : make_uint4(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv),
+                                   pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  }
+  if (warp == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 // ------------------------------------------------------------------ host side
 
 // [n_pages, page_size, H, D] codes, box = D x 1 head x rows x 1 page
@@ -1487,7 +1548,9 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   ma.TT = TT;
   const int rows = std::min(2 * TT, pa.n_tok) * G;
   ProfScope ps("paged_attn_merge", s);
-  const int y = std::min(16, (rows + kMergeWarps - 1) / kMergeWarps);
+  if (pa.part_rows > kRows)
+    return launch_pdl(paged_merge_rows_kernel<D>, dim3(P, pa.part_rows / 32), dim3(D * 2), 0, s, ma);
+  const int y = (rows + kMergeWarps - 1) / kMergeWarps;
   return launch_pdl(paged_merge_kernel<D>, dim3(P, y), dim3(kMergeWarps * 32), 0, s, ma);
 }
 
