@@ -42,32 +42,43 @@ __device__ __forceinline__ int row_exponent(uint32_t u) {
   return min(max(e, -116), 119);
 }
 
-// 8 bf16 of one 16-byte piece -> 8 codes of x * inv
-__device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
-  float f[8];
-  unpack16(u, f, uint16_t());
-  uint2 r;
-  r.x = f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-  r.y = f32x2_to_e4m3x2(f[4] * inv, f[5] * inv) | (f32x2_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-  return r;
+// two bf16 -> two E4M3 codes of x * inv (inv a power of two in both halves: exact)
+__device__ __forceinline__ uint32_t quantise2(uint32_t w, float2 inv) {
+  float2 x;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 c, a, b;\n"
+      " mov.b64 {%0, %1}, c;\n}\n"
+      : "=f"(x.x), "=f"(x.y)
+      : "f"(bf16_lo(w)), "f"(bf16_hi(w)), "f"(inv.x), "f"(inv.y));
+  return f32x2_to_e4m3x2(x.x, x.y);
 }
 
-// largest finite magnitude (bf16 bits) of one 16-byte piece; 0xffff if it holds a NaN
-__device__ __forceinline__ uint32_t finite_max8(const uint4 &u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 8 bf16 of one 16-byte piece -> 8 codes of x * inv
+__device__ __forceinline__ uint2 quantise8(const uint4 &u, float2 inv) {
+  return make_uint2(quantise2(u.x, inv) | (quantise2(u.y, inv) << 16), quantise2(u.z, inv) | (quantise2(u.w, inv) << 16));
+}
+
+// largest magnitude (bf16 bits) of either half over two 16-byte pieces
+__device__ __forceinline__ uint32_t max2x8(const uint4 &u, const uint4 &v) {
+  constexpr uint32_t k = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k)),
+                  __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k)));
+}
+
+// the same over finite elements alone, one result; 0xffff if the pieces hold a NaN
+__device__ __forceinline__ uint32_t finite_max(const uint4 &u, const uint4 &v) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
   uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-    m = max(m, lo < 0x7f80u ? lo : lo == 0x7f80u ? 0u : 0xffffu);
-    m = max(m, hi < 0x7f80u ? hi : hi == 0x7f80u ? 0u : 0xffffu);
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t x = (w[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+    m = max(m, x < 0x7f80u ? x : x == 0x7f80u ? 0u : 0xffffu);
   }
   return m;
 }
 
-// One CTA writes `tpc` tokens.  First every sequence whose rows meet the CTA's tokens puts
-// their slots (page * page_size + offset; -1: not written) into shared memory: one round of
-// loads for all sequences and one for the page table, whatever B is.  Then rows (token, K or
+// One CTA writes `tpc` tokens.  First every sequence whose rows meet the CTA's tokens marks
+// them, then a thread per token looks up its slot (page * page_size + offset; -1: not written):
+// one round of loads for all sequences and one for the tokens, whatever B is.  Then rows (token, K or
 // V, head) go out D / 16 lanes each, a lane holding the 16-byte pieces l and l + D / 16 of
 // the row, so that every load covers whole row segments and every store whole sectors.
 template <int D, bool FP8>
@@ -80,61 +91,76 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheWriteArgs
   grid_dep_wait();
   for (int i = tid; i < a.tpc; i += kThreads) s_slot[i] = -1;
   __syncthreads();
-  const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
   for (int b = tid; b < a.B; b += kThreads) {
     const int qs = a.q_start[b], qe = a.q_start[b + 1];
-    const int lo = max(qs, n0), hi = min(qe, n1);
-    if (lo >= hi) continue;
-    const int kv = a.kv_len[b];
-    DSA_CHECK(qs >= 0 && qe <= a.n_tok && kv >= qe - qs && kv <= cap);
-    const long long end = min(max(static_cast<long long>(kv), 0ll), cap);
-    for (int n = lo; n < hi; ++n) {
-      const long long pos = end - (static_cast<long long>(qe) - n);
-      if (pos < 0) continue;
-      const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + pos / a.page_size];
+    DSA_CHECK(qs >= 0 && qe <= a.n_tok);
+    for (int n = max(qs, n0); n < min(qe, n1); ++n) s_slot[n - n0] = b;
+  }
+  __syncthreads();
+  if (tid < n1 - n0 && s_slot[tid] >= 0) {
+    const int b = static_cast<int>(s_slot[tid]);
+    const int qe = a.q_start[b + 1], kv = a.kv_len[b], cap = a.max_pages << a.lg_page;
+    DSA_CHECK(kv >= 0 && kv <= cap);
+    const long long pos = min(max(kv, 0), cap) - (static_cast<long long>(qe) - (n0 + tid));
+    DSA_CHECK(pos >= 0);
+    long long slot = -1;
+    if (pos >= 0) {
+      const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + (pos >> a.lg_page)];
       DSA_CHECK(page >= 0 && page < a.n_pages);
       if (page >= 0 && page < a.n_pages)
-        s_slot[n - n0] = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+        slot = (static_cast<long long>(page) << a.lg_page) + (pos & (a.page_size - 1));
     }
+    s_slot[tid] = slot;
   }
   __syncthreads();
   const int l = tid % LPR;
   const int per_tok = 2 * a.H_kv;             // rows of a token: K heads, then V heads
   const int rows = (n1 - n0) * per_tok;
+  // this thread's row of the pass: row x of token n0 + i
+  int i = (tid / LPR) / per_tok, x = (tid / LPR) % per_tok;
+#pragma unroll 2
   for (int base = 0; base < rows; base += RPP) {   // uniform trip count
-    const int r0 = base + tid / LPR;
-    const bool in = r0 < rows;
-    const int r = in ? r0 : 0;
-    const int i = r / per_tok, x = r - i * per_tok;
     const bool is_k = x < a.H_kv;
     const int h = is_k ? x : x - a.H_kv;
-    const long long slot = in ? s_slot[i] : -1;
-    const uint16_t *src = (is_k ? a.k_new + (n0 + i) * a.k_stride : a.v_new + (n0 + i) * a.v_stride) +
-                          static_cast<size_t>(h) * D;
+    const long long slot = i < n1 - n0 ? s_slot[i] : -1;
     uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
     if (slot >= 0) {
-      u0 = __ldg(reinterpret_cast<const uint4 *>(src) + l);
-      u1 = __ldg(reinterpret_cast<const uint4 *>(src) + l + LPR);
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          (is_k ? a.k_new + (n0 + i) * a.k_stride : a.v_new + (n0 + i) * a.v_stride) + static_cast<size_t>(h) * D);
+      u0 = __ldg(src + l);
+      u1 = __ldg(src + l + LPR);
     }
+    const size_t row = static_cast<size_t>(slot) * a.H_kv + h;
     if constexpr (FP8) {
-      uint32_t m = max(finite_max8(u0), finite_max8(u1));
+      uint32_t m2 = max2x8(u0, u1);
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+      for (int o = LPR / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(kFull, m2, o));
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+      if (__any_sync(kFull, m >= 0x7f80u)) {         // infinities or NaN in some row: rare
+        m = finite_max(u0, u1);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+      }
       if (slot >= 0) {
         const bool nan = m == 0xffffu;
         const int e = nan ? 0 : row_exponent(m);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const size_t row = static_cast<size_t>(slot) * a.H_kv + h;
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float2 inv = make_float2(f, f);
         uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + row * D);
         dst[l] = quantise8(u0, inv);
         dst[l + LPR] = quantise8(u1, inv);
         if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = static_cast<uint8_t>(nan ? 255 : e + 127);
       }
     } else if (slot >= 0) {
-      const size_t row = static_cast<size_t>(slot) * a.H_kv + h;
       uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_k ? a.k_pages : a.v_pages) + row * D);
       dst[l] = u0;
       dst[l + LPR] = u1;
+    }
+    i += RPP / per_tok;
+    x += RPP % per_tok;
+    if (x >= per_tok) {
+      x -= per_tok;
+      ++i;
     }
   }
 }
@@ -230,6 +256,7 @@ cudaError_t launch_kv_write(const CacheWriteArgs &a0, cudaStream_t s) {
   int tpc = (rpp + 2 * a.H_kv - 1) / (2 * a.H_kv);
   while (tpc < 16 && a.n_tok / (2 * tpc) >= 4 * 152) tpc *= 2;
   a.tpc = tpc;
+  while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
   const dim3 grid((a.n_tok + tpc - 1) / tpc);
   const size_t smem = static_cast<size_t>(tpc) * sizeof(long long);
   ProfScope ps("kv_cache_write", s);

@@ -258,7 +258,7 @@ struct CacheWriteArgs {
   bool fp8;
   void *k_pages, *v_pages;
   uint8_t *k_scale, *v_scale;
-  int tpc;                         // tokens per CTA (set by the launcher)
+  int tpc, lg_page;                // tokens per CTA, log2 of page_size (set by the launcher)
 };
 cudaError_t launch_kv_write(const CacheWriteArgs &a, cudaStream_t s);
 struct CacheReadArgs {
