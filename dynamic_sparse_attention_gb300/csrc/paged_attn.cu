@@ -46,6 +46,9 @@
 //
 // Keys that no row of the item sees (behind the sequence, before the window, bad pages) have
 // their value rows zeroed, so whatever the pages hold there cannot reach the sums as 0 * NaN.
+// Where some rows of an item see a key and others do not, an infinity or NaN in its value row
+// does reach the others' sums that way; the epilogue finds such rows by their results and
+// computes the columns again from the keys that they see (repair_row).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -145,6 +148,9 @@ struct Cfg {
 
 struct Args {
   CUtensorMap tq, tk, tv;
+  const uint16_t *q;     // for repair_row, with the pages
+  long long q_stride;
+  const void *k_pages, *v_pages;
   const int32_t *q_start, *kv_len, *page_table;
   const uint8_t *k_scale, *v_scale;
   uint16_t *out;
@@ -301,15 +307,30 @@ struct WaitCtl {
   }
 };
 
-// the whole warp waits; the outcome is warp-uniform
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The whole warp waits; the outcome is warp-uniform.  Every lane asks, without a time hint: the
+// hardware then holds the warp until the phase completes (or a limit of its own passes).  One
+// lane polling, or hints, cost the other roles issue slots and woke late: 128K chunk 3.57 ->
+// 3.89 ms, and up to 5.5 with long hints.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
-  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
   const uint32_t t0 = WaitCtl::clock_lo();
-  while (!__all_sync(kFull, mbar_try_wait(bar, parity)))
+  do {
     if (__any_sync(kFull, w.over(t0))) {
       w.abort[0] = 1;
       return false;
     }
+  } while (!__all_sync(kFull, mbar_try_wait(bar, parity)));
   return true;
 }
 
@@ -396,6 +417,102 @@ __device__ __forceinline__ void swap4(uint4 &x, uint4 &y, int up, int mask) {
   t.w = __shfl_xor_sync(kFull, t.w, mask);
   if (up) x = t;
   else y = t;
+}
+
+// ------------------------------------------------------------------ rows with infinities or NaN
+
+// 8 consecutive elements of a cached row (pieces of 8, `scale` of the row for FP8) as floats
+template <bool FP8>
+__device__ __forceinline__ void cached8(const void *pages, size_t at, uint32_t scale, float *x) {
+  if constexpr (FP8) {
+    const float f = __uint_as_float(scale == 255u ? 0x7fffffffu : scale << 23);
+    const uint2 c = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + at);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(c.x), x[0], x[1]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(c.x >> 16), x[2], x[3]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(c.y), x[4], x[5]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(c.y >> 16), x[6], x[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= f;
+  } else {
+    unpack16(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(pages) + at), x, uint16_t());
+  }
+}
+
+// One row (a warp) whose O over a piece is not finite: the columns into which only value rows
+// that the row does not see can have carried an infinity or NaN are computed again, in fp32,
+// from the keys that it sees; x[0..8) of lane c < D / 8 are columns 8 c .. of the sum over the
+// piece of exp2(sl2 q . k - m) v, and the return value has bit i set if x[i] is to be used.
+// Such keys lie in tiles that not every row of the item sees alike: only those are searched,
+// and where the row itself sees an infinity or NaN its own result stands.
+template <int D, bool FP8>
+__device__ __forceinline__ uint32_t repair_row(const Args &a, const Item &it, int tok, int head, float m, float *x) {
+  const int lane = threadIdx.x & 31;
+  const int p = it.p0 + tok;
+  const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+  auto sees = [&](int j) { return j <= p && (a.n_stream < 0 || j > p - a.n_stream || j < a.n_sink); };
+  // row of key j in the cache (-1: none; only keys up to the item's last position have a page)
+  auto row_of = [&](int j) -> long long {
+    if (j > it.p_hi) return -1;
+    const int page = table[j >> a.lg_page];
+    if (page < 0 || page >= a.n_pages) return -1;
+    return ((static_cast<long long>(page) << a.lg_page) + (j & (a.page_size - 1))) * a.H_kv + it.g;
+  };
+  const int col = (lane % (D / 8)) * 8;
+  uint32_t own = 0, others = 0;   // columns with an infinity or NaN in seen, in unseen rows
+#pragma unroll 1
+  for (int k = 0; k < it.T; ++k) {
+    const int t = it.t0 + k, base = (t < it.ns ? t : it.w0 + t - it.ns) * kKeys;
+    if (base + kKeys - 1 <= it.p0 && (a.n_stream < 0 || base >= it.p_hi - a.n_stream + 1)) continue;   // seen by all
+#pragma unroll 1
+    for (int j = base; j < base + kKeys; ++j) {
+      const long long r = row_of(j);
+      if (r < 0) continue;
+      cached8<FP8>(a.v_pages, static_cast<size_t>(r) * D + col, FP8 ? a.v_scale[r] : 0u, x);
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bad |= (x[i] - x[i] == 0.f ? 0u : 1u) << i;
+      if (sees(j)) own |= bad;
+      else others |= bad;
+    }
+  }
+  const uint32_t redo = others & ~own;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0.f;
+  if (!__any_sync(kFull, redo)) return 0;
+  const uint16_t *q = a.q + (it.tok0 + tok) * a.q_stride + static_cast<size_t>(head) * D;
+#pragma unroll 1
+  for (int k = 0; k < it.T; ++k) {
+    const int t = it.t0 + k, base = (t < it.ns ? t : it.w0 + t - it.ns) * kKeys;
+#pragma unroll 1
+    for (int j0 = base; j0 < base + kKeys; j0 += 32) {
+      const int j = j0 + lane;   // a key per lane: its weight
+      const long long r = sees(j) ? row_of(j) : -1;
+      float w = 0.f;
+      if (r >= 0) {
+        float s = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 8) {
+          float kx[8], qx[8];
+          cached8<FP8>(a.k_pages, static_cast<size_t>(r) * D + c, FP8 ? a.k_scale[r] : 0u, kx);
+          unpack16(*reinterpret_cast<const uint4 *>(q + c), qx, uint16_t());
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = fmaf(qx[i], kx[i], s);
+        }
+        w = fast_exp2(s * a.sl2 - m);
+      }
+#pragma unroll 1
+      for (int y = 0; y < 32; ++y) {
+        const long long ry = __shfl_sync(kFull, r, y);
+        const float wy = __shfl_sync(kFull, w, y);
+        if (ry < 0) continue;
+        float vx[8];
+        cached8<FP8>(a.v_pages, static_cast<size_t>(ry) * D + col, FP8 ? a.v_scale[ry] : 0u, vx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(wy, vx[i], x[i]);
+      }
+    }
+  }
+  return redo;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -879,17 +996,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       }
       tile += T;
     }
-    if (!ok || abort.abort[0]) {
-      // let this CTA's copies land before it exits
-      if (lane == 0) {
-        if (q_open) drain_wait(q_full, q_phase, 200000000ull);
-        for (int s = 0; s < NS; ++s) {
-          // slots before rp.slot were last filled in this round, the others in the one before
-          // (or never: that wait returns at once)
-          drain_wait(&rf[s], s < rp.slot ? rp.phase : rp.phase ^ 1u, 200000000ull);
-        }
-      }
+    // every copy has landed before the CTA can exit, also when another role gave up
+    if (lane == 0) {
+      if (q_open) drain_wait(q_full, q_phase, 200000000ull);
+      for (int s = 0; s < NS; ++s)
+        // slots before rp.slot were last filled in this round, the others in the one before (or
+        // never: that wait returns at once)
+        drain_wait(&rf[s], s < rp.slot ? rp.phase : rp.phase ^ 1u, 200000000ull);
     }
+    __syncwarp();
   } else if (warp <= C::kSoft + 2) {
     // ---------------------------------------------------------------- MMA issuers
     reg_set<C::kRegMisc, C::kRegLaunch>();
@@ -1051,6 +1166,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         if (__any_sync(kFull, row_ok)) {
           const uint32_t o_col = o_base + i * D;
           // 16 columns of O (the streams' halves merged, normalised if the result is final)
+          float finite = 0.f;                         // NaN once a column of the row is not finite
           auto columns = [&](int c, float *x) {
             uint32_t o[16];
             if (keys) tmem_ld16(o_col + c, o);
@@ -1065,6 +1181,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 for (int q = 0; q < 16; ++q) x[q] = fmaf(__uint_as_float(o[q]), g1, x[q]);
               }
             }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) finite = fmaf(x[q], 0.f, finite);
           };
           if (whole) {
             const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
@@ -1105,6 +1223,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                       make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
               }
               dst += static_cast<size_t>(4) * a.part_rows;
+            }
+          }
+          uint32_t todo = __ballot_sync(kFull, row_ok && finite != 0.f);
+          __syncwarp();                               // the stores above come before the repairs
+          while (todo) {                              // rare: see repair_row
+            const int src = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const float mr = __shfl_sync(kFull, m, src), ir = __shfl_sync(kFull, inv, src);
+            const int r = (warp & 3) * 32 + src, rt = r / a.G + i * a.TT, rh = it.g * a.G + r % a.G;
+            float x[8];
+            const uint32_t redo = repair_row<D, FP8>(a, it, rt, rh, mr == -INFINITY ? 0.f : mr, x);
+            if (lane >= D / 8) continue;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (!((redo >> q) & 1u)) continue;
+              const int c = 8 * lane + q;
+              if (whole)
+                a.out[(static_cast<size_t>(it.tok0 + rt) * a.H_q + rh) * D + c] =
+                    static_cast<uint16_t>(pack_bf16x2(x[q] * ir, 0.f));
+              else
+                a.part[((static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + i * kRows + r) * 4 + (c & 3)] = x[q];
             }
           }
           if (row_ok) {
@@ -1486,6 +1625,10 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
            : make_bshd_map(&a.tk, pa.k_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R) &&
                  make_bshd_map(&a.tv, pa.v_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R));
   if (!maps) return cudaErrorInvalidValue;
+  a.q = static_cast<const uint16_t *>(pa.q);
+  a.q_stride = pa.q_stride;
+  a.k_pages = pa.k_pages;
+  a.v_pages = pa.v_pages;
   a.q_start = pa.q_start;
   a.kv_len = pa.kv_len;
   a.page_table = pa.page_table;

@@ -473,8 +473,8 @@ int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
  * calls (or two captured graphs) that may run at the same time need workspaces of their own.
  * The launches use programmatic dependent launch and wait for the stream's previous kernel
  * before they read anything.
- * Errors: INVALID_ARG / UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA; a CTA whose bounded waits ran
- * out leaves its rows unwritten and sets bit 3 of dsa_device_error. */
+ * Errors: INVALID_ARG / UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA; where a CTA's bounded waits ran
+ * out, bit 3 of dsa_device_error is set and the results of the call are unspecified. */
 int paged_attn(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
                const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *q_start,
                const int32_t *kv_len, const int32_t *page_table, const dsa_paged_shape *shape,

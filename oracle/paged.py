@@ -52,17 +52,20 @@ def dequantise(codes: np.ndarray, e: np.ndarray) -> np.ndarray:
     return np.where(e[..., None] == E_NAN, np.nan, x)
 
 
-def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float):
+def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float, lost=None):
     """q [n, H_q, D] at positions p0 .. over k, v [T, H_kv, D] (all float64): (out, lse, spread,
     size), where spread = sum_j w_j |v_j| (what a relative error of the weights can move) and
     size = the largest scale * sum_d |q_d k_d| of a head (what a rounding of the dot product is
-    relative to)."""
+    relative to).  lost [T] marks keys that are not there (their page is no page).  A NaN in a
+    key that a row sees makes the row NaN; other infinities and NaN reach only who sees them."""
     n, H_q, D = q.shape
     T, H_kv, _ = k.shape
     G = H_q // H_kv
     p = p0 + np.arange(n)[:, None]
     j = np.arange(T)[None]
     see = (j <= p) if n_stream is None else (j <= p) & ((j > p - n_stream) | (j < n_sink))
+    if lost is not None:
+        see = see & ~lost[None]
     out, spread = np.zeros((n, H_q, D)), np.zeros((n, H_q, D))
     lse, size = np.full((n, H_q), -np.inf), np.zeros((n, H_q))
     for h in range(H_q):
@@ -81,6 +84,8 @@ def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float):
         out[:, h], spread[:, h] = w @ vz, w @ np.abs(vz)
         for x in np.flatnonzero(bad.any(1)):          # only the rows that see the key
             out[see[:, x], h] += np.where(bad[x], vv[x], 0.0)
+        nan = (see & np.isnan(kk).any(1)[None]).any(1)
+        out[nan, h], lse[nan, h] = np.nan, np.nan
         ab = scale * (np.abs(q[:, h]) @ np.abs(np.nan_to_num(kk, posinf=0, neginf=0)).T)
         size[:, h] = np.where(see, ab, 0.0).max(1, initial=0.0)
     return out, lse, spread, size

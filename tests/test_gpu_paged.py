@@ -103,7 +103,7 @@ class Batch:
     def attn(self, **kw):
         return dsa.paged_attn(self.q, self.cache, self.q_start, self.kv_len, self.table, **kw)
 
-    def check(self, out, lse, n_sink=0, n_stream=None, scale=None, rows=None):
+    def check(self, out, lse, n_sink=0, n_stream=None, scale=None, rows=None, lost=None):
         torch.cuda.synchronize()
         scale = self.D ** -0.5 if scale is None else scale
         o, z, q = f64(out), lse.cpu().numpy().astype(np.float64), f64(self.q)
@@ -111,18 +111,21 @@ class Batch:
         for b, (n, t) in enumerate(self.seqs):
             if n and (rows is None or b in rows):
                 k, v = self.held(b)
-                O, L, spread, size = paged.attend(q[at:at + n], k, v, t - n, n_sink, n_stream, scale)
+                O, L, spread, size = paged.attend(q[at:at + n], k, v, t - n, n_sink, n_stream, scale,
+                                                  None if lost is None else lost[b])
                 ds = 2 * self.D * 2.0 ** -24 * size
                 got, zb = o[at:at + n], z[at:at + n]
                 assert np.array_equal(np.isneginf(L), np.isneginf(zb)), f"sequence {b}: empty rows"
+                assert np.array_equal(np.isnan(L), np.isnan(zb)), f"sequence {b}: NaN of lse"
                 fin = np.isfinite(L)
                 with np.errstate(invalid="ignore"):
                     err = np.abs(zb - L)[fin] - (ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(L))[fin]
                 assert (err <= 0).all(), f"sequence {b}: lse off by {err.max():.2e} too much"
                 tol = H * np.abs(O) + (H + 2 * ds + 2.0 ** -18)[..., None] * spread
                 good = np.isfinite(O)
-                assert np.array_equal(good, np.isfinite(got)), f"sequence {b}: {np.sum(good != np.isfinite(got))} rows"
-                err = np.abs(got - O)[good] - tol[good]
+                assert np.array_equal(np.isnan(O), np.isnan(got)), f"sequence {b}: NaN where there is none, or none"
+                assert np.array_equal(got[~good], O[~good], equal_nan=True), f"sequence {b}: infinities"
+                err = np.abs(got[good] - O[good]) - tol[good]
                 assert (err <= 0).all(), f"sequence {b}: out off by {err.max():.2e} too much"
             at += n
 
@@ -222,3 +225,257 @@ def test_attention_over_all_keys(case, fp8):
 def test_attention_window_and_sinks(n_sink, n_stream, fp8):
     b = Batch([(1, 1), (1, 700), (300, 900), (40, 45), (129, 640)], 8, 2, 128, 32, fp8, seed=40).write()
     b.check(*b.attn(n_sink=n_sink, n_stream=n_stream), n_sink=n_sink, n_stream=n_stream)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n_sink,n_stream", [(0, None), (40, 100)])
+@pytest.mark.parametrize("seqs", [[(1, 300), (60, 60), (7, 200)], [(300, 900), (150, 150)]])
+def test_infinities_and_nan_reach_only_who_sees_them(seqs, n_sink, n_stream, fp8):
+    """Value rows (and one key row) of some tokens hold infinities or NaN: rows that do not see
+    them -- earlier ones of the chunk, later ones beyond the window -- get their plain result."""
+    b = Batch(seqs, 8, 2, 128, 32, fp8, seed=50)
+    for s, (n, t) in enumerate(seqs):
+        for j, x in ((t - 1, float("nan")), (t - n // 2 - 1, float("inf")), (max(0, t - n - 30), float("-inf")), (5, float("nan"))):
+            b.v[s][j, 0, 3 + j % 7] = x
+    b.k[-1][seqs[-1][1] - 9, 1, 0] = float("nan")
+    b.write()
+    if fp8:   # a row with a NaN is NaN throughout; an infinity saturates
+        assert np.isnan(b.held(0)[1][5, 0]).all()
+    b.check(*b.attn(n_sink=n_sink, n_stream=n_stream), n_sink=n_sink, n_stream=n_stream)
+
+
+def test_nan_recomputed_across_shares():
+    """The same where the launch cuts the item into pieces, and with one query tile."""
+    for seqs in ([(3, 9000)], [(40, 9000)]):
+        b = Batch(seqs, 4, 1, 64, 64, False, seed=51)
+        b.v[0][-1, 0, 7] = float("nan")
+        b.v[0][-2, 0, 9] = float("inf")
+        b.write()
+        b.check(*b.attn())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_scores_and_moving_references(fp8):
+    """Scores of hundreds of units that grow along the keys: the softmax reference moves on
+    almost every tile, and early tiles vanish against later ones."""
+    b = Batch([(70, 1500), (1, 1500)], 8, 2, 128, 64, fp8, seed=52)
+    for s in range(2):
+        b.k[s] *= torch.linspace(0.1, 12.0, 1500, device="cuda")[:, None, None].bfloat16()
+    b.write()
+    b.check(*b.attn())
+    b.check(*b.attn(scale=1e-4), scale=1e-4)
+
+
+def test_values_at_the_top_of_the_range():
+    b = Batch([(20, 400)], 4, 2, 128, 16, True, seed=53)
+    b.v[0] *= 2.0 ** 100
+    b.k[0] *= 2.0 ** -100
+    b.write()
+    b.check(*b.attn())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+def test_bad_pages_are_skipped(page, fp8):
+    b = Batch([(1, 700), (50, 700), (40, 40)], 8, 2, 128, page, fp8, seed=54).write()
+    lost, table = [], b.table.cpu().numpy()
+    for s, (_, t) in enumerate(b.seqs):
+        i = np.arange(-(-t // page))
+        table[s, i[1::3]] = [-1, b.cache.k.shape[0], 2 ** 31 - 1][s]
+        lost.append(np.isin(np.arange(t) // page, i[1::3]))
+    b.table.copy_(torch.from_numpy(table))
+    b.check(*b.attn(), lost=lost)
+    k, _ = dsa.kv_cache_read(b.cache, b.kv_len, b.table)
+    for s, (_, t) in enumerate(b.seqs):
+        want = np.where(lost[s][:, None, None], 0.0, b.held(s)[0])
+        assert np.array_equal(f64(k[s, :t]), want)
+
+
+def test_rows_outside_the_chunks_and_short_lengths():
+    """Token rows before q_start[0] and behind q_start[B] stay as they were; a chunk longer than
+    its kv_len has rows at negative positions, which see nothing and are not written."""
+    b = Batch([(40, 100), (300, 300)], 4, 1, 128, 64, False, seed=55)
+    q = torch.cat([b.rows(5, 4), b.q, b.rows(130, 4)])
+    start = b.q_start + 5
+    b.write()
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 5.0, device="cuda")
+    dsa.paged_attn(q, b.cache, start, b.kv_len, b.table, out=out, lse=lse)
+    b.check(out[5:-130], lse[5:-130])
+    for t, x in ((out, 3.0), (lse, 5.0)):
+        assert (t[:5] == x).all() and (t[-130:] == x).all()
+    short = torch.tensor([25, 10], dtype=torch.int32, device="cuda")      # of 40 and 300 rows
+    before = b.cache.k.clone()
+    dsa.kv_cache_write(b.cache, b.rows(b.N, 1), b.rows(b.N, 1), b.q_start, short, b.table)
+    changed = (b.cache.k.view(torch.int16) != before.view(torch.int16)).flatten(2).any(2).sum()
+    assert int(changed) == 35
+    out, lse = b.attn()
+    out, lse = dsa.paged_attn(b.q, b.cache, b.q_start, short, b.table)
+    assert (out[:15] == 0).all() and torch.isneginf(lse[:15]).all() and torch.isfinite(lse[15:40]).all()
+    assert (out[40:330] == 0).all() and torch.isneginf(lse[40:330]).all() and torch.isfinite(lse[330:]).all()
+
+
+def test_no_tokens():
+    b = Batch([(1, 10)], 4, 1, 64, 16, False, seed=56).write()
+    none = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = dsa.paged_attn(q, b.cache, none, b.kv_len, b.table)
+    assert out.shape == q.shape and lse.shape == (0, 4)
+    dsa.kv_cache_write(b.cache, q[:, :1], q[:, :1], none, b.kv_len, b.table)
+    b.check(*b.attn())
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(57)
+    seqs = [(int(rng.integers(0, 4)), int(rng.integers(4, 200))) for _ in range(700)]
+    b = Batch(seqs, 4, 2, 64, 16, True, seed=57).write()
+    b.check(*b.attn(), rows=range(0, 700, 23))
+
+
+# ------------------------------------------------------------ as a program calls them
+
+def test_strided_tokens():
+    """q, k_new and v_new as slices of one fused projection."""
+    b = Batch([(30, 90), (1, 50)], 8, 2, 128, 32, True, seed=60)
+    b.write()
+    qkv = torch.zeros(b.N, 12 * 128, dtype=torch.bfloat16, device="cuda")
+    q, k, v = (x.view(b.N, -1, 128) for x in qkv.split([1024, 256, 256], dim=1))
+    q.copy_(b.q)
+    k.copy_(torch.cat([x[t - n:] for x, (n, t) in zip(b.k, b.seqs)]))
+    v.copy_(torch.cat([x[t - n:] for x, (n, t) in zip(b.v, b.seqs)]))
+    before = [t.clone() for t in (b.cache.k, b.cache.v, b.cache.k_scale, b.cache.v_scale)]
+    dsa.kv_cache_write(b.cache, k, v, b.q_start, b.kv_len, b.table)
+    for t, o in zip((b.cache.k, b.cache.v, b.cache.k_scale, b.cache.v_scale), before):
+        assert torch.equal(t, o)
+    out, lse = dsa.paged_attn(q, b.cache, b.q_start, b.kv_len, b.table)
+    want, wl = b.attn()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunks_one_after_another_equal_the_whole_prompt(fp8):
+    """A prompt in chunks, then single tokens: each step writes its rows and attends; every row
+    matches the float64 attention of the whole, and the cache read back feeds the selection and
+    the sparse decode, which attend the same window and sinks."""
+    T, steps = 700, [300, 129, 128, 140, 1, 1, 1]
+    b = Batch([(T, T)], 8, 2, 128, 64, fp8, seed=61)
+    got, lse, at = [], [], 0
+    for n in steps:
+        qs = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        kl = torch.tensor([at + n], dtype=torch.int32, device="cuda")
+        rows = slice(at, at + n)
+        dsa.kv_cache_write(b.cache, b.k[0][rows], b.v[0][rows], qs, kl, b.table)
+        o, z = dsa.paged_attn(b.q[rows], b.cache, qs, kl, b.table)
+        got.append(o)
+        lse.append(z)
+        at += n
+    b.check(torch.cat(got), torch.cat(lse))
+    # the decode step of the contiguous path over the same cache: no selection, sinks and window
+    k, v = dsa.kv_cache_read(b.cache, kl, b.table)
+    q = b.q[-1:].view(1, 1, 8, 128)
+    none, cnt = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    o1, l1 = dsa.sparse_attn_decode(q, k, v, kl, none, cnt, n_sink=20, n_stream=200)
+    o2, l2 = dsa.paged_attn(b.q[-1:], b.cache, qs, kl, b.table, n_sink=20, n_stream=200)
+    torch.cuda.synchronize()
+    # two roundings of P and of the result each (values are at most a few units)
+    assert (o1.float().view(8, 128) - o2.float().view(8, 128)).abs().max() <= 4 * H * float(v.abs().max())
+    assert (l1.view(-1) - l2.view(-1)).abs().max() <= 1e-3
+    # and the selection runs over what was read back
+    sel, n = dsa.hip_select(q, k, kl, dsa.HipConfig((64, 16), (128, 64), 20, 200))
+    assert 0 < int(n[0]) <= 64 and int(sel[0, 0]) >= 20
+
+
+def test_other_streams_graphs_and_repeats():
+    b = Batch([(64, 700), (1, 3000), (200, 200)], 8, 2, 128, 64, True, seed=62).write()
+    want, wl = b.attn()
+    torch.cuda.synchronize()
+    for _ in range(3):                                   # the same bits every time
+        out, lse = b.attn()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    s1.wait_stream(torch.cuda.current_stream())
+    s2.wait_stream(torch.cuda.current_stream())
+    o1, l1 = b.attn(stream=s1)                           # two calls at once
+    with torch.cuda.stream(s2):
+        o2, l2 = b.attn()
+    torch.cuda.synchronize()
+    for o, z in ((o1, l1), (o2, l2)):
+        assert torch.equal(o, want) and torch.equal(z, wl)
+    # two graphs with workspaces of their own, replayed side by side, on changed inputs
+    graphs = []
+    for _ in range(2):
+        n = dsa.paged_attn_workspace_bytes(b.q, b.cache, b.table)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(want), torch.empty_like(wl)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            k = torch.cat([x[t - n:] for x, (n, t) in zip(b.k, b.seqs)])
+            v = torch.cat([x[t - n:] for x, (n, t) in zip(b.v, b.seqs)])
+            dsa.kv_cache_write(b.cache, k, v, b.q_start, b.kv_len, b.table)
+            b.attn(out=out, lse=lse, workspace=ws)
+        graphs.append((g, out, lse))
+    b.q.copy_(b.rows(b.N, 8))
+    new, nl = b.attn()
+    torch.cuda.synchronize()
+    for (g, _, _), s in zip(graphs, (s1, s2)):
+        with torch.cuda.stream(s):
+            g.replay()
+            g.replay()
+    torch.cuda.synchronize()
+    for _, out, lse in graphs:
+        assert torch.equal(out, new) and torch.equal(lse, nl)
+    b.check(new, nl)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose first element lies beyond 2^31 elements of the cache."""
+    page, heads, D = 64, 8, 128
+    n = 2 ** 31 // (page * heads * D) + 40
+    b = Batch([(33, 500), (1, 900)], 16, heads, D, page, False, seed=63)
+    b.cache = dsa.PagedKVCache(*(torch.empty(n, page, heads, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    t = b.table
+    t[t >= 0] += n - 25
+    b.write()
+    b.check(*b.attn())
+    k, _ = dsa.kv_cache_read(b.cache, b.kv_len, b.table)
+    assert np.array_equal(f64(k[1, :900]), b.held(1)[0])
+
+
+def test_waits_that_run_out():
+    b = Batch([(100, 2000)], 8, 2, 128, 64, False, seed=64).write()
+    want, wl = b.attn()
+    torch.cuda.synchronize()
+    try:
+        dsa.set_wait_limit(1)
+        b.attn()
+        torch.cuda.synchronize()
+        assert dsa.device_error() == 8
+    finally:
+        dsa.set_wait_limit(0)
+    out, lse = b.attn()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_arguments_on_the_gpu():
+    b = Batch([(4, 40)], 8, 2, 128, 16, True, seed=65).write()
+    bad = [dict(n_sink=-1), dict(n_stream=-2), dict(scale=0.0), dict(scale=float("nan"))]
+    for kw in bad:
+        with pytest.raises((dsa.DsaError, ValueError)):
+            b.attn(**kw)
+    with pytest.raises(ValueError):
+        b.attn(out=torch.empty(4, 8, 128, device="cuda"))
+    with pytest.raises(dsa.DsaError):
+        b.attn(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        dsa.paged_attn(b.q.transpose(0, 1), b.cache, b.q_start, b.kv_len, b.table)
+    with pytest.raises(TypeError):
+        dsa.paged_attn(b.q, b.cache, b.q_start.long(), b.kv_len, b.table)
+    with pytest.raises(ValueError):
+        dsa.paged_attn(b.q, dsa.PagedKVCache(b.cache.k, b.cache.v), b.q_start, b.kv_len, b.table)
+    with pytest.raises(ValueError):
+        dsa.kv_cache_read(b.cache, b.kv_len, b.table, out=(b.q, b.q))
+    with pytest.raises(dsa.DsaError):                    # 24-token pages
+        c = dsa.PagedKVCache.empty(4, 24, 2, 128)
+        dsa.kv_cache_read(c, b.kv_len, b.table)
+    torch.cuda.synchronize()
+    b.check(*b.attn())
