@@ -82,7 +82,7 @@ constexpr float kSlack = 8.f;      // log2 units
 constexpr uint64_t kWaitLimitNs = 500000000ull;
 
 static __device__ int g_paged_error;   // sticky error word, read by dsa_device_error
-static __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
+std::atomic<unsigned long long> g_wait_limit_ns{kWaitLimitNs};   // of later launches
 
 struct TileMeta {
   uint32_t seen[kKeys / 32];   // bit c: key c of the tile is in a good page and some row sees it
@@ -162,6 +162,7 @@ struct Args {
   int part_rows, lg_min_units;
   int n_sink, n_stream;  // n_stream < 0: no window
   float sl2;
+  uint32_t wait_clocks;  // limit of a wait
 };
 
 // ------------------------------------------------------------------ schedule
@@ -294,18 +295,16 @@ __device__ __forceinline__ int tile_base(const Item &it, int k) {
 
 // ------------------------------------------------------------------ waits
 
-// What bounds the waits of a CTA: set once one gave up, and the limit in clocks.
+// What bounds the waits of a CTA: a word set once one gave up, and the limit in clocks.
 struct WaitCtl {
-  volatile int *abort;   // [0] gave up, [1] limit
-  __device__ __forceinline__ bool over(uint32_t t0) const {
-    return abort[0] || clock_lo() - t0 > static_cast<uint32_t>(abort[1]);
-  }
-  static __device__ __forceinline__ uint32_t clock_lo() {
-    uint32_t t;
-    asm volatile("mov.u32 %0, %%clock;\n" : "=r"(t));
-    return t;
-  }
+  volatile int *abort;
+  uint32_t limit, soon;   // the word is looked at after `soon` clocks
 };
+__device__ __forceinline__ uint32_t clock_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock;\n" : "=r"(t));
+  return t;
+}
 
 __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
@@ -324,10 +323,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
 // 3.89 ms, and up to 5.5 with long hints.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
   if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
-  const uint32_t t0 = WaitCtl::clock_lo();
+  const uint32_t t0 = clock_lo();
   do {
-    if (__any_sync(kFull, w.over(t0))) {
-      w.abort[0] = 1;
+    const uint32_t t = clock_lo() - t0;
+    if (__any_sync(kFull, t > w.soon) && __any_sync(kFull, t > w.limit || *w.abort)) {
+      *w.abort = 1;
       return false;
     }
   } while (!__all_sync(kFull, mbar_try_wait(bar, parity)));
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *turn = drained + 2, *fin = turn + 2;
   uint64_t *clean = fin + 1, *item_full = clean + C::kClean, *item_empty = item_full + kItems;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
-  const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4)};
+  const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4), a.wait_clocks, min(a.wait_clocks, 100000u)};
   Plan *plan = reinterpret_cast<Plan *>(sm + C::oMl);   // read before the first piece is handed out
   TileMeta *meta = reinterpret_cast<TileMeta *>(sm + C::oMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -578,9 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], C::kReaders);
     }
-    abort.abort[0] = 0;
-    // about two clocks a nanosecond; at most 2^31 of them, a second
-    abort.abort[1] = static_cast<int>(min(2ull * g_wait_limit_ns, 0x7fffffffull));
+    *abort.abort = 0;
     fence_mbar_init();
   }
   if (warp == C::kSoft + 1) {
@@ -1429,7 +1427,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (tid == 0 && abort.abort[0]) atomicExch(&g_paged_error, 1);
+  if (tid == 0 && *abort.abort) atomicExch(&g_paged_error, 1);
 }
 
 // ------------------------------------------------------------------ merge
@@ -1655,6 +1653,8 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.n_sink = std::min(pa.n_sink, cap);
   a.n_stream = pa.n_stream < 0 ? -1 : std::min(pa.n_stream, cap);
   a.sl2 = pa.scale * kLog2e;
+  // about two clocks a nanosecond; at most 2^31 of them, a second
+  a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
   auto kern = paged_attn_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
   if (e != cudaSuccess) return e;
@@ -1724,7 +1724,8 @@ int paged_attn_device_error() {
 }
 
 int paged_attn_set_wait_limit(unsigned long long ns) {
-  return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns)) == cudaSuccess ? 0 : -1;
+  g_wait_limit_ns = std::min(ns, 1ull << 40);
+  return 0;
 }
 
 }  // namespace dsa
