@@ -279,7 +279,7 @@ struct PagedPiece {
   long long item_u0;               // first schedule unit of the item
   long long q;                     // units per share (the first r of the P shares: one more)
   int r, P;
-  int n, lw;                       // key tiles, log2 of the units per tile
+  int n, u;                        // key tiles, schedule units of one
   int tok0, ntok, g;               // first token row, tokens, KV head
   int valid;
 };

@@ -75,6 +75,11 @@ using namespace tc;
 constexpr int kRows = 128;         // query rows per tile
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run at most 4 ahead)
+// The schedule's units are tenths of the time of a key tile of a two-tile item.  Key tiles of
+// one-tile items, bf16 (their bytes bound it) | FP8, few rows | FP8, more rows; and what an item
+// costs beside its tiles (the pipeline runs empty between two items, results leave); and the
+// least a share is worth cutting for.
+constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsQuad8 = 5, kUnitsOne8 = 6, kUnitsItem = 25, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -103,6 +108,9 @@ constexpr int kHasKeys = 2;    // some row sees a key
 constexpr int kWhole = 4;      // every tile of the item: the result is final
 constexpr int kStart = 8;      // the item's first tile
 constexpr int kEnd = 16;       // no piece: the share is done
+constexpr int kQuad = 32;      // at most kQuadRows rows, which all softmax warps share (FP8)
+constexpr int kQuadRows = 32;
+constexpr uint32_t kQuadTile = kQuadRows * 128;   // bytes of their P over 64 keys
 
 template <int D, bool FP8>
 struct Cfg {
@@ -135,11 +143,16 @@ struct Cfg {
   static constexpr uint32_t oItem = oMl + 2 * kRows * 8;
   static constexpr uint32_t oBar = oItem + kItems * sizeof(Item);
   // q_full, q_empty, slot full/empty, raw full/empty, then for both streams s_full, p_full,
-  // o_final, ml_full, drained, turn; fin, clean, item full/empty
-  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems;
+  // o_final, ml_full, drained, turn; fin, clean, item full/empty, maxed
+  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems + 2;
   static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item (not the producer)
   static constexpr uint32_t oMisc = oBar + kBars * 8;
-  static constexpr uint32_t kBytes = oMisc + 16;
+  // kQuad items, in the space of the second query tile: P of both streams (rows of 64 keys,
+  // [stream][half]); and the warps' maxima [stream][2][4 warps][32 rows]
+  static constexpr bool kShare = FP8;
+  static constexpr uint32_t oP = oQ + kTile;
+  static constexpr uint32_t oMax = D == 128 ? oP + 4 * kQuadTile : oMisc + 16;
+  static constexpr uint32_t kBytes = oMisc + 16 + (kShare && D != 128 ? 2048 : 0);
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -148,6 +161,7 @@ struct Cfg {
 
 struct Args {
   CUtensorMap tq, tk, tv;
+  CUtensorMap tq4;       // kQuad items' query rows
   const uint16_t *q;     // for repair_row, with the pages
   long long q_stride;
   const void *k_pages, *v_pages;
@@ -159,7 +173,8 @@ struct Args {
   float *part_ml;        // [2 * max_ctas][part_rows][2]
   PagedPiece *piece;     // [max_ctas]
   int B, n_tok, max_pages, n_pages, page_size, lg_page, H_q, H_kv, G, TT;
-  int part_rows, lg_min_units;
+  int TT4;               // tokens of a kQuad item's tile at most (0: no such items)
+  int part_rows;
   int n_sink, n_stream;  // n_stream < 0: no window
   float sl2;
   uint32_t wait_clocks;  // limit of a wait
@@ -174,7 +189,8 @@ struct Entry {
   int p_hi;            // position of the last one (< 0: no row sees a key)
   int ns, w0;          // tiles [0, ns), then [w0, w0 + n - ns)
   int n;               // tiles (at least 1: an entry without keys still writes its rows)
-  int lw;              // log2 of a tile's schedule weight: two query tiles weigh 2, one 1
+  int u;               // schedule units of a tile
+  bool one;            // one query tile
   bool keys;           // some row sees a key
 };
 
@@ -203,7 +219,8 @@ __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) 
   e.ntok = min(2 * a.TT, s.nq - m * 2 * a.TT);
   e.p0 = s.kv - s.nq + m * 2 * a.TT;
   e.p_hi = e.p0 + e.ntok - 1;
-  e.lw = e.ntok > a.TT ? 1 : 0;
+  e.one = e.ntok <= a.TT;
+  e.u = !e.one ? kUnitsTwo : e.ntok <= a.TT4 ? kUnitsQuad8 : a.k_scale ? kUnitsOne8 : kUnitsOne;
   e.ns = e.w0 = e.n = 0;
   if (e.p_hi >= 0) {
     const int last = e.p_hi / kKeys;
@@ -251,11 +268,18 @@ struct Walk {
 // first unit of share c: the units are dealt out q to each, the first r shares one more
 __device__ __forceinline__ long long share_begin(long long q, int r, int c) { return q * c + min(c, r); }
 
-// tiles [t0, t1) of an item (n tiles of 2^lw units from item_u0 on) in the share [u0, u1)
-__device__ __forceinline__ void piece_of(long long u0, long long u1, long long item_u0, int n, int lw,
-                                         int &t0, int &t1) {
-  t0 = u0 > item_u0 ? static_cast<int>(min((u0 - item_u0) >> lw, static_cast<long long>(n))) : 0;
-  t1 = u1 < item_u0 + (static_cast<long long>(n) << lw) ? static_cast<int>((u1 - item_u0) >> lw) : n;
+// Schedule units of an item of n tiles of u units: what it costs beside its tiles, then those.
+__device__ __forceinline__ long long units_of(int n, int u) { return kUnitsItem + static_cast<long long>(n) * u; }
+
+// tiles [t0, t1) of an item (its units from item_u0 on) in the share [u0, u1)
+__device__ __forceinline__ void piece_of(long long u0, long long u1, long long item_u0, int n, int u, int &t0,
+                                         int &t1) {
+  auto tile = [&](long long x) -> int {   // at most 2^23 tiles of 10 units: 32 bits
+    x = min(max(x - item_u0 - kUnitsItem, 0ll), static_cast<long long>(n) * u);
+    return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(u));
+  };
+  t0 = tile(u0);
+  t1 = tile(u1);
 }
 
 // the first non-empty piece at or after the current item
@@ -263,9 +287,9 @@ __device__ __forceinline__ void walk_settle(const Args &a, Walk &w) {
   while (true) {
     w.valid = w.item_u0 < w.u1;
     if (!w.valid) return;
-    piece_of(w.u0, w.u1, w.item_u0, w.e.n, w.e.lw, w.t0, w.t1);
+    piece_of(w.u0, w.u1, w.item_u0, w.e.n, w.e.u, w.t0, w.t1);
     if (w.t1 > w.t0) return;
-    w.item_u0 += static_cast<long long>(w.e.n) << w.e.lw;
+    w.item_u0 += units_of(w.e.n, w.e.u);
     if (++w.g == a.H_kv) {
       w.g = 0;
       ++w.m;
@@ -283,7 +307,7 @@ __device__ __forceinline__ void walk_settle(const Args &a, Walk &w) {
 }
 
 __device__ __forceinline__ void walk_next(const Args &a, Walk &w) {
-  w.u0 = max(w.u0, w.item_u0 + (static_cast<long long>(w.e.n) << w.e.lw));   // this item is done
+  w.u0 = max(w.u0, w.item_u0 + units_of(w.e.n, w.e.u));   // this item is done
   walk_settle(a, w);
 }
 
@@ -543,6 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   uint64_t *s_full = raw_empty + C::kRawSlots, *p_full = s_full + 2, *o_final = p_full + 2;
   uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *turn = drained + 2, *fin = turn + 2;
   uint64_t *clean = fin + 1, *item_full = clean + C::kClean, *item_empty = item_full + kItems;
+  uint64_t *maxed = item_empty + kItems;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
   const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4), a.wait_clocks, min(a.wait_clocks, 100000u)};
   Plan *plan = reinterpret_cast<Plan *>(sm + C::oMl);   // read before the first piece is handed out
@@ -571,6 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       mbar_init(&ml_full[i], 4);
       mbar_init(&drained[i], 4);
       mbar_init(&turn[i], 1);
+      mbar_init(&maxed[i], 4);
     }
     mbar_init(fin, 2);
     for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 1);
@@ -602,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         many = s.nq > 2 * a.TT;
         if (!many && s.nq > 0) {
           const Entry e = make_entry(a, s, 0);
-          u = (static_cast<long long>(e.n) << e.lw) * a.H_kv;
+          u = units_of(e.n, e.u) * a.H_kv;
         }
       }
       uint32_t todo = __ballot_sync(kFull, many);
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         long long x = 0;
         for (int m = lane; m < np; m += 32) {
           const Entry e = make_entry(a, s, m);
-          x += static_cast<long long>(e.n) << e.lw;
+          x += units_of(e.n, e.u);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
@@ -636,10 +662,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         if (b < a.B) su[b] = run + v;   // inclusive
         run += __shfl_sync(kFull, v, 31);
       }
-      // shares: at least min_units each, so that a short launch is not cut finer than pays
+      // shares: at least kUnitsMin each, so that a short launch is not cut finer than pays
       const long long total = run;
-      const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total >> a.lg_min_units)));
-      // total / P digit by digit (total < 2^46: 4096 sequences of 2^23 tiles, twice, 128 heads
+      const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total / kUnitsMin)));
+      // total / P digit by digit (total < 2^47: 4096 sequences of 2^23 tiles, 10 units, 128 heads
       // at most, and P < 2^16)
       const uint32_t up = static_cast<uint32_t>(P), high = static_cast<uint32_t>(total >> 16);
       const uint32_t mid = ((high % up) << 16) | static_cast<uint32_t>(total & 0xffff);
@@ -664,10 +690,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         // its pair that holds u0, 32 pairs at a time
         for (int m0 = 0; m0 < np; m0 += 32) {
           const int mm = m0 + lane;
-          uint32_t item = 0;   // units of one KV head: at most 2^24
+          uint32_t item = 0;   // units of one KV head: below 2^27
           if (mm < np) {
             const Entry e = make_entry(a, s, mm);
-            item = static_cast<uint32_t>(e.n) << e.lw;
+            item = static_cast<uint32_t>(units_of(e.n, e.u));
           }
           const long long own = static_cast<long long>(item) * a.H_kv;
           long long v = own;
@@ -722,8 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     const uint32_t s_col = tl + C::cS + i * kKeys;
     const uint32_t o_col = tl + C::cO + i * D;
     float2 *ml = reinterpret_cast<float2 *>(sm + C::oMl) + i * kRows + row;
-    const int rtok = row / a.G;
-    uint32_t s_phase = 0, d_phase = 1;
+    uint32_t s_phase = 0, d_phase = 1, x_buf = 0;
     uint32_t tile = 0;                                // key tiles seen so far (meta ring)
     bool ok = true;
     // The piece is read from its ring entry as it is needed and given back at the end.
@@ -732,6 +757,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       const Item &it = items[ri.slot];
       if (it.flags & kEnd) break;
       const bool single = it.flags & kSingle, keys = it.flags & kHasKeys;
+      // Few rows lie in every warp's lanes (see the producer), and each warp takes 32 of the keys.
+      const bool quad = C::kShare && (it.flags & kQuad);
+      const int rtok = (quad ? lane : row) / a.G;
       const int tok = rtok + (single ? 0 : i * a.TT); // token of the piece's entry
       const bool row_ok = rtok < a.TT && tok < it.ntok;
       const bool warp_ok = __any_sync(kFull, row_ok);
@@ -775,15 +803,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
               }
             };
             constexpr int kParts = kKeys / C::kPart;
+            const int part0 = quad ? warp & 3 : 0, part1 = quad ? part0 : kParts - 1;
             float mt = -INFINITY;
 #pragma unroll 1
-            for (int part = 0; part < kParts; ++part) {
+            for (int part = part0; part <= part1; ++part) {
               scores(part);
               float mx[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int c = 0; c < C::kPart; c += 2)
                 mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
               mt = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+            }
+            if (quad) {                               // the maximum over all four warps' keys
+              float *x = reinterpret_cast<float *>(sm + C::oMax) + (2 * i + x_buf) * kRows;
+              x[row] = mt;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&maxed[i]);
+              if (!(ok = warp_wait(&maxed[i], x_buf, abort))) break;
+              x_buf ^= 1u;                            // buffer and phase alike: the one before is read
+              mt = fmax3(x[lane], x[lane + 32], fmaxf(x[lane + 64], x[lane + 96]));
             }
             mt *= a.sl2;
             const bool move = mt > m_ref + kSlack;
@@ -794,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 l *= f;
                 m_ref = mt;
               }
-              if (k > first) {                        // O holds earlier tiles of this piece
+              if (k > first && (!quad || (warp & 3) == 0)) {   // O holds earlier tiles of this piece
                 const float2 f2 = make_float2(f, f);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
@@ -815,8 +853,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             const float2 nm2 = make_float2(nm, nm), sl22 = make_float2(a.sl2, a.sl2);
             float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int part = kParts - 1; part >= 0; --part) {   // the last part is still here
-              if (kParts > 1 && part < kParts - 1) scores(part);
+            for (int part = part1; part >= part0; --part) {   // the last part is still here
+              if (kParts > 1 && part < part1) scores(part);
 #pragma unroll
               for (int c0 = 0; c0 < C::kPart; c0 += 32) {
                 uint32_t pk[16];
@@ -828,7 +866,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                   else acc0 = fadd2(acc0, x);
                   pk[c >> 1] = pack_bf16x2(x.x, x.y);
                 }
-                tmem_st16(s_col + C::kPart * part + c0, pk);
+                if (quad) {                           // 64 bytes of the row's 128 for these 64 keys
+                  unsigned char *dst = sm + C::oP + (2 * i + (part >> 1)) * kQuadTile + lane * 128;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(dst + ((((part & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+                        make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+                  fence_proxy_async_smem();
+                } else {
+                  tmem_st16(s_col + C::kPart * part + c0, pk);
+                }
               }
             }
             const float2 as = fadd2(acc0, acc1);
@@ -896,8 +943,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       it.T = w.t1 - w.t0;
       it.b = w.b;
       it.g = w.g;
-      it.flags = !w.valid ? kEnd : (w.e.lw == 0 ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
-                                       (start ? kStart : 0);
+      it.flags = !w.valid ? kEnd : (w.e.one ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
+                                       (start ? kStart : 0) | (w.e.ntok <= a.TT4 ? kQuad : 0);
       if (lane == 0) {
         items[ri.slot] = it;
         mbar_arrive(&item_full[ri.slot]);
@@ -908,7 +955,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           d.r = plan_r;
           d.P = plan_P;
           d.n = w.e.n;
-          d.lw = w.e.lw;
+          d.u = w.e.u;
           d.tok0 = w.e.tok0;
           d.ntok = w.e.ntok;
           d.g = w.g;
@@ -935,12 +982,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       }
       q_open = true;
       if (lane == 0) {
-        const int nt = single ? 1 : 2;
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nt * C::kHalves * a.TT * a.G * 128));
+        // two tiles, one, or a few rows into each softmax warp's lanes
+        const bool quad = C::kShare && (it.flags & kQuad);
+        const int nt = quad ? 4 : single ? 1 : 2, tt = quad ? a.TT4 : a.TT;
+        const uint32_t pitch = quad ? kQuadTile : C::kTile;
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nt * C::kHalves * tt * a.G * 128));
         for (int t = 0; t < nt; ++t)
           for (int hh = 0; hh < C::kHalves; ++hh)
-            tma_load_4d(sm + C::oQ + t * C::kTile + hh * C::kHalf, &a.tq, q_full, 64 * hh, it.g * a.G,
-                        it.tok0 + t * a.TT, 0);
+            tma_load_4d(sm + C::oQ + t * pitch + hh * C::kHalf, quad ? &a.tq4 : &a.tq, q_full, 64 * hh, it.g * a.G,
+                        it.tok0 + (quad ? 0 : t * a.TT), 0);
       }
       __syncwarp();
       const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
@@ -1015,6 +1065,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     const uint64_t dq = sdesc_sw128(smem_u32(sm + C::oQ), 16, 1024);
     const uint64_t dk = sdesc_sw128(smem_u32(sm + C::oRing), 16, 1024);
     const uint64_t dv = sdesc_sw128(smem_u32(sm + C::oRing), C::kHalf, 1024);
+    const uint64_t dp = sdesc_sw128(smem_u32(sm + C::oP + 2 * i * kQuadTile), 16, 1024);
     const uint32_t leader = lane == 0 ? 1u : 0u;
     Ring<C::kSlots> rp;
     Ring<FP8 ? 1 : C::kClean> rc;
@@ -1037,7 +1088,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       // O_i of the piece before has been read (every piece is waited for, so that no phase is
       // missed)
       d_phase ^= 1u;
-      const bool single = it.flags & kSingle;
+      const bool single = it.flags & kSingle, quad = C::kShare && (it.flags & kQuad);
       const int T = it.T, ahead = single ? 2 : 1;
       if (!(it.flags & kHasKeys)) {
         ok = warp_wait(&drained[i], d_phase, abort);
@@ -1081,11 +1132,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           tc_fence_after();
           const uint64_t bd = dv + static_cast<uint32_t>(slot) * (C::kTile >> 4);
           const uint32_t acc = first ? 0u : 1u;
+          if (quad) {
+            // P in shared memory; the tile's rows behind kQuadRows are whatever lies there, their
+            // O is not read
 #pragma unroll
-          for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(leader, o_tm, s_tm + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, kk > 0 ? 1u : acc);
+            for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+              mma_ss(leader, o_tm, dp + (kk >> 2) * (kQuadTile >> 4) + (kk & 3) * 2, bd + kk * 128, id_pv,
+                     kk > 0 ? 1u : acc);
+          } else {
+#pragma unroll
+            for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(leader, o_tm, s_tm + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, kk > 0 ? 1u : acc);
+          }
           commit_if(leader, &empty[slot]);
           if (k == last) {
+            if (quad) commit_if(leader, q_empty);     // P lies in the second query tile's space
             commit_if(leader, &o_final[i]);
             pass_turn();
           }
@@ -1099,7 +1160,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           }
           commit_if(leader, &s_full[i]);
           commit_if(leader, &empty[slot]);
-          if (k == last) commit_if(leader, q_empty);
+          if (k == last && !quad) commit_if(leader, q_empty);
           if (k >= ahead) pass_turn();
         }
       }
@@ -1144,12 +1205,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         const int tok = rtok + i * a.TT;              // token of the piece's entry
         const bool row_ok = rtok < a.TT && tok < it.ntok;
         if (!(ok = wait_o(i, keys))) break;
-        float m = ml[i * kRows].x, l = ml[i * kRows].y, f0 = 1.f, f1 = 0.f;
+        const bool quad = C::kShare && (it.flags & kQuad);   // a sum per softmax warp, one reference
+        auto sum = [&](int s) -> float {
+          const float2 *x = ml + s * kRows;
+          return quad && warp == C::kEpi ? (x[0].y + x[32].y) + (x[64].y + x[96].y) : x[0].y;
+        };
+        float m = ml[i * kRows].x, l = sum(i), f0 = 1.f, f1 = 0.f;
         bool two = false;
         if (single) {                                 // the other half of the key tiles
           two = keys && it.T > 1;
           if (!(ok = wait_o(1, two))) break;
-          const float2 o = ml[kRows];
+          const float2 o = make_float2(ml[kRows].x, sum(1));
           const float mm = fmaxf(m, o.x);
           f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
           f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mm);
@@ -1452,7 +1518,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Mer
   grid_dep_wait();
   const PagedPiece pc = a.piece[blockIdx.x];
   if (!pc.valid) return;
-  const long long end = pc.item_u0 + (static_cast<long long>(pc.n) << pc.lw);
+  const long long end = pc.item_u0 + units_of(pc.n, pc.u);
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.part);
   constexpr int kStep = 128 / D;                      // pieces added per step
@@ -1469,7 +1535,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Mer
       int slot = -1;                                  // this lane's share has no piece
       if (c < pc.P && share_begin(pc.q, pc.r, c) < end) {
         int t0, t1;
-        piece_of(share_begin(pc.q, pc.r, c), share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
+        piece_of(share_begin(pc.q, pc.r, c), share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.u, t0, t1);
         if (t1 > t0) slot = 2 * c + (t0 == 0 ? 1 : 0);
       }
       const uint32_t have = __ballot_sync(kFull, slot >= 0);
@@ -1532,7 +1598,7 @@ __global__ void __launch_bounds__(D * 2) paged_merge_rows_kernel(const MergeArgs
   const int t = qt * a.TT + r / a.G, j = r % a.G;
   const bool in = r < a.TT * a.G && t < pc.ntok;
   if (!__any_sync(kFull, in)) return;
-  const long long end = pc.item_u0 + (static_cast<long long>(pc.n) << pc.lw);
+  const long long end = pc.item_u0 + units_of(pc.n, pc.u);
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + prow;
   const float4 *po = reinterpret_cast<const float4 *>(a.part) + static_cast<size_t>(4 * warp) * a.part_rows + prow;
   float M = -INFINITY, L = 0.f;
@@ -1544,7 +1610,7 @@ __global__ void __launch_bounds__(D * 2) paged_merge_rows_kernel(const MergeArgs
     const long long u0 = share_begin(pc.q, pc.r, c);
     if (u0 >= end) break;
     int t0, t1;
-    piece_of(u0, share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.lw, t0, t1);
+    piece_of(u0, share_begin(pc.q, pc.r, c + 1), pc.item_u0, pc.n, pc.u, t0, t1);
     if (t1 <= t0 || !in) continue;
     const int slot = 2 * c + (t0 == 0 ? 1 : 0);
     const float2 v = ml[static_cast<size_t>(slot) * a.part_rows];
@@ -1609,6 +1675,29 @@ bool make_query_map(CUtensorMap *m, const void *base, int D, int H, long long st
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What a launch needs of the current device: its SMs, the kernel's shared memory allowed there
+// and its registers as the warpgroups' shares expect them (they add up to what the launch holds;
+// a build that holds less would wait for registers that no warp gives back).  Asked once per
+// device: the three calls took 1.2 us of each launch.
+template <int D, bool FP8, class Kern>
+cudaError_t prepare(Kern kern, int &sms) {
+  using C = Cfg<D, FP8>;
+  static std::atomic<int> known[64];                  // SMs by device, 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (sms = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if (fa.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if (keep) known[dev].store(sms, std::memory_order_release);
+  return cudaSuccess;
+}
+
 template <int D, bool FP8>
 cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   using C = Cfg<D, FP8>;
@@ -1622,7 +1711,9 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
                  make_code_map(&a.tv, pa.v_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R)
            : make_bshd_map(&a.tk, pa.k_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R) &&
                  make_bshd_map(&a.tv, pa.v_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R));
-  if (!maps) return cudaErrorInvalidValue;
+  a.TT4 = C::kShare ? kQuadRows / G : 0;
+  if (!maps || (a.TT4 > 0 && !make_query_map(&a.tq4, pa.q, D, pa.H_q, pa.q_stride, pa.n_tok, G, a.TT4)))
+    return cudaErrorInvalidValue;
   a.q = static_cast<const uint16_t *>(pa.q);
   a.q_stride = pa.q_stride;
   a.k_pages = pa.k_pages;
@@ -1648,7 +1739,6 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.G = G;
   a.TT = TT;
   a.part_rows = pa.part_rows;
-  a.lg_min_units = 1;
   const int cap = pa.max_pages * pa.page_size;
   a.n_sink = std::min(pa.n_sink, cap);
   a.n_stream = pa.n_stream < 0 ? -1 : std::min(pa.n_stream, cap);
@@ -1656,23 +1746,12 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   // about two clocks a nanosecond; at most 2^31 of them, a second
   a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
   auto kern = paged_attn_kernel<D, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
+  int sms = 0;
+  cudaError_t e = prepare<D, FP8>(kern, sms);
   if (e != cudaSuccess) return e;
-  // the warpgroups' register shares add up to what the launch holds; a build that holds less
-  // would wait for registers that no warp gives back
-  static std::atomic<bool> regs_ok{false};
-  if (!regs_ok) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-    if (fa.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
-    regs_ok = true;
-  }
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  // no more CTAs than the launch can have shares of min_units
+  // no more CTAs than the launch can have shares of kUnitsMin
   const long long pairs = pa.B + pa.n_tok / (2 * TT);
-  const long long most = pairs * pa.H_kv * 2 * ((cap + kKeys - 1) / kKeys + 1) / (1 << a.lg_min_units) + 1;
+  const long long most = pairs * pa.H_kv * (kUnitsTwo * ((cap + kKeys - 1) / kKeys + 1) + kUnitsItem) / kUnitsMin + 1;
   const int P = static_cast<int>(std::min(static_cast<long long>(std::min(sms, kPagedMaxCtas)), most));
   {
     ProfScope ps(FP8 ? "paged_attn_fp8" : "paged_attn", s);

@@ -255,6 +255,19 @@ def test_nan_recomputed_across_shares():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [1, 3, 4, 5, 32, 33])
+@pytest.mark.parametrize("n_sink,n_stream", [(0, None), (40, 300)])
+def test_few_rows_between_many(group, D, fp8, n_sink, n_stream):
+    """Items of at most 32 rows, of one more, and of two tiles, handed out in turn."""
+    t = max(32 // group, 1)
+    two = 2 * (128 // group)
+    seqs = [(t, 700), (two, two + 250), (1, 1), (t + 1, 130), (1, 128), (two + 1, two + 140), (1, 900), (t, t)]
+    b = Batch(seqs, 2 * group, 2, D, 16, fp8, seed=20 + group).write()
+    b.check(*b.attn(n_sink=n_sink, n_stream=n_stream), n_sink=n_sink, n_stream=n_stream)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_large_scores_and_moving_references(fp8):
     """Scores of hundreds of units that grow along the keys: the softmax reference moves on
     almost every tile, and early tiles vanish against later ones."""
