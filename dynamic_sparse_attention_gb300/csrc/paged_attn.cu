@@ -1195,11 +1195,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         tc_fence_after();
         return true;
       };
-      auto release = [&](int i) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&drained[i]);
-      };
 #pragma unroll 1
       for (int i = 0; i < (single ? 1 : 2); ++i) {
         const int tok = rtok + i * a.TT;              // token of the piece's entry
@@ -1227,16 +1222,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         const bool none = !keys || f0 == 0.f || l == 0.f;
         const size_t orow = static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + rhead;
         const int prow = i * kRows + row;
-        if (__any_sync(kFull, row_ok)) {
+        auto release = [&]() {                        // TMEM and (m, l) are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&drained[i]);
+            if (single) mbar_arrive(&drained[1]);
+          }
+        };
+        if (!__any_sync(kFull, row_ok)) {
+          release();
+        } else {
           const uint32_t o_col = o_base + i * D;
           // 16 columns of O (the streams' halves merged, normalised if the result is final)
-          float finite = 0.f;                         // NaN once a column of the row is not finite
+          float2 finite = make_float2(0.f, 0.f);      // NaN once a column of the row is not finite
           auto columns = [&](int c, float *x) {
             uint32_t o[16];
             if (keys) tmem_ld16(o_col + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] = none ? 0.f : __uint_as_float(o[q]) * g0;
+            for (int q = 0; q < 16; q += 2) {
+              const float2 y = fmul2(make_float2(__uint_as_float(o[q]), __uint_as_float(o[q + 1])), make_float2(g0, g0));
+              x[q] = none ? 0.f : y.x;
+              x[q + 1] = none ? 0.f : y.y;
+            }
             if (two) {
               tmem_ld16(o_col + D + c, o);
               tmem_wait_ld();
@@ -1246,17 +1255,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
               }
             }
 #pragma unroll
-            for (int q = 0; q < 16; ++q) finite = fmaf(x[q], 0.f, finite);
+            for (int q = 0; q < 16; q += 2) finite = ffma2(make_float2(x[q], x[q + 1]), make_float2(0.f, 0.f), finite);
           };
           if (whole) {
             const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              // 4 x 4 transpose of 16-byte pieces over four lanes: store j then covers 64
-              // contiguous bytes of row j of the quad instead of 16 bytes of every row
-              uint4 y[4];
+            constexpr int kCols = 32;
+            long long to[4];                          // rows of the lane's quad (-1: no such row)
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
+            for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(kFull, mine_row, (lane & ~3) + x);
+#pragma unroll 1
+            for (int c = 0; c < D; c += kCols) {
+              uint4 y[kCols / 8];
+#pragma unroll
+              for (int q = 0; q < kCols / 16; ++q) {
                 float x[16];
                 columns(c + 16 * q, x);
                 y[2 * q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -1264,14 +1275,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 y[2 * q + 1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]),
                                           pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
               }
-              swap4(y[0], y[1], lane & 1, 1);
-              swap4(y[2], y[3], lane & 1, 1);
-              swap4(y[0], y[2], lane & 2, 2);
-              swap4(y[1], y[3], lane & 2, 2);
+              if (c + kCols == D) release();             // the next item's P V need not wait for the stores
+              // 4 x 4 transposes of 16-byte pieces over four lanes: store x then covers 64
+              // contiguous bytes of row x of the quad instead of 16 bytes of every row
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const long long r = __shfl_sync(kFull, mine_row, (lane & ~3) + x);   // -1: no such row
-                if (r >= 0) *reinterpret_cast<uint4 *>(a.out + r * D + c + 8 * (lane & 3)) = y[x];
+              for (int h = 0; h < kCols / 8; h += 4) {
+                swap4(y[h], y[h + 1], lane & 1, 1);
+                swap4(y[h + 2], y[h + 3], lane & 1, 1);
+                swap4(y[h], y[h + 2], lane & 2, 2);
+                swap4(y[h + 1], y[h + 3], lane & 2, 2);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if (to[x] >= 0)
+                    *reinterpret_cast<uint4 *>(a.out + to[x] * D + c + 8 * h + 8 * (lane & 3)) = y[h + x];
               }
             }
           } else {
@@ -1288,8 +1304,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
               }
               dst += static_cast<size_t>(4) * a.part_rows;
             }
+            release();
           }
-          uint32_t todo = __ballot_sync(kFull, row_ok && finite != 0.f);
+          uint32_t todo = __ballot_sync(kFull, row_ok && finite.x + finite.y != 0.f);
           __syncwarp();                               // the stores above come before the repairs
           while (todo) {                              // rare: see repair_row
             const int src = __ffs(todo) - 1;
@@ -1317,8 +1334,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
               a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           }
         }
-        release(i);
-        if (single) release(1);
       }
       ml_phase ^= 1u;
     }
