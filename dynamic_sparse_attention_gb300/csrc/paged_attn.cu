@@ -127,7 +127,7 @@ struct Cfg {
   // registers a thread after the split by warpgroup (softmax x 2, warps 8-11, epilogue,
   // converters x 2); what the launch holds, threads x kRegLaunch, is what the shares add up to
   static constexpr int kRegLaunch = FP8 ? 80 : 128;
-  static constexpr int kRegSoft = FP8 ? 96 : 176, kRegMisc = FP8 ? 64 : 72, kRegEpi = FP8 ? 80 : 88,
+  static constexpr int kRegSoft = FP8 ? 104 : 176, kRegMisc = FP8 ? 64 : 72, kRegEpi = FP8 ? 64 : 88,
                        kRegConv = FP8 ? 72 : 0;
   static_assert(256 * kRegSoft + 128 * kRegMisc + 128 * kRegEpi + 256 * kRegConv == kThreads * kRegLaunch,
                 "register split");
@@ -1157,11 +1157,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           for (uint32_t kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (C::kHalf >> 4) + (kk & 3) * 2;
             mma_ss(leader, s_tm, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+            // (the turn reaches the other issuer while the last ones run)
+            if (kk == D / 16 - 2 && k >= ahead) pass_turn();
           }
           commit_if(leader, &s_full[i]);
           commit_if(leader, &empty[slot]);
           if (k == last && !quad) commit_if(leader, q_empty);
-          if (k >= ahead) pass_turn();
         }
       }
       if (ok && single && i == 1 && (T & 1)) {        // stream 0 had one tile more
