@@ -358,6 +358,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
   return true;
 }
 
+// The same for what takes a whole piece of T key tiles: T limits more.
+__device__ __forceinline__ bool warp_wait_piece(uint64_t *bar, uint32_t parity, const WaitCtl &w, int T) {
+  uint32_t t0 = clock_lo();
+  while (!__all_sync(kFull, mbar_try_wait(bar, parity))) {
+    const uint32_t t = clock_lo() - t0;
+    if (!__any_sync(kFull, t > w.soon)) continue;
+    const bool over = __any_sync(kFull, t > w.limit);
+    if ((over && T-- <= 0) || __any_sync(kFull, *w.abort)) {
+      *w.abort = 1;
+      return false;
+    }
+    if (over) t0 = clock_lo();
+  }
+  return true;
+}
+
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -1188,7 +1204,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       const int slot = 2 * blockIdx.x + (it.flags & kStart ? 1 : 0);
       // (m, l) of stream i, and O_i complete; false: gave up
       auto wait_o = [&](int i, bool any) -> bool {
-        if (!warp_wait(&ml_full[i], ml_phase, abort)) return false;
+        if (!warp_wait_piece(&ml_full[i], ml_phase, abort, it.T)) return false;
         if (any) {
           if (!warp_wait(&o_final[i], of_phase[i], abort)) return false;
           of_phase[i] ^= 1u;

@@ -469,6 +469,21 @@ def test_waits_that_run_out():
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+def test_items_longer_than_the_wait_limit():
+    """A wait is bounded per key tile, not per item: items of 160 tiles on average (some 300 us
+    each) under a limit of 100 us."""
+    b = Batch([(40960, 40960)], 1, 1, 64, 128, False, seed=31).write()
+    try:
+        dsa.set_wait_limit(100_000)
+        out, lse = b.attn()
+        torch.cuda.synchronize()
+        assert dsa.device_error() == 0
+    finally:
+        dsa.set_wait_limit(0)
+    want, want_lse = b.attn()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_arguments_on_the_gpu():
     b = Batch([(4, 40)], 8, 2, 128, 16, True, seed=65).write()
     bad = [dict(n_sink=-1), dict(n_stream=-2), dict(scale=0.0), dict(scale=float("nan"))]
