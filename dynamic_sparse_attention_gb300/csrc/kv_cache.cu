@@ -11,7 +11,10 @@
 // top of the range.  A row that holds a NaN takes the scale byte 255 (E8M0's NaN) and reads
 // back as NaN throughout.
 //
-// Both kernels are bound by HBM: a row is read once and written once.
+// Both kernels are bound by HBM: a row is read once and written once.  Measured (of 6,773 GB/s):
+// writing 48,549 tokens of 8 heads of 128 to an FP8 cache (299 MB) 50.6 us, 5,900 GB/s (87 %);
+// 10,764 tokens of 16 heads of 64 in bf16 (88 MB) 18 us; reading 131,072 tokens of 8 heads of 128
+// back from FP8 (807 MB) 121 us, 6,670 GB/s (98 %); a decode step's few rows take a launch, 2.4 us.
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"

@@ -8,12 +8,12 @@
 // rows (row = token * G + head), so a K/V tile is loaded once for all of them and a single
 // token already brings G rows.  An item is one KV head of up to two such 128-row tiles of
 // one sequence, over the 128-key tiles that any of its rows sees (sink tiles, then window
-// tiles).  The items' key tiles of the whole launch, laid end to end, are cut into equal
-// shares, one per CTA (one CTA per SM): uneven lengths, one long context and many short ones
-// all fill the GPU without a schedule made on the host, which knows no length.  A CTA finds
-// its share from q_start and kv_len alone (one parallel pass over the sequences).  An item
-// that a share boundary cuts leaves fp32 partials (O, m, l) in the workspace, and a second
-// kernel merges them.
+// tiles).  The items' key tiles of the whole launch, laid end to end and weighed by what they
+// and the items take (kUnitsTwo and so on), are cut into equal shares, one per CTA (one CTA per
+// SM): uneven lengths, one long context and many short ones all fill the GPU without a schedule
+// made on the host, which knows no length.  A CTA finds its share from q_start and kv_len alone
+// (one parallel pass over the sequences).  An item that a share boundary cuts leaves fp32
+// partials (O, m, l) in the workspace, and a second kernel merges them.
 //
 // One CTA, two streams of scores (i = 0, 1), each with its own TMEM buffers S_i, O_i and its
 // own four softmax warps, so that one stream's softmax runs while the tensor core works for
@@ -21,7 +21,10 @@
 //   two-tile items: stream i is query tile i, both see every key tile (256 rows per loaded
 //     K/V tile);
 //   one-tile items (a few tokens): both streams hold the same query tile and take the key
-//     tiles alternately; their halves are merged in TMEM at the end of the item.
+//     tiles alternately; the epilogue joins their halves.  Of FP8 caches' items with at most 32
+//     rows the query rows lie four times in the tile, once in each softmax warp's TMEM lanes:
+//     each warp takes the exponentials of 32 of a tile's keys (one warp would take all of them
+//     otherwise) and P goes through shared memory (1M-key FP8 token: 633 -> 562 us).
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (schedule and
 // TMA), 9 and 10 MMA issuers of stream 0 and 1 (one issuer for both spent 1,800 clocks a turn
 // on waits, 16 MMAs and commits against 1,024 in the tensor core), 11 cleaner (bf16 caches),
@@ -32,7 +35,24 @@
 // other role holds that state: beside 224 KB of shared memory next to no L1 is left, and a
 // spilled register costs a round trip to L2.  Every role is one compact loop: instruction
 // fetches bound this kernel before its pipes do (with each role's code unrolled and inlined per
-// case, 150 KB in all, the FP8 cases took two to three times as long).
+// case the FP8 cases took two to three times as long; an epilogue of 64 columns at a time in
+// place of 32 costs the 8K window 159 -> 188 us).
+//
+// What bounds it (one GB300, 6,773 GB/s and 1,849 TFLOP/s measured):
+//   2,048 tokens against 131,072 bf16 keys, 32/8 heads of 128: 3.15 ms, 1,384 TFLOP/s, 75 % of the
+//     tensor core's burst and 83 % of its sustained rate (the card is at its power limit).  Beside
+//     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
+//     stream depend on one another, and 512 TMEM columns hold no third stream.
+//   16 tokens over 32,768 bf16 keys each: 180 us, 6,490 GB/s (96 %): HBM.
+//   one token over 1,048,576 FP8 keys: 547 us, 3,950 GB/s (58 %): the converters' chain (a tile
+//     takes each of their warps 1,700 clocks of 1,900) and the shared memory's bandwidth (TMA
+//     writes, conversion, both products' operands: 1,800 clocks a tile).
+//   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
+//     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and 2.5 more that
+//     pass between two items.
+//   one token over 2,048 keys: 14 us, a chain of latencies (share, page, Q and K, two products,
+//     partials, merge) with 1.2 us of bytes in it.
+//
 //   S_i = Q_i K^T (M = N = 128, K = D), P over S_i (each 32 columns' P in the first 16),
 //   O_i += P V.
 // Each stream issues P V (tile t) and right behind it Q K^T (its next tile): S_i full then
@@ -78,7 +98,8 @@ constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run
 // The schedule's units are tenths of the time of a key tile of a two-tile item.  Key tiles of
 // one-tile items, bf16 (their bytes bound it) | FP8, few rows | FP8, more rows; and what an item
 // costs beside its tiles (the pipeline runs empty between two items, results leave); and the
-// least a share is worth cutting for.
+// least a share is worth cutting for.  With equal tiles for every CTA, whatever their items, CTAs
+// took 296,000 to 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.
 constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsQuad8 = 5, kUnitsOne8 = 6, kUnitsItem = 25, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -133,7 +154,8 @@ struct Cfg {
                 "register split");
   // Scores a thread holds at a time.  bf16: the whole row of the tile.  FP8: 32, read from TMEM
   // once for the maximum and again for P: the unrolled body beside the converters' did not
-  // fit the instruction cache (3.3 of 10 stall cycles were instruction fetches).
+  // fit the instruction cache (3.3 of 10 stall cycles were instruction fetches; 64 at a time,
+  // with the registers for it: one token over 1M keys 547 -> 621 us).
   static constexpr int kPart = FP8 ? 32 : 128;
   static constexpr uint32_t oQ = 0;
   static constexpr uint32_t oRing = oQ + 2 * kTile;
