@@ -100,7 +100,7 @@ constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run
 // costs beside its tiles (the pipeline runs empty between two items, results leave); and the
 // least a share is worth cutting for.  With equal tiles for every CTA, whatever their items, CTAs
 // took 296,000 to 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.
-constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsQuad8 = 5, kUnitsOne8 = 6, kUnitsItem = 25, kUnitsMin = 24;
+constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsQuad8 = 5, kUnitsOne8 = 6, kUnitsItem = 20, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -1296,54 +1296,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
 #pragma unroll
             for (int q = 0; q < 16; q += 2) finite = ffma2(make_float2(x[q], x[q + 1]), make_float2(0.f, 0.f), finite);
           };
-          if (whole) {
-            const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
-            constexpr int kCols = 32;
-            long long to[4];                          // rows of the lane's quad (-1: no such row)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(kFull, mine_row, (lane & ~3) + x);
+          const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
+          const long long to0 = __shfl_sync(kFull, mine_row, lane & ~1), to1 = __shfl_sync(kFull, mine_row, lane | 1);
+          float4 *dst = reinterpret_cast<float4 *>(a.part) + static_cast<size_t>(slot) * (D / 4) * a.part_rows + prow;
 #pragma unroll 1
-            for (int c = 0; c < D; c += kCols) {
-              uint4 y[kCols / 8];
+          for (int c = 0; c < D; c += 16) {
+            float x[16];
+            columns(c, x);
+            if (c + 16 == D) release();               // the next item's P V need not wait for the stores
+            if (whole) {
+              uint4 y0 = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                    pack_bf16x2(x[6], x[7]));
+              uint4 y1 = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                                    pack_bf16x2(x[14], x[15]));
+              // two lanes exchange halves: each store then covers whole sectors of a row (-1: none)
+              swap4(y0, y1, lane & 1, 1);
+              if (to0 >= 0) *reinterpret_cast<uint4 *>(a.out + to0 * D + c + 8 * (lane & 1)) = y0;
+              if (to1 >= 0) *reinterpret_cast<uint4 *>(a.out + to1 * D + c + 8 * (lane & 1)) = y1;
+            } else if (row_ok) {
 #pragma unroll
-              for (int q = 0; q < kCols / 16; ++q) {
-                float x[16];
-                columns(c + 16 * q, x);
-                y[2 * q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                      pack_bf16x2(x[6], x[7]));
-                y[2 * q + 1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]),
-                                          pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
-              }
-              if (c + kCols == D) release();             // the next item's P V need not wait for the stores
-              // 4 x 4 transposes of 16-byte pieces over four lanes: store x then covers 64
-              // contiguous bytes of row x of the quad instead of 16 bytes of every row
-#pragma unroll
-              for (int h = 0; h < kCols / 8; h += 4) {
-                swap4(y[h], y[h + 1], lane & 1, 1);
-                swap4(y[h + 2], y[h + 3], lane & 1, 1);
-                swap4(y[h], y[h + 2], lane & 2, 2);
-                swap4(y[h + 1], y[h + 3], lane & 2, 2);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  if (to[x] >= 0)
-                    *reinterpret_cast<uint4 *>(a.out + to[x] * D + c + 8 * h + 8 * (lane & 3)) = y[h + x];
-              }
+              for (int q = 0; q < 4; ++q)
+                dst[static_cast<size_t>(c / 4 + q) * a.part_rows] =
+                    make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             }
-          } else {
-            float4 *dst = reinterpret_cast<float4 *>(a.part) + static_cast<size_t>(slot) * (D / 4) * a.part_rows + prow;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float x[16];
-              columns(c, x);
-              if (row_ok) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  dst[static_cast<size_t>(q) * a.part_rows] =
-                      make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-              }
-              dst += static_cast<size_t>(4) * a.part_rows;
-            }
-            release();
           }
           uint32_t todo = __ballot_sync(kFull, row_ok && finite.x + finite.y != 0.f);
           __syncwarp();                               // the stores above come before the repairs
