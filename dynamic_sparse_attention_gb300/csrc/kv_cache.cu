@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheReadArgs a
   const long long t0 = static_cast<long long>(blockIdx.x) * kReadTok;
   grid_dep_wait();
   const int kv = a.kv_len[b];
-  const long long cap = min(static_cast<long long>(a.max_pages) * a.page_size, static_cast<long long>(a.T_max));
-  DSA_CHECK(kv >= 0 && kv <= cap);
+  const long long held = static_cast<long long>(a.max_pages) * a.page_size;
+  DSA_CHECK(kv >= 0 && kv <= held);
+  const long long cap = min(held, static_cast<long long>(a.T_max));
   const long long end = min(max(static_cast<long long>(kv), 0ll), cap);
   if (t0 >= end) return;
   const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + t0 / a.page_size];

@@ -66,9 +66,9 @@
 //
 // Keys that no row of the item sees (behind the sequence, before the window, bad pages) have
 // their value rows zeroed, so whatever the pages hold there cannot reach the sums as 0 * NaN.
-// Where some rows of an item see a key and others do not, an infinity or NaN in its value row
-// does reach the others' sums that way; the epilogue finds such rows by their results and
-// computes the columns again from the keys that they see (repair_row).
+// Where some rows of an item see a key and others do not (tiles at the diagonal, at a window's
+// edge), infinities and NaN in its value row are taken out as well, and the epilogue adds them to
+// the rows that do see the key (add_lost).  Such tiles are searched for them as they arrive.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -124,6 +124,7 @@ struct alignas(16) Item {
   int flags;           // kSingle ...
 };
 constexpr int kItems = 4;      // pieces handed out ahead
+constexpr int kLostRing = 2 * kItems;   // (an entry is cleared when its item before has left the epilogue)
 constexpr int kSingle = 1;     // one query tile: both streams take turns over the key tiles
 constexpr int kHasKeys = 2;    // some row sees a key
 constexpr int kWhole = 4;      // every tile of the item: the result is final
@@ -173,8 +174,9 @@ struct Cfg {
   // [stream][half]); and the warps' maxima [stream][2][4 warps][32 rows]
   static constexpr bool kShare = FP8;
   static constexpr uint32_t oP = oQ + kTile;
-  static constexpr uint32_t oMax = D == 128 ? oP + 4 * kQuadTile : oMisc + 16;
-  static constexpr uint32_t kBytes = oMisc + 16 + (kShare && D != 128 ? 2048 : 0);
+  static constexpr uint32_t oLost = oMisc + 16;             // by item: something was taken out of its values
+  static constexpr uint32_t oMax = D == 128 ? oP + 4 * kQuadTile : oLost + 4 * kLostRing;
+  static constexpr uint32_t kBytes = oLost + 4 * kLostRing + (kShare && D != 128 ? 2048 : 0);
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -184,9 +186,7 @@ struct Cfg {
 struct Args {
   CUtensorMap tq, tk, tv;
   CUtensorMap tq4;       // kQuad items' query rows
-  const uint16_t *q;     // for repair_row, with the pages
-  long long q_stride;
-  const void *k_pages, *v_pages;
+  const void *v_pages;   // for add_lost
   const int32_t *q_start, *kv_len, *page_table;
   const uint8_t *k_scale, *v_scale;
   uint16_t *out;
@@ -481,100 +481,54 @@ __device__ __forceinline__ void swap4(uint4 &x, uint4 &y, int up, int mask) {
   else y = t;
 }
 
-// ------------------------------------------------------------------ rows with infinities or NaN
+// ------------------------------------------------------------------ infinities and NaN
 
-// 8 consecutive elements of a cached row (pieces of 8, `scale` of the row for FP8) as floats
-template <bool FP8>
-__device__ __forceinline__ void cached8(const void *pages, size_t at, uint32_t scale, float *x) {
-  if constexpr (FP8) {
-    const float f = __uint_as_float(scale == 255u ? 0x7fffffffu : scale << 23);
-    const uint2 c = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + at);
-    f16x2_to_f32x2(e4m3x2_to_f16x2(c.x), x[0], x[1]);
-    f16x2_to_f32x2(e4m3x2_to_f16x2(c.x >> 16), x[2], x[3]);
-    f16x2_to_f32x2(e4m3x2_to_f16x2(c.y), x[4], x[5]);
-    f16x2_to_f32x2(e4m3x2_to_f16x2(c.y >> 16), x[6], x[7]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= f;
-  } else {
-    unpack16(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(pages) + at), x, uint16_t());
-  }
+// Every row of the item sees every key of the tile that begins at `base` (bad pages aside).
+__device__ __forceinline__ bool seen_by_all(const Args &a, const Item &it, int base) {
+  return base + kKeys - 1 <= it.p0 &&
+         (a.n_stream < 0 || base > it.p_hi - a.n_stream || base + kKeys <= a.n_sink);
 }
 
-// One row (a warp) whose O over a piece is not finite: the columns into which only value rows
-// that the row does not see can have carried an infinity or NaN are computed again, in fp32,
-// from the keys that it sees; x[0..8) of lane c < D / 8 are columns 8 c .. of the sum over the
-// piece of exp2(sl2 q . k - m) v, and the return value has bit i set if x[i] is to be used.
-// Such keys lie in tiles that not every row of the item sees alike: only those are searched,
-// and where the row itself sees an infinity or NaN its own result stands.
-template <int D, bool FP8>
-__device__ __forceinline__ uint32_t repair_row(const Args &a, const Item &it, int tok, int head, float m, float *x) {
+// 16-bit halves of `w` that are infinite or NaN in bf16 as masks
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); }
+
+// What was taken out of a value tile (see the cleaner and the converters) goes to those of the
+// warp's n_rows rows, from row `first` of stream i's query tile on, that see it: their weight is
+// positive, so an infinity stays one of its sign, and opposite ones or a NaN make a NaN.
+// add(row - first, token, column, value) adds to a row's result or partial; a column's lane is
+// the same for every key.
+template <int D, bool FP8, class Add>
+__device__ __forceinline__ void add_lost(const Args &a, const Item &it, int first, int n_rows, int i, Add add) {
   const int lane = threadIdx.x & 31;
-  const int p = it.p0 + tok;
   const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
-  auto sees = [&](int j) { return j <= p && (a.n_stream < 0 || j > p - a.n_stream || j < a.n_sink); };
-  // row of key j in the cache (-1: none; only keys up to the item's last position have a page)
-  auto row_of = [&](int j) -> long long {
-    if (j > it.p_hi) return -1;
-    const int page = table[j >> a.lg_page];
-    if (page < 0 || page >= a.n_pages) return -1;
-    return ((static_cast<long long>(page) << a.lg_page) + (j & (a.page_size - 1))) * a.H_kv + it.g;
-  };
-  const int col = (lane % (D / 8)) * 8;
-  uint32_t own = 0, others = 0;   // columns with an infinity or NaN in seen, in unseen rows
+  const int col = (lane % (D / 4)) * 4;
 #pragma unroll 1
   for (int k = 0; k < it.T; ++k) {
-    const int t = it.t0 + k, base = (t < it.ns ? t : it.w0 + t - it.ns) * kKeys;
-    if (base + kKeys - 1 <= it.p0 && (a.n_stream < 0 || base >= it.p_hi - a.n_stream + 1)) continue;   // seen by all
+    const int base = tile_base(it, k);
+    if (seen_by_all(a, it, base)) continue;
 #pragma unroll 1
-    for (int j = base; j < base + kKeys; ++j) {
-      const long long r = row_of(j);
-      if (r < 0) continue;
-      cached8<FP8>(a.v_pages, static_cast<size_t>(r) * D + col, FP8 ? a.v_scale[r] : 0u, x);
-      uint32_t bad = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) bad |= (x[i] - x[i] == 0.f ? 0u : 1u) << i;
-      if (sees(j)) own |= bad;
-      else others |= bad;
-    }
-  }
-  const uint32_t redo = others & ~own;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (!__any_sync(kFull, redo)) return 0;
-  const uint16_t *q = a.q + (it.tok0 + tok) * a.q_stride + static_cast<size_t>(head) * D;
+    for (int j = base; j < min(base + kKeys, it.p_hi + 1); ++j) {
+      const int page = table[j >> a.lg_page];
+      if (page < 0 || page >= a.n_pages) continue;
+      const size_t r = ((static_cast<size_t>(page) << a.lg_page) + (j & (a.page_size - 1))) * a.H_kv + it.g;
+      uint2 v;
+      if constexpr (FP8) v.x = v.y = a.v_scale[r] == 255 ? 0x7fff7fffu : 0u;
+      else v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.v_pages) + r * D + col);
+      const uint32_t b0 = not_finite(v.x), b1 = not_finite(v.y);
+      if (!__any_sync(kFull, b0 | b1)) continue;
 #pragma unroll 1
-  for (int k = 0; k < it.T; ++k) {
-    const int t = it.t0 + k, base = (t < it.ns ? t : it.w0 + t - it.ns) * kKeys;
-#pragma unroll 1
-    for (int j0 = base; j0 < base + kKeys; j0 += 32) {
-      const int j = j0 + lane;   // a key per lane: its weight
-      const long long r = sees(j) ? row_of(j) : -1;
-      float w = 0.f;
-      if (r >= 0) {
-        float s = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 8) {
-          float kx[8], qx[8];
-          cached8<FP8>(a.k_pages, static_cast<size_t>(r) * D + c, FP8 ? a.k_scale[r] : 0u, kx);
-          unpack16(*reinterpret_cast<const uint4 *>(q + c), qx, uint16_t());
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s = fmaf(qx[i], kx[i], s);
-        }
-        w = fast_exp2(s * a.sl2 - m);
-      }
-#pragma unroll 1
-      for (int y = 0; y < 32; ++y) {
-        const long long ry = __shfl_sync(kFull, r, y);
-        const float wy = __shfl_sync(kFull, w, y);
-        if (ry < 0) continue;
-        float vx[8];
-        cached8<FP8>(a.v_pages, static_cast<size_t>(ry) * D + col, FP8 ? a.v_scale[ry] : 0u, vx);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(wy, vx[i], x[i]);
+      for (int row = 0; row < n_rows; ++row) {
+        const int tok = (first + row) / a.G + i * a.TT, p = it.p0 + tok;
+        if ((first + row) / a.G >= a.TT || tok >= it.ntok) continue;
+        if (j > p || !(a.n_stream < 0 || j > p - a.n_stream || j < a.n_sink)) continue;
+        if (lane >= D / 4) continue;
+        if (b0 & 0xffffu) add(row, tok, col, bf16_lo(v.x));
+        if (b0 >> 16) add(row, tok, col + 1, bf16_hi(v.x));
+        if (b1 & 0xffffu) add(row, tok, col + 2, bf16_lo(v.y));
+        if (b1 >> 16) add(row, tok, col + 3, bf16_hi(v.y));
       }
     }
   }
-  return redo;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -766,11 +720,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Item *items = reinterpret_cast<Item *>(sm + C::oItem);
+  volatile int *lost = reinterpret_cast<volatile int *>(sm + C::oLost);
   // Readers of the item ring: the next piece into `it` (a copy), false at the end
   Ring<kItems> ri;
+  int lost_at = 0;                                    // the piece's entry of `lost`
   auto next_item = [&](Item &it) -> bool {
     if (!warp_wait(&item_full[ri.slot], ri.phase, abort)) return false;
     it = items[ri.slot];
+    lost_at = ri.slot + (ri.phase ? kItems : 0);
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[ri.slot]);
     ri.step();
@@ -985,6 +942,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                                        (start ? kStart : 0) | (w.e.ntok <= a.TT4 ? kQuad : 0);
       if (lane == 0) {
         items[ri.slot] = it;
+        lost[ri.slot + (ri.phase ? kItems : 0)] = 0;
         mbar_arrive(&item_full[ri.slot]);
         if (w.valid && start && !whole) {             // a cut item, described for the merge where it begins
           PagedPiece d;
@@ -1173,7 +1131,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           if (quad) {
             // P in shared memory; the tile's rows behind kQuadRows are whatever lies there, their
             // O is not read
-#pragma unroll
+#pragma unroll 2
             for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
               mma_ss(leader, o_tm, dp + (kk >> 2) * (kQuadTile >> 4) + (kk & 3) * 2, bd + kk * 128, id_pv,
                      kk > 0 ? 1u : acc);
@@ -1274,7 +1232,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         } else {
           const uint32_t o_col = o_base + i * D;
           // 16 columns of O (the streams' halves merged, normalised if the result is final)
-          float2 finite = make_float2(0.f, 0.f);      // NaN once a column of the row is not finite
           auto columns = [&](int c, float *x) {
             uint32_t o[16];
             if (keys) tmem_ld16(o_col + c, o);
@@ -1293,8 +1250,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 for (int q = 0; q < 16; ++q) x[q] = fmaf(__uint_as_float(o[q]), g1, x[q]);
               }
             }
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) finite = ffma2(make_float2(x[q], x[q + 1]), make_float2(0.f, 0.f), finite);
           };
           const long long mine_row = row_ok ? static_cast<long long>(orow) : -1ll;
           const long long to0 = __shfl_sync(kFull, mine_row, lane & ~1), to1 = __shfl_sync(kFull, mine_row, lane | 1);
@@ -1320,26 +1275,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                     make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             }
           }
-          uint32_t todo = __ballot_sync(kFull, row_ok && finite.x + finite.y != 0.f);
-          __syncwarp();                               // the stores above come before the repairs
-          while (todo) {                              // rare: see repair_row
-            const int src = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const float mr = __shfl_sync(kFull, m, src), ir = __shfl_sync(kFull, inv, src);
-            const int r = (warp & 3) * 32 + src, rt = r / a.G + i * a.TT, rh = it.g * a.G + r % a.G;
-            float x[8];
-            const uint32_t redo = repair_row<D, FP8>(a, it, rt, rh, mr == -INFINITY ? 0.f : mr, x);
-            if (lane >= D / 8) continue;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (!((redo >> q) & 1u)) continue;
-              const int c = 8 * lane + q;
-              if (whole)
-                a.out[(static_cast<size_t>(it.tok0 + rt) * a.H_q + rh) * D + c] =
-                    static_cast<uint16_t>(pack_bf16x2(x[q] * ir, 0.f));
-              else
-                a.part[((static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + i * kRows + r) * 4 + (c & 3)] = x[q];
-            }
+          if (keys && lost[lost_at]) {                // rare
+            __syncwarp();                             // the stores above come first
+            const int first = (warp & 3) * 32;
+            add_lost<D, FP8>(a, it, first, 32, i, [&](int r, int tok, int c, float v) {
+              if (whole) {
+                uint16_t *o = a.out + (static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + (first + r) % a.G) * D + c;
+                *o = static_cast<uint16_t>(pack_bf16x2(bf16_lo(*o) + v, 0.f));
+              } else {
+                a.part[((static_cast<size_t>(slot) * (D / 4) + c / 4) * a.part_rows + i * kRows + first + r) * 4 + (c & 3)] += v;
+              }
+            });
           }
           if (row_ok) {
             if (!whole)
@@ -1373,7 +1319,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       auto convert = [&](int k, uint32_t sb_raw) -> bool {
         if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
         const TileMeta *md = &meta[(tile + k) % kMetaRing];
-        const bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
+        bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
+        if (values && seen && sb_raw == 255 && !seen_by_all(a, it, tile_base(it, k))) {
+          seen = false;                               // a row of NaN that not every row sees: see add_lost
+          lost[lost_at] = 1;
+        }
         const int sb = seen ? static_cast<int>(sb_raw) : 127;
         // 2^e as 2^(120 + e) on the raw bits (scales above 2^7: see below); a row that is not
         // seen is multiplied by 0, one with a NaN scale (255) by NaN
@@ -1485,6 +1435,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           if (k < 0 || k >= it.T) continue;
           if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
           if (value) {
+            unsigned char *v = sm + C::oRing + rp.slot * C::kTile;
             const uint4 s4 = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
             if ((s4.x & s4.y & s4.z & s4.w) != 0xffffffffu) {
               const int at = lane >> 3;               // eight lanes per 128-byte row
@@ -1497,11 +1448,32 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                   if (!((sw >> (r + at)) & 1u))
 #pragma unroll
                     for (int hh = 0; hh < C::kHalves; ++hh)
-                      *reinterpret_cast<uint4 *>(sm + C::oRing + rp.slot * C::kTile + hh * C::kHalf +
-                                                 (r0 + r + at) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                      *reinterpret_cast<uint4 *>(v + hh * C::kHalf + (r0 + r + at) * 128 + (lane & 7) * 16) =
+                          make_uint4(0, 0, 0, 0);
               }
               fence_proxy_async_smem();
               __syncwarp();
+            }
+            if (!seen_by_all(a, it, tile_base(it, k))) {
+              uint4 *w = reinterpret_cast<uint4 *>(v);
+              constexpr uint32_t kMag = 0x7fff7fffu;
+              uint32_t m = 0;                         // largest magnitudes of both halves
+#pragma unroll 4
+              for (uint32_t x = lane; x < C::kTile / 16; x += 32) {
+                const uint4 u = w[x];
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(u.x & kMag, u.y & kMag), __vmaxu2(u.z & kMag, u.w & kMag)));
+              }
+              if (__any_sync(kFull, not_finite(m))) {   // rare
+#pragma unroll 1
+                for (uint32_t x = lane; x < C::kTile / 16; x += 32) {
+                  const uint4 u = w[x];
+                  w[x] = make_uint4(u.x & ~not_finite(u.x), u.y & ~not_finite(u.y), u.z & ~not_finite(u.z),
+                                    u.w & ~not_finite(u.w));
+                }
+                lost[lost_at] = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
             }
             if (lane == 0) mbar_arrive(&clean[rc.slot]);
             rc.step();
@@ -1743,9 +1715,6 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.TT4 = C::kShare ? kQuadRows / G : 0;
   if (!maps || (a.TT4 > 0 && !make_query_map(&a.tq4, pa.q, D, pa.H_q, pa.q_stride, pa.n_tok, G, a.TT4)))
     return cudaErrorInvalidValue;
-  a.q = static_cast<const uint16_t *>(pa.q);
-  a.q_stride = pa.q_stride;
-  a.k_pages = pa.k_pages;
   a.v_pages = pa.v_pages;
   a.q_start = pa.q_start;
   a.kv_len = pa.kv_len;

@@ -47,6 +47,9 @@ def main():
         out, *codes = run()
         assert codes == [0, 0, 0], codes
         assert torch.isfinite(out.float()).all()
+        dsa.kv_cache_read(cache, lens, table, T_max=70)   # shorter than the sequences: no error
+        torch.cuda.synchronize()
+        assert dsa.device_error() == 0
         bad = table.clone()
         bad[0, 2] = 8                      # past the cache: the chunk's own page and keys
         bad[1, 1] = -1

@@ -254,6 +254,25 @@ def test_nan_recomputed_across_shares():
         b.check(*b.attn())
 
 
+def test_nan_in_every_item_of_a_long_context():
+    """Token 64 m + 40 of a chunk holds a NaN (an infinity) in column m of its value row: rows
+    from it on have it, the 40 tokens before it that share its tiles have a finite result, and
+    the launch stays far inside the limit of its waits."""
+    n, t = 8192, 65536
+    b = Batch([(n, t)], 4, 1, 128, 128, False, seed=52)
+    for m in range(128):
+        b.v[0][t - n + 64 * m + 40, 0, m] = float("nan") if m % 2 else float("inf")
+    b.write()
+    out, lse = b.attn()
+    torch.cuda.synchronize()
+    row, col = torch.arange(n, device="cuda")[:, None], torch.arange(128, device="cuda")[None]
+    hit = (row >= 64 * col + 40)[:, None].expand(n, 4, 128)
+    odd = (col % 2 == 1)[:, None].expand(n, 4, 128)
+    assert torch.equal(torch.isnan(out), hit & odd)
+    assert torch.equal(torch.isposinf(out), hit & ~odd)
+    assert torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("group", [1, 3, 4, 5, 32, 33])
