@@ -514,18 +514,18 @@ __device__ __forceinline__ void add_lost(const Args &a, const Item &it, int firs
       uint2 v;
       if constexpr (FP8) v.x = v.y = a.v_scale[r] == 255 ? 0x7fff7fffu : 0u;
       else v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.v_pages) + r * D + col);
-      const uint32_t b0 = not_finite(v.x), b1 = not_finite(v.y);
-      if (!__any_sync(kFull, b0 | b1)) continue;
+      if (!__any_sync(kFull, not_finite(v.x) | not_finite(v.y))) continue;
 #pragma unroll 1
       for (int row = 0; row < n_rows; ++row) {
         const int tok = (first + row) / a.G + i * a.TT, p = it.p0 + tok;
         if ((first + row) / a.G >= a.TT || tok >= it.ntok) continue;
         if (j > p || !(a.n_stream < 0 || j > p - a.n_stream || j < a.n_sink)) continue;
         if (lane >= D / 4) continue;
-        if (b0 & 0xffffu) add(row, tok, col, bf16_lo(v.x));
-        if (b0 >> 16) add(row, tok, col + 1, bf16_hi(v.x));
-        if (b1 & 0xffffu) add(row, tok, col + 2, bf16_lo(v.y));
-        if (b1 >> 16) add(row, tok, col + 3, bf16_hi(v.y));
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x = (q < 2 ? v.x : v.y) >> (16 * (q & 1));
+          if (not_finite(x) & 0xffffu) add(row, tok, col + q, bf16_lo(x));
+        }
       }
     }
   }
@@ -1319,11 +1319,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       auto convert = [&](int k, uint32_t sb_raw) -> bool {
         if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
         const TileMeta *md = &meta[(tile + k) % kMetaRing];
-        bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
-        if (values && seen && sb_raw == 255 && !seen_by_all(a, it, tile_base(it, k))) {
-          seen = false;                               // a row of NaN that not every row sees: see add_lost
-          lost[lost_at] = 1;
-        }
+        const bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
         const int sb = seen ? static_cast<int>(sb_raw) : 127;
         // 2^e as 2^(120 + e) on the raw bits (scales above 2^7: see below); a row that is not
         // seen is multiplied by 0, one with a NaN scale (255) by NaN
@@ -1353,13 +1349,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             put(2 * (p0 + p) + 1, make_uint4(y2.x, y2.y, y3.x, y3.y));
           }
         }
-        if (__any_sync(kFull, seen && e2 > 0 && sb != 255)) {
-          // rare: a scale above 2^7 takes a second exact multiply
+        if (__any_sync(kFull, seen && e2 > 0)) {
+          // rare: a scale above 2^7 takes a second exact multiply, and values of NaN (255) that
+          // not every row of the item sees are taken out (see add_lost)
           const uint32_t f2 = (static_cast<uint32_t>(e2 + 127) << 7) * 0x00010001u;
+          const bool again = seen && e2 > 0 && sb != 255;
+          const bool out = values && seen && sb == 255 && !seen_by_all(a, it, tile_base(it, k));
+          if (out) lost[lost_at] = 1;
 #pragma unroll 1
-          for (int q = 0; seen && e2 > 0 && sb != 255 && q < D / 8; ++q) {
+          for (int q = 0; (again || out) && q < D / 8; ++q) {
             uint4 *o = reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4));
-            *o = make_uint4(mul_bf16x2(o->x, f2), mul_bf16x2(o->y, f2), mul_bf16x2(o->z, f2), mul_bf16x2(o->w, f2));
+            *o = out ? make_uint4(0u, 0u, 0u, 0u)
+                     : make_uint4(mul_bf16x2(o->x, f2), mul_bf16x2(o->y, f2), mul_bf16x2(o->z, f2), mul_bf16x2(o->w, f2));
           }
         }
         fence_proxy_async_smem();
