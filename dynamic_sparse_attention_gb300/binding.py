@@ -769,6 +769,7 @@ class PagedKVCache:
         return _is_fp8(self.k)
 
 
+_MAX_KEYS = 1 << 30   # of a sequence: larger windows see no more
 _FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
 
 # Every decode step makes these calls, and a small one is over on the GPU in a few
@@ -855,6 +856,8 @@ class _on:
     that outputs and workspaces are allocated and a call is enqueued on."""
 
     def __init__(self, dev, stream):
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"stream is on device {stream.device_index}, the cache on device {dev}")
         self.device_ctx = torch.cuda.device(dev)
         self.stream = stream
 
@@ -952,6 +955,8 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
         n_stream = -1
     elif n_stream < 0:
         raise ValueError("n_stream must be >= 0, or None for every key")
+    if n_sink > _MAX_KEYS or n_stream > _MAX_KEYS:
+        n_sink, n_stream = min(n_sink, _MAX_KEYS), min(n_stream, _MAX_KEYS)
     shape, nbytes = _paged_shape(B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D, dtype)
     device = q.device
     if out is None:

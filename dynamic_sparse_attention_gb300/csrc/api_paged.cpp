@@ -50,6 +50,39 @@ int check_stride(const char *name, long long stride, int heads, int D) {
   return DSA_OK;
 }
 
+// a range of device memory
+struct Span {
+  const char *name;
+  const void *p;
+  long long n;
+};
+
+// each of `outs` is apart from the others and from every one of `ins`
+template <int N, int M>
+int check_apart(const Span (&outs)[N], const Span (&ins)[M]) {
+  auto apart = [](const Span &x, const Span &y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return !x.p || !y.p || (a < b ? static_cast<unsigned long long>(x.n) <= b - a
+                                  : static_cast<unsigned long long>(y.n) <= a - b);
+  };
+  for (int i = 0; i < N; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (!apart(outs[i], outs[j]))
+        return fail(DSA_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, outs[j].name);
+    for (int j = 0; j < M; ++j)
+      if (!apart(outs[i], ins[j])) return fail(DSA_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, ins[j].name);
+  }
+  return DSA_OK;
+}
+
+long long token_bytes(const dsa_paged_shape *s, long long stride, int heads) {
+  return ((s->n_tok - 1) * stride + static_cast<long long>(heads) * s->D) * 2;
+}
+
+long long page_bytes(const dsa_paged_shape *s) {
+  return static_cast<long long>(s->n_pages) * s->page_size * s->H_kv * s->D * (s->dtype == DSA_BF16_FP8KV ? 1 : 2);
+}
+
 struct PagedWs {
   float *part, *part_ml;
   PagedPiece *piece;
@@ -89,6 +122,10 @@ int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, lon
   if (shape->n_tok == 0) return DSA_OK;
   if (!aligned(k_new, 16) || !aligned(v_new, 16))
     return fail(DSA_ERR_ALIGNMENT, "k_new and v_new must be non-NULL and 16-byte aligned");
+  const Span outs[] = {{"k_pages", k_pages, page_bytes(shape)}, {"v_pages", v_pages, page_bytes(shape)}};
+  const Span ins[] = {{"k_new", k_new, token_bytes(shape, k_stride, shape->H_kv)},
+                      {"v_new", v_new, token_bytes(shape, v_stride, shape->H_kv)}};
+  if ((st = check_apart(outs, ins))) return st;
   CacheWriteArgs a{};
   a.k_new = static_cast<const uint16_t *>(k_new);
   a.v_new = static_cast<const uint16_t *>(v_new);
@@ -124,6 +161,10 @@ int kv_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_sca
   if (T_max < 1) return fail(DSA_ERR_INVALID_ARG, "T_max=%d < 1", T_max);
   if (!aligned(k_out, 16) || !aligned(v_out, 16))
     return fail(DSA_ERR_ALIGNMENT, "k_out and v_out must be non-NULL and 16-byte aligned");
+  const long long rows = static_cast<long long>(shape->B) * T_max * shape->H_kv * shape->D * 2;
+  const Span outs[] = {{"k_out", k_out, rows}, {"v_out", v_out, rows}};
+  const Span ins[] = {{"k_pages", k_pages, page_bytes(shape)}, {"v_pages", v_pages, page_bytes(shape)}};
+  if ((st = check_apart(outs, ins))) return st;
   CacheReadArgs a{};
   a.k_pages = k_pages;
   a.v_pages = v_pages;
@@ -176,6 +217,12 @@ int paged_attn(const void *q, long long q_stride, const void *k_pages, const voi
   const size_t need = paged_layout(shape, nullptr).bytes;
   if (ws_bytes < need || !aligned(ws, 16))
     return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) needed, got %zu", need, ws_bytes);
+  const long long rows = static_cast<long long>(shape->n_tok) * shape->H_q;
+  const Span outs[] = {{"out", out, rows * shape->D * 2}, {"lse", lse, rows * 4}, {"workspace", ws, static_cast<long long>(need)}};
+  const Span ins[] = {{"q", q, token_bytes(shape, q_stride, shape->H_q)},
+                      {"k_pages", k_pages, page_bytes(shape)},
+                      {"v_pages", v_pages, page_bytes(shape)}};
+  if ((st = check_apart(outs, ins))) return st;
   if ((st = paged_attn_ready())) return st;
   const PagedWs w = paged_layout(shape, ws);
   PagedAttnArgs a{};

@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
             m = m0 + l;
             base += __shfl_sync(kFull, v - own, l);
             item = __shfl_sync(kFull, item, l);
-            g = static_cast<int>(static_cast<uint32_t>(u0 - base) / item);   // below 2^31 units an entry
+            for (int x = 64; x > 0; x >>= 1)            // (u0 - base) / item, below H_kv <= 128
+              if (static_cast<long long>(item) * (g + x) <= u0 - base) g += x;
             base += static_cast<long long>(item) * g;
             break;
           }
@@ -1682,14 +1683,14 @@ bool make_query_map(CUtensorMap *m, const void *base, int D, int H, long long st
 // a build that holds less would wait for registers that no warp gives back).  Asked once per
 // device: the three calls took 1.2 us of each launch.
 template <int D, bool FP8, class Kern>
-cudaError_t prepare(Kern kern, int &sms) {
+cudaError_t prepare(Kern kern, int &sms, bool again = false) {
   using C = Cfg<D, FP8>;
   static std::atomic<int> known[64];                  // SMs by device, 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool keep = dev >= 0 && dev < 64;
-  if (keep && (sms = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  if (keep && !again && (sms = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;
@@ -1752,9 +1753,13 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   const long long pairs = pa.B + pa.n_tok / (2 * TT);
   const long long most = pairs * pa.H_kv * (kUnitsTwo * ((cap + kKeys - 1) / kKeys + 1) + kUnitsItem) / kUnitsMin + 1;
   const int P = static_cast<int>(std::min(static_cast<long long>(std::min(sms, kPagedMaxCtas)), most));
-  {
+  for (int turn = 0; turn < 2; ++turn) {
     ProfScope ps(FP8 ? "paged_attn_fp8" : "paged_attn", s);
     e = launch_pdl(kern, dim3(P), dim3(C::kThreads), C::kBytes, s, a);
+    if (e != cudaErrorInvalidValue || turn) break;
+    // a context that was torn down and made again has forgotten the shared memory's limit
+    cudaGetLastError();
+    if ((e = prepare<D, FP8>(kern, sms, true)) != cudaSuccess) break;
   }
   if (e != cudaSuccess) return e;
   MergeArgs ma;

@@ -426,7 +426,9 @@ int sparse_attn_prefill(const void *q, const void *k, const void *v,
  * Bad device data is not dereferenced: lengths are clamped, rows whose position is negative
  * are not written (cache write) or see no key (attention), and positions whose page lies
  * outside [0, n_pages) are skipped.  One page may serve several sequences (a shared prefix),
- * but a page that a call writes must belong to one. */
+ * but a page that a call writes must stand in the table once (its rows else have two
+ * writers).  Outputs, pages that are written and the workspace overlap neither each other nor an
+ * input (INVALID_ARG). */
 typedef struct {
   int B, n_tok, max_pages, n_pages, page_size;
   int H_q, H_kv, D;
@@ -439,7 +441,8 @@ typedef struct {
  * takes each (token, head) row with a = its largest finite magnitude as codes of x * 2^-e
  * (nearest, ties to even, saturating at 448), e the smallest integer with a * 2^-e <= 448,
  * kept in [-116, 119] (0 for a row of zeros), and stores s = e + 127, or s = 255 if the row
- * holds a NaN.  Every value the cache then stands for is exactly a bf16.  shape->H_q is not used but checked.
+ * holds a NaN.  Every value the cache then stands for is exactly a bf16.  shape->H_q is not
+ * used but checked.
  * Errors: INVALID_ARG / UNSUPPORTED (shape, strides), ALIGNMENT, CUDA. */
 int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, long long v_stride,
                    const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
@@ -469,8 +472,8 @@ int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
  *   H_q * D); out [n_tok, H_q, D] bf16; lse [n_tok, H_q] fp32, natural log (NULL to skip);
  *   scale positive and finite.  A row that attends nothing gets out = 0, lse = -inf.
  * Nothing that the pages hold at positions no row of the call attends reaches a result.
- * Deterministic: the same call gives the same bits.  out must not overlap the inputs; two
- * calls (or two captured graphs) that may run at the same time need workspaces of their own.
+ * Deterministic: the same call gives the same bits.  Two calls (or two captured graphs) that may
+ * run at the same time need workspaces of their own.
  * The launches use programmatic dependent launch and wait for the stream's previous kernel
  * before they read anything.
  * Errors: INVALID_ARG / UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA; where a CTA's bounded waits ran
@@ -513,7 +516,8 @@ int dsa_profile_collect(dsa_kernel_stat *out, int max_out, int *n_out);
 int dsa_device_error(int *code);
 
 /* Sets the limit of those bounded waits to `ns` nanoseconds (0: back to the default of
- * half a second) for every later launch; it synchronises (cudaMemcpyToSymbol).  A test
+ * half a second) for every later launch (captured launches of the paged attention keep the
+ * one they were captured with); it synchronises (cudaMemcpyToSymbol).  A test
  * aid: a limit of a few nanoseconds makes the waits run out, so that the give-up path
  * (stop, drain, free, error word) can be exercised without any fault.  Not a
  * source-page operation. */

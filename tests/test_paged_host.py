@@ -72,6 +72,32 @@ def test_bad_pointers_and_strides_are_rejected(lib):
     assert _attn(lib, s, ws_bytes=100) == -3 and _attn(lib, s, ws=None) == -3
 
 
+def test_overlapping_memory_is_rejected(lib):
+    """Ranges that share a byte; the same arguments apart would go on to a launch."""
+    s = _shape()                                        # q and out: 8 tokens of 8 heads of 128, 16 KB
+    far = [OK + (i << 32) for i in range(8)]
+    call = lambda q=far[0], out=far[1], lse=far[2], ws=far[3], k=far[4], v=far[5]: lib.paged_attn(
+        q, 1024, k, v, None, None, OK, OK, OK, ctypes.byref(s), 0, -1, 0.1, out, lse, ws, 1 << 31, None)
+    names = lambda: lib.dsa_last_error().decode()
+    for kw, two in ((dict(out=far[0]), "out and q"), (dict(out=far[0] + 16384 - 16), "out and q"),
+                    (dict(lse=far[1] + 64), "lse and out"), (dict(ws=far[4] + 1024), "workspace and k_pages"),
+                    (dict(v=far[1] - 64 * 64 * 2 * 256 + 16), "out and v_pages"), (dict(ws=far[2]), "workspace and lse")):
+        assert call(**kw) == -1 and two in names(), (kw, names())
+    assert lib.kv_cache_write(far[0], far[1], 256, 256, OK, OK, OK, ctypes.byref(s), far[2], far[2] + 4096, None, None,
+                              None) == -1 and "v_pages and k_pages" in names()
+    assert lib.kv_cache_write(far[0], far[1], 256, 256, OK, OK, OK, ctypes.byref(s), far[2], far[1], None, None,
+                              None) == -1 and "v_pages and v_new" in names()
+    assert lib.kv_cache_read(far[0], far[1], None, None, OK, OK, ctypes.byref(s), 100, far[2], far[2], None) == -1
+    assert "v_out and k_out" in names()
+
+
+def test_stream_of_another_device():
+    class Other:
+        cuda_stream, device_index = 7, 3
+    with pytest.raises(ValueError, match="device 3"):
+        binding._on(0, Other())
+
+
 def test_nothing_to_do(lib):
     s = _shape(n_tok=0)
     assert _write(lib, s, k_new=None) == 0
