@@ -96,11 +96,11 @@ constexpr int kRows = 128;         // query rows per tile
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run at most 4 ahead)
 // The schedule's units are tenths of the time of a key tile of a two-tile item.  Key tiles of
-// one-tile items, bf16 (their bytes bound it) | FP8, few rows | FP8, more rows; and what an item
+// one-tile items, bf16 (their bytes bound it) | FP8; and what an item
 // costs beside its tiles (the pipeline runs empty between two items, results leave); and the
 // least a share is worth cutting for.  With equal tiles for every CTA, whatever their items, CTAs
 // took 296,000 to 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.
-constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsQuad8 = 5, kUnitsOne8 = 6, kUnitsItem = 20, kUnitsMin = 24;
+constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsOne8 = 6, kUnitsItem = 20, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -130,11 +130,10 @@ constexpr int kHasKeys = 2;    // some row sees a key
 constexpr int kWhole = 4;      // every tile of the item: the result is final
 constexpr int kStart = 8;      // the item's first tile
 constexpr int kEnd = 16;       // no piece: the share is done
-constexpr int kQuad = 32;      // at most kQuadRows rows, which all softmax warps share (FP8)
-constexpr int kQuadRows = 32;
-constexpr uint32_t kQuadTile = kQuadRows * 128;   // bytes of their P over 64 keys
+constexpr int kFewRows = 32;   // rows at most of a launch whose softmax warps share them (FEW)
+constexpr uint32_t kFewTile = kFewRows * 128;   // bytes of them over 64 dims, or of their P over 64 keys
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool FEW>
 struct Cfg {
   static constexpr int kHalves = D / 64;                    // 128-byte column blocks of a bf16 tile
   static constexpr uint32_t kHalf = kKeys * 128;            // bytes of one of them (128 rows)
@@ -149,8 +148,8 @@ struct Cfg {
   // registers a thread after the split by warpgroup (softmax x 2, warps 8-11, epilogue,
   // converters x 2); what the launch holds, threads x kRegLaunch, is what the shares add up to
   static constexpr int kRegLaunch = FP8 ? 80 : 128;
-  static constexpr int kRegSoft = FP8 ? 104 : 176, kRegMisc = FP8 ? 64 : 72, kRegEpi = FP8 ? 64 : 88,
-                       kRegConv = FP8 ? 72 : 0;
+  static constexpr int kRegSoft = FEW ? 80 : FP8 ? 104 : 176, kRegMisc = FP8 ? 64 : 72, kRegEpi = FP8 ? 64 : 88,
+                       kRegConv = FEW ? 96 : FP8 ? 72 : 0;
   static_assert(256 * kRegSoft + 128 * kRegMisc + 128 * kRegEpi + 256 * kRegConv == kThreads * kRegLaunch,
                 "register split");
   // Scores a thread holds at a time.  bf16: the whole row of the tile.  FP8: 32, read from TMEM
@@ -170,13 +169,12 @@ struct Cfg {
   static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems + 2;
   static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item (not the producer)
   static constexpr uint32_t oMisc = oBar + kBars * 8;
-  // kQuad items, in the space of the second query tile: P of both streams (rows of 64 keys,
+  // FEW, in the space of the second query tile: P of both streams (rows of 64 keys,
   // [stream][half]); and the warps' maxima [stream][2][4 warps][32 rows]
-  static constexpr bool kShare = FP8;
   static constexpr uint32_t oP = oQ + kTile;
   static constexpr uint32_t oLost = oMisc + 16;             // by item: something was taken out of its values
-  static constexpr uint32_t oMax = D == 128 ? oP + 4 * kQuadTile : oLost + 4 * kLostRing;
-  static constexpr uint32_t kBytes = oLost + 4 * kLostRing + (kShare && D != 128 ? 2048 : 0);
+  static constexpr uint32_t oMax = D == 128 ? oP + 4 * kFewTile : oLost + 4 * kLostRing;
+  static constexpr uint32_t kBytes = oLost + 4 * kLostRing + (FEW && D != 128 ? 2048 : 0);
   static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -185,7 +183,6 @@ struct Cfg {
 
 struct Args {
   CUtensorMap tq, tk, tv;
-  CUtensorMap tq4;       // kQuad items' query rows
   const void *v_pages;   // for add_lost
   const int32_t *q_start, *kv_len, *page_table;
   const uint8_t *k_scale, *v_scale;
@@ -195,7 +192,6 @@ struct Args {
   float *part_ml;        // [2 * max_ctas][part_rows][2]
   PagedPiece *piece;     // [max_ctas]
   int B, n_tok, max_pages, n_pages, page_size, lg_page, H_q, H_kv, G, TT;
-  int TT4;               // tokens of a kQuad item's tile at most (0: no such items)
   int part_rows;
   int n_sink, n_stream;  // n_stream < 0: no window
   float sl2;
@@ -242,7 +238,7 @@ __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) 
   e.p0 = s.kv - s.nq + m * 2 * a.TT;
   e.p_hi = e.p0 + e.ntok - 1;
   e.one = e.ntok <= a.TT;
-  e.u = !e.one ? kUnitsTwo : e.ntok <= a.TT4 ? kUnitsQuad8 : a.k_scale ? kUnitsOne8 : kUnitsOne;
+  e.u = !e.one ? kUnitsTwo : a.k_scale ? kUnitsOne8 : kUnitsOne;
   e.ns = e.w0 = e.n = 0;
   if (e.p_hi >= 0) {
     const int last = e.p_hi / kKeys;
@@ -548,9 +544,9 @@ __device__ __forceinline__ void reg_set() {
   else if constexpr (N < kLaunch) reg_dec<N>();
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(const __grid_constant__ Args a) {
-  using C = Cfg<D, FP8>;
+template <int D, bool FP8, bool FEW>
+__global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<D, FP8, FEW>;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::oBar);
   uint64_t *q_full = bars, *q_empty = bars + 1;
@@ -752,10 +748,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       if (!ok || !(ok = warp_wait(&item_full[ri.slot], ri.phase, abort))) break;
       const Item &it = items[ri.slot];
       if (it.flags & kEnd) break;
-      const bool single = it.flags & kSingle, keys = it.flags & kHasKeys;
-      // Few rows lie in every warp's lanes (see the producer), and each warp takes 32 of the keys.
-      const bool quad = C::kShare && (it.flags & kQuad);
-      const int rtok = (quad ? lane : row) / a.G;
+      const bool single = FEW || (it.flags & kSingle), keys = it.flags & kHasKeys;
+      // FEW: the rows lie in every warp's lanes (see the producer), and each warp takes 32 of
+      // the keys.
+      const int rtok = (FEW ? lane : row) / a.G;
       const int tok = rtok + (single ? 0 : i * a.TT); // token of the piece's entry
       const bool row_ok = rtok < a.TT && tok < it.ntok;
       const bool warp_ok = __any_sync(kFull, row_ok);
@@ -799,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
               }
             };
             constexpr int kParts = kKeys / C::kPart;
-            const int part0 = quad ? warp & 3 : 0, part1 = quad ? part0 : kParts - 1;
+            const int part0 = FEW ? warp & 3 : 0, part1 = FEW ? part0 : kParts - 1;
             float mt = -INFINITY;
 #pragma unroll 1
             for (int part = part0; part <= part1; ++part) {
@@ -810,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
               mt = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
             }
-            if (quad) {                               // the maximum over all four warps' keys
+            if (FEW) {                                // the maximum over all four warps' keys
               float *x = reinterpret_cast<float *>(sm + C::oMax) + (2 * i + x_buf) * kRows;
               x[row] = mt;
               __syncwarp();
@@ -828,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                 l *= f;
                 m_ref = mt;
               }
-              if (k > first && (!quad || (warp & 3) == 0)) {   // O holds earlier tiles of this piece
+              if (k > first && (!FEW || (warp & 3) == 0)) {   // O holds earlier tiles of this piece
                 const float2 f2 = make_float2(f, f);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
@@ -862,8 +858,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
                   else acc0 = fadd2(acc0, x);
                   pk[c >> 1] = pack_bf16x2(x.x, x.y);
                 }
-                if (quad) {                           // 64 bytes of the row's 128 for these 64 keys
-                  unsigned char *dst = sm + C::oP + (2 * i + (part >> 1)) * kQuadTile + lane * 128;
+                if (FEW) {                            // 64 bytes of the row's 128 for these 64 keys
+                  unsigned char *dst = sm + C::oP + (2 * i + (part >> 1)) * kFewTile + lane * 128;
 #pragma unroll
                   for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<uint4 *>(dst + ((((part & 1) * 4 + q) ^ (lane & 7)) << 4)) =
@@ -940,7 +936,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       it.b = w.b;
       it.g = w.g;
       it.flags = !w.valid ? kEnd : (w.e.one ? kSingle : 0) | (w.e.keys ? kHasKeys : 0) | (whole ? kWhole : 0) |
-                                       (start ? kStart : 0) | (w.e.ntok <= a.TT4 ? kQuad : 0);
+                                       (start ? kStart : 0);
       if (lane == 0) {
         items[ri.slot] = it;
         lost[ri.slot + (ri.phase ? kItems : 0)] = 0;
@@ -969,7 +965,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     const int part = FP8 ? lane : lane / C::kHalves, hh = FP8 ? 0 : lane - part * C::kHalves;
     for (; ok && hand_out(); walk_next(a, w)) {
       if (!(it.flags & kHasKeys)) continue;
-      const bool single = it.flags & kSingle;
+      const bool single = FEW || (it.flags & kSingle);
       const int T = it.T;
       // the item's query tiles, once the MMAs of the one before have read theirs
       if (q_open) {
@@ -980,14 +976,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       q_open = true;
       if (lane == 0) {
         // two tiles, one, or a few rows into each softmax warp's lanes
-        const bool quad = C::kShare && (it.flags & kQuad);
-        const int nt = quad ? 4 : single ? 1 : 2, tt = quad ? a.TT4 : a.TT;
-        const uint32_t pitch = quad ? kQuadTile : C::kTile;
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nt * C::kHalves * tt * a.G * 128));
+        const int nt = FEW ? 4 : single ? 1 : 2;
+        constexpr uint32_t kPitch = FEW ? kFewTile : C::kTile;
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nt * C::kHalves * a.TT * a.G * 128));
         for (int t = 0; t < nt; ++t)
           for (int hh = 0; hh < C::kHalves; ++hh)
-            tma_load_4d(sm + C::oQ + t * pitch + hh * C::kHalf, quad ? &a.tq4 : &a.tq, q_full, 64 * hh, it.g * a.G,
-                        it.tok0 + (quad ? 0 : t * a.TT), 0);
+            tma_load_4d(sm + C::oQ + t * kPitch + hh * C::kHalf, &a.tq, q_full, 64 * hh, it.g * a.G,
+                        it.tok0 + (FEW ? 0 : t * a.TT), 0);
       }
       __syncwarp();
       const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
@@ -1062,7 +1057,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     const uint64_t dq = sdesc_sw128(smem_u32(sm + C::oQ), 16, 1024);
     const uint64_t dk = sdesc_sw128(smem_u32(sm + C::oRing), 16, 1024);
     const uint64_t dv = sdesc_sw128(smem_u32(sm + C::oRing), C::kHalf, 1024);
-    const uint64_t dp = sdesc_sw128(smem_u32(sm + C::oP + 2 * i * kQuadTile), 16, 1024);
+    const uint64_t dp = sdesc_sw128(smem_u32(sm + C::oP + 2 * i * kFewTile), 16, 1024);
     const uint32_t leader = lane == 0 ? 1u : 0u;
     Ring<C::kSlots> rp;
     Ring<FP8 ? 1 : C::kClean> rc;
@@ -1085,7 +1080,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       // O_i of the piece before has been read (every piece is waited for, so that no phase is
       // missed)
       d_phase ^= 1u;
-      const bool single = it.flags & kSingle, quad = C::kShare && (it.flags & kQuad);
+      const bool single = FEW || (it.flags & kSingle);
       const int T = it.T, ahead = single ? 2 : 1;
       if (!(it.flags & kHasKeys)) {
         ok = warp_wait(&drained[i], d_phase, abort);
@@ -1129,12 +1124,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           tc_fence_after();
           const uint64_t bd = dv + static_cast<uint32_t>(slot) * (C::kTile >> 4);
           const uint32_t acc = first ? 0u : 1u;
-          if (quad) {
-            // P in shared memory; the tile's rows behind kQuadRows are whatever lies there, their
+          if (FEW) {
+            // P in shared memory; the tile's rows behind kFewRows are whatever lies there, their
             // O is not read
 #pragma unroll 2
             for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-              mma_ss(leader, o_tm, dp + (kk >> 2) * (kQuadTile >> 4) + (kk & 3) * 2, bd + kk * 128, id_pv,
+              mma_ss(leader, o_tm, dp + (kk >> 2) * (kFewTile >> 4) + (kk & 3) * 2, bd + kk * 128, id_pv,
                      kk > 0 ? 1u : acc);
           } else {
 #pragma unroll
@@ -1143,7 +1138,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           }
           commit_if(leader, &empty[slot]);
           if (k == last) {
-            if (quad) commit_if(leader, q_empty);     // P lies in the second query tile's space
+            if (FEW) commit_if(leader, q_empty);      // P lies in the second query tile's space
             commit_if(leader, &o_final[i]);
             pass_turn();
           }
@@ -1159,7 +1154,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
           }
           commit_if(leader, &s_full[i]);
           commit_if(leader, &empty[slot]);
-          if (k == last && !quad) commit_if(leader, q_empty);
+          if (k == last && !FEW) commit_if(leader, q_empty);
         }
       }
       if (ok && single && i == 1 && (T & 1)) {        // stream 0 had one tile more
@@ -1181,7 +1176,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
     bool ok = true;
     Item it;
     while (ok && next_item(it)) {
-      const bool single = it.flags & kSingle, keys = it.flags & kHasKeys, whole = it.flags & kWhole;
+      const bool single = FEW || (it.flags & kSingle), keys = it.flags & kHasKeys, whole = it.flags & kWhole;
       const int slot = 2 * blockIdx.x + (it.flags & kStart ? 1 : 0);
       // (m, l) of stream i, and O_i complete; false: gave up
       auto wait_o = [&](int i, bool any) -> bool {
@@ -1198,10 +1193,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
         const int tok = rtok + i * a.TT;              // token of the piece's entry
         const bool row_ok = rtok < a.TT && tok < it.ntok;
         if (!(ok = wait_o(i, keys))) break;
-        const bool quad = C::kShare && (it.flags & kQuad);   // a sum per softmax warp, one reference
-        auto sum = [&](int s) -> float {
+        auto sum = [&](int s) -> float {              // (FEW: a sum per softmax warp, one reference)
           const float2 *x = ml + s * kRows;
-          return quad && warp == C::kEpi ? (x[0].y + x[32].y) + (x[64].y + x[96].y) : x[0].y;
+          return FEW && warp == C::kEpi ? (x[0].y + x[32].y) + (x[64].y + x[96].y) : x[0].y;
         };
         float m = ml[i * kRows].x, l = sum(i), f0 = 1.f, f1 = 0.f;
         bool two = false;
@@ -1376,7 +1370,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       };
       while (ok && next_item(it)) {
         if (!(it.flags & kHasKeys)) continue;
-        const int ahead = it.flags & kSingle ? 2 : 1;
+        const int ahead = FEW || (it.flags & kSingle) ? 2 : 1;
         const int T = it.T;
         // the row's page two tiles ahead and its scale byte one tile ahead of the conversion,
         // so that neither load's latency is waited for
@@ -1427,7 +1421,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1) paged_attn_kernel(co
       Item it;
       while (ok && next_item(it)) {
         if (!(it.flags & kHasKeys)) continue;
-        const int ahead = it.flags & kSingle ? 2 : 1;
+        const int ahead = FEW || (it.flags & kSingle) ? 2 : 1;
         // Every slot is waited for and released, K tiles too: only who holds a slot back sees
         // each of its phases.
 #pragma unroll 1
@@ -1682,9 +1676,9 @@ bool make_query_map(CUtensorMap *m, const void *base, int D, int H, long long st
 // and its registers as the warpgroups' shares expect them (they add up to what the launch holds;
 // a build that holds less would wait for registers that no warp gives back).  Asked once per
 // device: the three calls took 1.2 us of each launch.
-template <int D, bool FP8, class Kern>
+template <int D, bool FP8, bool FEW, class Kern>
 cudaError_t prepare(Kern kern, int &sms, bool again = false) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<D, FP8, FEW>;
   static std::atomic<int> known[64];                  // SMs by device, 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1701,12 +1695,12 @@ cudaError_t prepare(Kern kern, int &sms, bool again = false) {
   return cudaSuccess;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool FEW>
 cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<D, FP8, FEW>;
   Args a;
   std::memset(&a, 0, sizeof(a));
-  const int G = pa.H_q / pa.H_kv, TT = kRows / G;
+  const int G = pa.H_q / pa.H_kv, TT = (FEW ? kFewRows : kRows) / G;
   const int R = std::min(pa.page_size, kKeys);
   const bool maps =
       make_query_map(&a.tq, pa.q, D, pa.H_q, pa.q_stride, pa.n_tok, G, TT) &&
@@ -1714,9 +1708,7 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
                  make_code_map(&a.tv, pa.v_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R)
            : make_bshd_map(&a.tk, pa.k_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R) &&
                  make_bshd_map(&a.tv, pa.v_pages, D, pa.H_kv, pa.page_size, pa.n_pages, R));
-  a.TT4 = C::kShare ? kQuadRows / G : 0;
-  if (!maps || (a.TT4 > 0 && !make_query_map(&a.tq4, pa.q, D, pa.H_q, pa.q_stride, pa.n_tok, G, a.TT4)))
-    return cudaErrorInvalidValue;
+  if (!maps) return cudaErrorInvalidValue;
   a.v_pages = pa.v_pages;
   a.q_start = pa.q_start;
   a.kv_len = pa.kv_len;
@@ -1745,9 +1737,9 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.sl2 = pa.scale * kLog2e;
   // about two clocks a nanosecond; at most 2^31 of them, a second
   a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
-  auto kern = paged_attn_kernel<D, FP8>;
+  auto kern = paged_attn_kernel<D, FP8, FEW>;
   int sms = 0;
-  cudaError_t e = prepare<D, FP8>(kern, sms);
+  cudaError_t e = prepare<D, FP8, FEW>(kern, sms);
   if (e != cudaSuccess) return e;
   // no more CTAs than the launch can have shares of kUnitsMin
   const long long pairs = pa.B + pa.n_tok / (2 * TT);
@@ -1759,7 +1751,7 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
     if (e != cudaErrorInvalidValue || turn) break;
     // a context that was torn down and made again has forgotten the shared memory's limit
     cudaGetLastError();
-    if ((e = prepare<D, FP8>(kern, sms, true)) != cudaSuccess) break;
+    if ((e = prepare<D, FP8, FEW>(kern, sms, true)) != cudaSuccess) break;
   }
   if (e != cudaSuccess) return e;
   MergeArgs ma;
@@ -1771,8 +1763,8 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   ma.part_rows = pa.part_rows;
   ma.H_q = pa.H_q;
   ma.G = G;
-  ma.TT = TT;
-  const int rows = std::min(2 * TT, pa.n_tok) * G;
+  ma.TT = kRows / G;
+  const int rows = std::min(2 * ma.TT, pa.n_tok) * G;
   ProfScope ps("paged_attn_merge", s);
   if (pa.part_rows > kRows)
     return launch_pdl(paged_merge_rows_kernel<D>, dim3(P, pa.part_rows / 32), dim3(D * 2), 0, s, ma);
@@ -1795,8 +1787,11 @@ int paged_attn_ready() {
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s) {
-  if (a.fp8) return a.D == 128 ? launch_d<128, true>(a, s) : launch_d<64, true>(a, s);
-  return a.D == 128 ? launch_d<128, false>(a, s) : launch_d<64, false>(a, s);
+  // FP8 launches of at most 32 rows a KV head, whatever their sequences: see FEW
+  if (a.fp8 && a.n_tok <= kFewRows / (a.H_q / a.H_kv))
+    return a.D == 128 ? launch_d<128, true, true>(a, s) : launch_d<64, true, true>(a, s);
+  if (a.fp8) return a.D == 128 ? launch_d<128, true, false>(a, s) : launch_d<64, true, false>(a, s);
+  return a.D == 128 ? launch_d<128, false, false>(a, s) : launch_d<64, false, false>(a, s);
 }
 
 int paged_attn_device_error() {
