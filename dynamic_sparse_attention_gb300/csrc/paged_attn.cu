@@ -21,10 +21,12 @@
 //   two-tile items: stream i is query tile i, both see every key tile (256 rows per loaded
 //     K/V tile);
 //   one-tile items (a few tokens): both streams hold the same query tile and take the key
-//     tiles alternately; the epilogue joins their halves.  Of FP8 caches' items with at most 32
-//     rows the query rows lie four times in the tile, once in each softmax warp's TMEM lanes:
-//     each warp takes the exponentials of 32 of a tile's keys (one warp would take all of them
-//     otherwise) and P goes through shared memory (1M-key FP8 token: 633 -> 562 us).
+//     tiles alternately; the epilogue joins their halves.
+// FP8 launches of at most 32 rows a KV head (FEW, a kernel of their own) hold the query rows four
+// times in the tile, once in each softmax warp's TMEM lanes: each warp takes the exponentials of
+// 32 of a tile's keys (one warp would take all of them otherwise) and P goes through shared memory
+// (1M-key FP8 token: 550 us without, 497 with).  Chosen by the launch, not by the item: both in one
+// kernel cost the larger items a tenth (mixed FP8 step 417 us against 378).
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (schedule and
 // TMA), 9 and 10 MMA issuers of stream 0 and 1 (one issuer for both spent 1,800 clocks a turn
 // on waits, 16 MMAs and commits against 1,024 in the tensor core), 11 cleaner (bf16 caches),
@@ -36,19 +38,21 @@
 // spilled register costs a round trip to L2.  Every role is one compact loop: instruction
 // fetches bound this kernel before its pipes do (with each role's code unrolled and inlined per
 // case the FP8 cases took two to three times as long; an epilogue of 64 columns at a time in
-// place of 32 costs the 8K window 159 -> 188 us).
+// place of 32 cost the 8K window 159 -> 188 us, and 16 made the FP8 cases 4 % faster).
 //
 // What bounds it (one GB300, 6,773 GB/s and 1,849 TFLOP/s measured):
 //   2,048 tokens against 131,072 bf16 keys, 32/8 heads of 128: 3.15 ms, 1,384 TFLOP/s, 75 % of the
 //     tensor core's burst and 83 % of its sustained rate (the card is at its power limit).  Beside
 //     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
 //     stream depend on one another, and 512 TMEM columns hold no third stream.
-//   16 tokens over 32,768 bf16 keys each: 180 us, 6,490 GB/s (96 %): HBM.
-//   one token over 1,048,576 FP8 keys: 547 us, 3,950 GB/s (58 %): the converters' chain (a tile
-//     takes each of their warps 1,700 clocks of 1,900) and the shared memory's bandwidth (TMA
-//     writes, conversion, both products' operands: 1,800 clocks a tile).
+//   16 tokens over 284,580 bf16 keys in all: 180 us, 6,490 GB/s (96 %): HBM.
+//   one token over 1,048,576 FP8 keys: 487 us, 4,445 GB/s (66 %): the converters' chain (a tile
+//     takes each of their warps 1,700 clocks of about 2,000; sixteen such warps with fewer
+//     registers are slower, 538 us, and P from TMEM in place of shared memory changes nothing).
+//   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 376 us, 830 TFLOP/s
+//     (45 %): the softmax, which reads the scores twice.
 //   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
-//     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and 2.5 more that
+//     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
 //     pass between two items.
 //   one token over 2,048 keys: 14 us, a chain of latencies (share, page, Q and K, two products,
 //     partials, merge) with 1.2 us of bytes in it.
@@ -61,7 +65,7 @@
 //
 // Softmax: the reference m follows the running maximum lazily, moving only when the maximum
 // exceeds it by more than 2^kSlack; P <= 2^kSlack is rounded to bf16 for the tensor core
-// (relative half step 2^-9 of each probability, as fine as the output's own rounding), the
+// (relative half step 2^-8 of each probability, as fine as the output's own rounding), the
 // row sum l adds the unrounded fp32 values, O accumulates in fp32.
 //
 // Keys that no row of the item sees (behind the sequence, before the window, bad pages) have
@@ -155,7 +159,7 @@ struct Cfg {
   // Scores a thread holds at a time.  bf16: the whole row of the tile.  FP8: 32, read from TMEM
   // once for the maximum and again for P: the unrolled body beside the converters' did not
   // fit the instruction cache (3.3 of 10 stall cycles were instruction fetches; 64 at a time,
-  // with the registers for it: one token over 1M keys 547 -> 621 us).
+  // with the registers for it: mixed FP8 step 377 -> 391 us).
   static constexpr int kPart = FP8 ? 32 : 128;
   static constexpr uint32_t oQ = 0;
   static constexpr uint32_t oRing = oQ + 2 * kTile;
@@ -179,6 +183,7 @@ struct Cfg {
   static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
   static_assert(kSlots * kTile >= 4096 * 8, "planning scratch");
+  static_assert(kRawSlots <= 2 * kSlots, "converters tell a slot's last two uses apart by parity");
 };
 
 struct Args {
@@ -1312,15 +1317,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       };
       // tile k (already described) with this row's scale byte sb
       auto convert = [&](int k, uint32_t sb_raw) -> bool {
-        if (!warp_wait(&raw_full[rr.slot], rr.phase, abort)) return false;
-        const TileMeta *md = &meta[(tile + k) % kMetaRing];
-        const bool seen = (md->seen[r >> 5] >> (r & 31)) & 1u;
+        // (The tile's description came with its K tile, which a V converter has seen go by.  K
+        // rows that no row sees need no zeroes: their scores are masked.)
+        const bool seen = !values || ((meta[(tile + k) % kMetaRing].seen[r >> 5] >> (r & 31)) & 1u);
         const int sb = seen ? static_cast<int>(sb_raw) : 127;
         // 2^e as 2^(120 + e) on the raw bits (scales above 2^7: see below); a row that is not
         // seen is multiplied by 0, one with a NaN scale (255) by NaN
         const int e1 = min(sb - 127, 7), e2 = sb - 127 - e1;
         const uint32_t f = !seen ? 0u : sb == 255 ? 0x7fff7fffu : (static_cast<uint32_t>(e1 + 247) << 7) * 0x00010001u;
-        if (!warp_wait(&empty[rp.slot], rp.phase ^ 1u, abort)) return false;
+        // The tile has come; the operand slot's tile before, another warps' perhaps, has been filled
+        // and given back.  Its filling is asked for as well, and in this order: every converter is
+        // past the tile four back, or this one's staging slot would not be full, so the slot's use
+        // two back has been filled, and a parity tells its last use from that one; once that is
+        // filled the use two back has been given back, and the same holds for the release.
+        uint64_t *w0 = &raw_full[rr.slot], *w1 = &full[rp.slot], *w2 = &empty[rp.slot];
+        const uint32_t before = rp.phase ^ 1u;
+        bool ready = mbar_test_wait(w0, rr.phase);
+        ready &= mbar_test_wait(w1, before);
+        ready &= mbar_test_wait(w2, before);
+        if (!__all_sync(kFull, ready) && !(warp_wait(w0, rr.phase, abort) && warp_wait(w1, before, abort) &&
+                                           warp_wait(w2, before, abort)))
+          return false;
         const unsigned char *src = sm + C::oRaw + rr.slot * C::kRaw + r * D;
         unsigned char *dst = sm + C::oRing + rp.slot * C::kTile + r * 128;
         // 16-byte piece p of the row of codes: 128-byte rows hold it at p ^ (r & 7), 64-byte
@@ -1331,13 +1348,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         auto put = [&](int q, const uint4 &o) {
           *reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4)) = o;
         };
+        constexpr int kAtOnce = FEW ? D / 16 : 2;     // loads in flight, as registers allow
 #pragma unroll
-        for (int p0 = 0; p0 < D / 16; p0 += 4) {
-          uint4 c[4];
+        for (int p0 = 0; p0 < D / 16; p0 += kAtOnce) {
+          uint4 c[kAtOnce];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) c[p] = piece(p0 + p);
+          for (int p = 0; p < kAtOnce; ++p) c[p] = piece(p0 + p);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
+          for (int p = 0; p < kAtOnce; ++p) {
             const uint2 y0 = widen4(c[p].x, f), y1 = widen4(c[p].y, f);
             const uint2 y2 = widen4(c[p].z, f), y3 = widen4(c[p].w, f);
             put(2 * (p0 + p), make_uint4(y0.x, y0.y, y1.x, y1.y));
