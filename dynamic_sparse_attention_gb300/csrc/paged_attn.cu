@@ -22,10 +22,11 @@
 //     K/V tile);
 //   one-tile items (a few tokens): both streams hold the same query tile and take the key
 //     tiles alternately; the epilogue joins their halves.
-// FP8 launches of at most 32 rows a KV head (FEW, a kernel of their own) hold the query rows four
+// FP8 decode steps (FEW, a kernel of their own: items of at most 32 rows) hold the query rows four
 // times in the tile, once in each softmax warp's TMEM lanes: each warp takes the exponentials of
 // 32 of a tile's keys (one warp would take all of them otherwise) and P goes through shared memory
-// (1M-key FP8 token: 550 us without, 497 with).  Chosen by the launch, not by the item: both in one
+// (1M-key FP8 token: 550 us without, 497 with; 16 sequences of up to 32,768 FP8
+// keys: 163 and 146).  Chosen by the launch, not by the item: both in one
 // kernel cost the larger items a tenth (mixed FP8 step 417 us against 378).
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (schedule and
 // TMA), 9 and 10 MMA issuers of stream 0 and 1 (one issuer for both spent 1,800 clocks a turn
@@ -46,10 +47,10 @@
 //     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
 //     stream depend on one another, and 512 TMEM columns hold no third stream.
 //   16 tokens over 284,580 bf16 keys in all: 180 us, 6,490 GB/s (96 %): HBM.
-//   one token over 1,048,576 FP8 keys: 487 us, 4,445 GB/s (66 %): the converters' chain (a tile
+//   one token over 1,048,576 FP8 keys: 482 us, 4,490 GB/s (66 %): the converters' chain (a tile
 //     takes each of their warps 1,700 clocks of about 2,000; sixteen such warps with fewer
 //     registers are slower, 538 us, and P from TMEM in place of shared memory changes nothing).
-//   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 376 us, 830 TFLOP/s
+//   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 375 us, 830 TFLOP/s
 //     (45 %): the softmax, which reads the scores twice.
 //   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
 //     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
@@ -98,12 +99,13 @@ using namespace tc;
 
 constexpr int kRows = 128;         // query rows per tile
 constexpr int kKeys = 128;         // keys per tile
-constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run at most 4 ahead)
-// The schedule's units are tenths of the time of a key tile of a two-tile item.  Key tiles of
-// one-tile items, bf16 (their bytes bound it) | FP8; and what an item
-// costs beside its tiles (the pipeline runs empty between two items, results leave); and the
-// least a share is worth cutting for.  With equal tiles for every CTA, whatever their items, CTAs
-// took 296,000 to 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.
+constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run at most 5 ahead of the softmax)
+// The schedule's units are tenths of the time of a key tile of a two-tile item: that, a key tile
+// of a one-tile item in bf16 (bound by its bytes) and FP8, what an item costs beside its tiles
+// (the pipeline runs empty between two items, results leave), and the least that a share is worth
+// cutting for.  With as many tiles for every CTA, whatever their items, CTAs took 296,000 to
+// 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.  FP8 tiles of one-tile
+// items at 5, 6 and 7: mixed FP8 step 434, 377 and 387 us.
 constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsOne8 = 6, kUnitsItem = 20, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -197,6 +199,7 @@ struct Args {
   float *part_ml;        // [2 * max_ctas][part_rows][2]
   PagedPiece *piece;     // [max_ctas]
   int B, n_tok, max_pages, n_pages, page_size, lg_page, H_q, H_kv, G, TT;
+  int TE;                // tokens of an entry: two query tiles' (FEW: one's)
   int part_rows;
   int n_sink, n_stream;  // n_stream < 0: no window
   float sl2;
@@ -233,14 +236,14 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int b) {
 }
 
 __device__ __forceinline__ int n_pairs(const Args &a, const Seq &s) {
-  return (s.nq + 2 * a.TT - 1) / (2 * a.TT);
+  return (s.nq + a.TE - 1) / a.TE;
 }
 
 __device__ __forceinline__ Entry make_entry(const Args &a, const Seq &s, int m) {
   Entry e;
-  e.tok0 = s.qs + m * 2 * a.TT;
-  e.ntok = min(2 * a.TT, s.nq - m * 2 * a.TT);
-  e.p0 = s.kv - s.nq + m * 2 * a.TT;
+  e.tok0 = s.qs + m * a.TE;
+  e.ntok = min(a.TE, s.nq - m * a.TE);
+  e.p0 = s.kv - s.nq + m * a.TE;
   e.p_hi = e.p0 + e.ntok - 1;
   e.one = e.ntok <= a.TT;
   e.u = !e.one ? kUnitsTwo : a.k_scale ? kUnitsOne8 : kUnitsOne;
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       bool many = false;
       if (b < a.B) {
         const Seq s = load_seq(a, b);
-        many = s.nq > 2 * a.TT;
+        many = s.nq > a.TE;
         if (!many && s.nq > 0) {
           const Entry e = make_entry(a, s, 0);
           u = units_of(e.n, e.u) * a.H_kv;
@@ -1428,8 +1431,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
     }
   } else {
     // ---------------------------------------------------------------- cleaner
-    // value rows that no row of the item sees are zeroed in their slot (the converters do it
-    // for FP8 caches)
+    // value rows that no row of the item sees are zeroed in their slot, infinities and NaN of tiles
+    // that the mask cuts taken out (the converters do both for FP8 caches)
     reg_set<C::kRegMisc, C::kRegLaunch>();
     if constexpr (!FP8) {
       Ring<C::kSlots> rp;
@@ -1748,6 +1751,7 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.H_kv = pa.H_kv;
   a.G = G;
   a.TT = TT;
+  a.TE = FEW ? TT : 2 * TT;
   a.part_rows = pa.part_rows;
   const int cap = pa.max_pages * pa.page_size;
   a.n_sink = std::min(pa.n_sink, cap);
@@ -1760,7 +1764,7 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   cudaError_t e = prepare<D, FP8, FEW>(kern, sms);
   if (e != cudaSuccess) return e;
   // no more CTAs than the launch can have shares of kUnitsMin
-  const long long pairs = pa.B + pa.n_tok / (2 * TT);
+  const long long pairs = pa.B + pa.n_tok / a.TE;
   const long long most = pairs * pa.H_kv * (kUnitsTwo * ((cap + kKeys - 1) / kKeys + 1) + kUnitsItem) / kUnitsMin + 1;
   const int P = static_cast<int>(std::min(static_cast<long long>(std::min(sms, kPagedMaxCtas)), most));
   for (int turn = 0; turn < 2; ++turn) {
@@ -1782,9 +1786,9 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   ma.H_q = pa.H_q;
   ma.G = G;
   ma.TT = kRows / G;
-  const int rows = std::min(2 * ma.TT, pa.n_tok) * G;
+  const int rows = std::min(a.TE, pa.n_tok) * G;
   ProfScope ps("paged_attn_merge", s);
-  if (pa.part_rows > kRows)
+  if (!FEW && pa.part_rows > kRows)
     return launch_pdl(paged_merge_rows_kernel<D>, dim3(P, pa.part_rows / 32), dim3(D * 2), 0, s, ma);
   const int y = (rows + kMergeWarps - 1) / kMergeWarps;
   return launch_pdl(paged_merge_kernel<D>, dim3(P, y), dim3(kMergeWarps * 32), 0, s, ma);
@@ -1805,8 +1809,11 @@ int paged_attn_ready() {
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s) {
-  // FP8 launches of at most 32 rows a KV head, whatever their sequences: see FEW
-  if (a.fp8 && a.n_tok <= kFewRows / (a.H_q / a.H_kv))
+  // FEW holds 32 rows of a sequence at a time: launches that cannot have more, and those with no
+  // more tokens than sequences, which are decode steps.  (Should such a launch put many tokens in
+  // one sequence all the same, that one's keys are read once for each 32 rows.)
+  const int few = kFewRows / (a.H_q / a.H_kv);
+  if (a.fp8 && few > 0 && a.n_tok <= std::max(few, a.B))
     return a.D == 128 ? launch_d<128, true, true>(a, s) : launch_d<64, true, true>(a, s);
   if (a.fp8) return a.D == 128 ? launch_d<128, true, false>(a, s) : launch_d<64, true, false>(a, s);
   return a.D == 128 ? launch_d<128, false, false>(a, s) : launch_d<64, false, false>(a, s);

@@ -365,6 +365,22 @@ def test_many_sequences():
 
 # ------------------------------------------------------------ as a program calls them
 
+@pytest.mark.parametrize("D,group", [(128, 4), (64, 8), (128, 32)])
+@pytest.mark.parametrize("n_sink,n_stream", [(0, None), (30, 90)])
+def test_no_more_tokens_than_sequences(D, group, n_sink, n_stream):
+    """FP8 launches that look like a decode step, with one token a sequence, and with thirty in
+    one (an infinity and a NaN among their values) and none in most others."""
+    even = [(1, 37 * i + 1) for i in range(40)]
+    uneven = [(0, 33)] * 15 + [(30, 500)] + [(0, 0)] * 15 + [(1, 200 + i) for i in range(8)] + [(0, 70)]
+    for seed, seqs in ((60, even), (61, uneven)):
+        b = Batch(seqs, 2 * group, 2, D, 16, True, seed=seed)
+        if seqs is uneven:
+            b.v[15][480, 0, 5] = float("nan")
+            b.v[15][490, 1, 6] = float("inf")
+        b.write()
+        b.check(*b.attn(n_sink=n_sink, n_stream=n_stream), n_sink=n_sink, n_stream=n_stream)
+
+
 def test_strided_tokens():
     """q, k_new and v_new as slices of one fused projection."""
     b = Batch([(30, 90), (1, 50)], 8, 2, 128, 32, True, seed=60)
