@@ -99,7 +99,7 @@ using namespace tc;
 
 constexpr int kRows = 128;         // query rows per tile
 constexpr int kKeys = 128;         // keys per tile
-constexpr int kMetaRing = 8;       // tile descriptions in flight (the rings run at most 5 ahead of the softmax)
+constexpr int kMetaRing = 16;      // tile descriptions in flight (the rings run at most 8 ahead of the softmax)
 // The schedule's units are tenths of the time of a key tile of a two-tile item: that, a key tile
 // of a one-tile item in bf16 (bound by its bytes) and FP8, what an item costs beside its tiles
 // (the pipeline runs empty between two items, results leave), and the least that a share is worth
@@ -145,9 +145,14 @@ struct Cfg {
   static constexpr uint32_t kHalf = kKeys * 128;            // bytes of one of them (128 rows)
   static constexpr uint32_t kTile = kHalves * kHalf;        // a Q, K or V tile in bf16
   static constexpr uint32_t kRaw = kKeys * D;               // an FP8 tile
-  static constexpr int kSlots = FP8 ? 3 : 5;                // operand ring (K and V tiles in order)
+  // 64-wide heads leave TMEM columns for P beside S (bf16: each row's scores are in registers
+  // then), so that Q K^T of a stream's next tile is issued before P V of the last.
+  static constexpr bool kEarly = !FP8 && D == 64;
+  static constexpr int kSlots = FP8 ? 3 : kEarly ? 8 : 5;   // operand ring (K and V tiles in order)
+  // K tiles before the first V: items of one query tile, of two
+  static constexpr int kAhead1 = kEarly ? 4 : 2, kAhead2 = kEarly ? 2 : 1;
   static constexpr int kRawSlots = FP8 ? 4 : 0;             // staging ring
-  static constexpr int kClean = FP8 ? 0 : 4;                // value tiles cleaned ahead of their use
+  static constexpr int kClean = FP8 ? 0 : kEarly ? 8 : 4;   // value tiles cleaned ahead of their use
   static constexpr int kSoft = 8;                           // softmax warps
   static constexpr int kEpi = kSoft + 4, kConv = kEpi + 4;  // first epilogue and converter warps
   static constexpr int kThreads = (kEpi + 4 + (FP8 ? 8 : 0)) * 32;
@@ -171,8 +176,8 @@ struct Cfg {
   static constexpr uint32_t oItem = oMl + 2 * kRows * 8;
   static constexpr uint32_t oBar = oItem + kItems * sizeof(Item);
   // q_full, q_empty, slot full/empty, raw full/empty, then for both streams s_full, p_full,
-  // o_final, ml_full, drained, turn; fin, clean, item full/empty, maxed
-  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems + 2;
+  // o_final, ml_full, drained, turn; fin, clean, item full/empty, maxed, s_free, o_done
+  static constexpr int kBars = 2 + 2 * kSlots + 2 * kRawSlots + 12 + 1 + kClean + 2 * kItems + 6;
   static constexpr int kReaders = kSoft + 2 + 4 + (FP8 ? 8 : 1);   // warps that read each item (not the producer)
   static constexpr uint32_t oMisc = oBar + kBars * 8;
   // FEW, in the space of the second query tile: P of both streams (rows of 64 keys,
@@ -181,8 +186,8 @@ struct Cfg {
   static constexpr uint32_t oLost = oMisc + 16;             // by item: something was taken out of its values
   static constexpr uint32_t oMax = D == 128 ? oP + 4 * kFewTile : oLost + 4 * kLostRing;
   static constexpr uint32_t kBytes = oLost + 4 * kLostRing + (FEW && D != 128 ? 2048 : 0);
-  static constexpr uint32_t cS = 0, cO = 2 * kKeys;         // TMEM columns: S_0, S_1 | O_0, O_1
-  static_assert(cO + 2 * D <= kTmemCols, "TMEM columns");
+  static constexpr uint32_t cS = 0, cO = 2 * kKeys, cP = cO + 2 * D;   // TMEM columns: S_0, S_1 | O_0, O_1 | kEarly: P_0, P_1
+  static_assert(cP + (kEarly ? kKeys : 0) <= kTmemCols, "TMEM columns");
   static_assert(kBytes <= 227 * 1024, "shared memory");
   static_assert(kSlots * kTile >= 4096 * 8, "planning scratch");
   static_assert(kRawSlots <= 2 * kSlots, "converters tell a slot's last two uses apart by parity");
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
   uint64_t *s_full = raw_empty + C::kRawSlots, *p_full = s_full + 2, *o_final = p_full + 2;
   uint64_t *ml_full = o_final + 2, *drained = ml_full + 2, *turn = drained + 2, *fin = turn + 2;
   uint64_t *clean = fin + 1, *item_full = clean + C::kClean, *item_empty = item_full + kItems;
-  uint64_t *maxed = item_empty + kItems;
+  uint64_t *maxed = item_empty + kItems, *s_free = maxed + 2, *o_done = s_free + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
   const WaitCtl abort{reinterpret_cast<volatile int *>(sm + C::oMisc + 4), a.wait_clocks, min(a.wait_clocks, 100000u)};
   Plan *plan = reinterpret_cast<Plan *>(sm + C::oMl);   // read before the first piece is handed out
@@ -593,6 +598,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       mbar_init(&drained[i], 4);
       mbar_init(&turn[i], 1);
       mbar_init(&maxed[i], 4);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&o_done[i], 1);
     }
     mbar_init(fin, 2);
     for (int i = 0; i < C::kClean; ++i) mbar_init(&clean[i], 1);
@@ -749,6 +756,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
     const uint32_t o_col = tl + C::cO + i * D;
     float2 *ml = reinterpret_cast<float2 *>(sm + C::oMl) + i * kRows + row;
     uint32_t s_phase = 0, d_phase = 1, x_buf = 0;
+    const uint32_t p_col = C::kEarly ? tl + C::cP + i * (kKeys / 2) : s_col;
     uint32_t tile = 0;                                // key tiles seen so far (meta ring)
     bool ok = true;
     // The piece is read from its ring entry as it is needed and given back at the end.
@@ -823,6 +831,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
               x_buf ^= 1u;                            // buffer and phase alike: the one before is read
               mt = fmax3(x[lane], x[lane + 32], fmaxf(x[lane + 64], x[lane + 96]));
             }
+            if (C::kEarly) {
+              // the scores are here: S may be filled again; and P V of the tile before, which may
+              // still run, is waited for before its O is scaled or its P written over
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_free[i]);
+              if (!(ok = warp_wait(&o_done[i], s_phase, abort))) break;
+              tc_fence_after();
+            }
             mt *= a.sl2;
             const bool move = mt > m_ref + kSlack;
             if (__any_sync(kFull, move)) {
@@ -874,13 +891,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
                         make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                   fence_proxy_async_smem();
                 } else {
-                  tmem_st16(s_col + C::kPart * part + c0, pk);
+                  tmem_st16(C::kEarly ? p_col + c0 / 2 : s_col + C::kPart * part + c0, pk);
                 }
               }
             }
             const float2 as = fadd2(acc0, acc1);
             l += as.x + as.y;
             tmem_wait_st();
+          } else if (C::kEarly) {
+            // (warps without rows keep step: they would be counted for two tiles of one phase)
+            if (lane == 0) mbar_arrive(&s_free[i]);
+            if (!(ok = warp_wait(&o_done[i], s_phase, abort))) break;
           }
           tc_fence_before();
           __syncwarp();
@@ -1005,9 +1026,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         }
         return page;
       };
-      int pg0 = a.n_pages, pg1 = a.n_pages;           // pages of the last two K tiles
+      int pg0 = a.n_pages, pg1 = pg0, pg2 = pg0, pg3 = pg0;   // pages of the last K tiles
       int page_next = page_of(0);
-      const int ahead = single ? 2 : 1;               // K tiles in flight before the first V
+      const int ahead = single ? C::kAhead1 : C::kAhead2;   // K tiles in flight before the first V
       const int lo = a.n_stream < 0 ? 0 : a.n_stream == 0 ? 0x7fffffff : max(it.p0, 0) - a.n_stream + 1;
 #pragma unroll 1
       for (int x = 0; ok && x < 2 * (T + ahead); ++x) {
@@ -1015,11 +1036,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         const int k = value ? (x >> 1) - ahead : x >> 1;
         if (k < 0 || k >= T) continue;
         const int base = tile_base(it, k);
-        // (behind the last K the pages shift by none: the shift is made when K is loaded)
-        int page = single && (x >> 1) < T + 1 ? pg1 : pg0;
+        const int back = min((x >> 1) - 1, T - 1) - k;   // V: K tiles loaded since its own
+        int page = back == 0 ? pg0 : back == 1 ? pg1 : C::kEarly && back == 2 ? pg2 : pg3;
         if (!value) {
           page = page_next;
           page_next = page_of(k + 1);                 // requested meanwhile
+          if (C::kEarly) {
+            pg3 = pg2;
+            pg2 = pg1;
+          }
           pg1 = pg0;
           pg0 = page;
           // the tile's visible keys
@@ -1060,7 +1085,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
     constexpr uint32_t id_pv = idesc_bf16_f32(kRows, D, false, true);
     const int i = __shfl_sync(kFull, warp - C::kSoft - 1, 0);   // stream
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    const uint32_t s_tm = tm + C::cS + i * kKeys, o_tm = tm + C::cO + i * D;
+    const uint32_t s_tm = tm + C::cS + i * kKeys, o_tm = tm + C::cO + i * D, p_tm = tm + C::cP + i * (kKeys / 2);
     // descriptors of the first tiles; the address field counts 16 bytes
     const uint64_t dq = sdesc_sw128(smem_u32(sm + C::oQ), 16, 1024);
     const uint64_t dk = sdesc_sw128(smem_u32(sm + C::oRing), 16, 1024);
@@ -1069,7 +1094,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
     const uint32_t leader = lane == 0 ? 1u : 0u;
     Ring<C::kSlots> rp;
     Ring<FP8 ? 1 : C::kClean> rc;
-    uint32_t q_phase = 0, p_phase = 0, d_phase = 0, t_phase = i ^ 1;
+    uint32_t q_phase = 0, p_phase = 0, d_phase = 0, f_phase = 1, t_phase = i ^ 1;
     bool ok = true;
     // The streams take turns: P V and the Q K^T behind it of one, then of the other.  Left to
     // themselves they fall into step, and then share the tensor core during one half of the
@@ -1089,7 +1114,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       // missed)
       d_phase ^= 1u;
       const bool single = FEW || (it.flags & kSingle);
-      const int T = it.T, ahead = single ? 2 : 1;
+      const int T = it.T, ahead = single ? C::kAhead1 : C::kAhead2;
       if (!(it.flags & kHasKeys)) {
         ok = warp_wait(&drained[i], d_phase, abort);
         continue;
@@ -1128,7 +1153,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           if (!(ok = warp_wait(&p_full[i], p_phase, abort))) break;
           p_phase ^= 1u;
           if (first && !(ok = warp_wait(&drained[i], d_phase, abort))) break;
-          if (!(ok = take_turn())) break;
+          if (!C::kEarly && !(ok = take_turn())) break;
           tc_fence_after();
           const uint64_t bd = dv + static_cast<uint32_t>(slot) * (C::kTile >> 4);
           const uint32_t acc = first ? 0u : 1u;
@@ -1142,15 +1167,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           } else {
 #pragma unroll
             for (uint32_t kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(leader, o_tm, s_tm + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv, kk > 0 ? 1u : acc);
+              mma_ts(leader, o_tm, C::kEarly ? p_tm + kk * 8 : s_tm + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * 128, id_pv,
+                     kk > 0 ? 1u : acc);
           }
           commit_if(leader, &empty[slot]);
           if (k == last) {
             if (FEW) commit_if(leader, q_empty);      // P lies in the second query tile's space
             commit_if(leader, &o_final[i]);
-            pass_turn();
+            if (!C::kEarly) pass_turn();
           }
+          if (C::kEarly) commit_if(leader, &o_done[i]);
         } else {
+          if (C::kEarly) {                            // the scores of the stream's tile before are read
+            if (!(ok = warp_wait(&s_free[i], f_phase, abort))) break;
+            f_phase ^= 1u;
+          }
           tc_fence_after();
           const uint64_t bd = dk + static_cast<uint32_t>(slot) * (C::kTile >> 4);
 #pragma unroll
@@ -1158,14 +1189,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
             const uint32_t off = (kk >> 2) * (C::kHalf >> 4) + (kk & 3) * 2;
             mma_ss(leader, s_tm, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
             // (the turn reaches the other issuer while the last ones run)
-            if (kk == D / 16 - 2 && k >= ahead) pass_turn();
+            if (!C::kEarly && kk == D / 16 - 2 && k >= ahead) pass_turn();
           }
           commit_if(leader, &s_full[i]);
           commit_if(leader, &empty[slot]);
           if (k == last && !FEW) commit_if(leader, q_empty);
         }
       }
-      if (ok && single && i == 1 && (T & 1)) {        // stream 0 had one tile more
+      if (!C::kEarly && ok && single && i == 1 && (T & 1)) {        // stream 0 had one tile more
         ok = take_turn();
         pass_turn();
       }
@@ -1391,7 +1422,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       };
       while (ok && next_item(it)) {
         if (!(it.flags & kHasKeys)) continue;
-        const int ahead = FEW || (it.flags & kSingle) ? 2 : 1;
+        const int ahead = FEW || (it.flags & kSingle) ? C::kAhead1 : C::kAhead2;
         const int T = it.T;
         // the row's page two tiles ahead and its scale byte one tile ahead of the conversion,
         // so that neither load's latency is waited for
@@ -1442,7 +1473,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       Item it;
       while (ok && next_item(it)) {
         if (!(it.flags & kHasKeys)) continue;
-        const int ahead = FEW || (it.flags & kSingle) ? 2 : 1;
+        const int ahead = FEW || (it.flags & kSingle) ? C::kAhead1 : C::kAhead2;
         // Every slot is waited for and released, K tiles too: only who holds a slot back sees
         // each of its phases.
 #pragma unroll 1
