@@ -47,7 +47,7 @@
 //     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
 //     stream depend on one another, and 512 TMEM columns hold no third stream.
 //   16 tokens over 284,580 bf16 keys in all: 180 us, 6,490 GB/s (96 %): HBM.
-//   one token over 1,048,576 FP8 keys: 482 us, 4,490 GB/s (66 %): the converters' chain (a tile
+//   one token over 1,048,576 FP8 keys: 487 us, 4,440 GB/s (66 %): the converters' chain (a tile
 //     takes each of their warps 1,700 clocks of about 2,000; sixteen such warps with fewer
 //     registers are slower, 538 us, and P from TMEM in place of shared memory changes nothing).
 //   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 375 us, 830 TFLOP/s
@@ -55,14 +55,18 @@
 //   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
 //     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
 //     pass between two items.
-//   one token over 2,048 keys: 14 us, a chain of latencies (share, page, Q and K, two products,
+//   one token over 2,048 keys: 15 us, a chain of latencies (share, page, Q and K, two products,
 //     partials, merge) with 1.2 us of bytes in it.
 //
 //   S_i = Q_i K^T (M = N = 128, K = D), P over S_i (each 32 columns' P in the first 16),
 //   O_i += P V.
 // Each stream issues P V (tile t) and right behind it Q K^T (its next tile): S_i full then
 // also says that P V before it has retired, so moving the softmax reference (O rescaled in
-// TMEM) needs no wait of its own.
+// TMEM) needs no wait of its own.  With 64-wide heads in bf16 (kEarly) P has columns of its own:
+// Q K^T of the next tile goes out as soon as the softmax holds a tile's scores, and P V of the tile
+// before is waited for before its O is scaled or its P written over (5,703 tokens of two prompts,
+// 16 heads of 64: 78 -> 68 us; the softmax warps are then busy for 2,700 clocks of a 2,900-clock
+// turn).
 //
 // Softmax: the reference m follows the running maximum lazily, moving only when the maximum
 // exceeds it by more than 2^kSlack; P <= 2^kSlack is rounded to bf16 for the tensor core
@@ -99,7 +103,6 @@ using namespace tc;
 
 constexpr int kRows = 128;         // query rows per tile
 constexpr int kKeys = 128;         // keys per tile
-constexpr int kMetaRing = 16;      // tile descriptions in flight (the rings run at most 8 ahead of the softmax)
 // The schedule's units are tenths of the time of a key tile of a two-tile item: that, a key tile
 // of a one-tile item in bf16 (bound by its bytes) and FP8, what an item costs beside its tiles
 // (the pipeline runs empty between two items, results leave), and the least that a share is worth
@@ -153,6 +156,7 @@ struct Cfg {
   static constexpr int kAhead1 = kEarly ? 4 : 2, kAhead2 = kEarly ? 2 : 1;
   static constexpr int kRawSlots = FP8 ? 4 : 0;             // staging ring
   static constexpr int kClean = FP8 ? 0 : kEarly ? 8 : 4;   // value tiles cleaned ahead of their use
+  static constexpr int kMetaRing = kEarly ? 16 : 8;         // tile descriptions: the rings run 8 or 5 ahead at most
   static constexpr int kSoft = 8;                           // softmax warps
   static constexpr int kEpi = kSoft + 4, kConv = kEpi + 4;  // first epilogue and converter warps
   static constexpr int kThreads = (kEpi + 4 + (FP8 ? 8 : 0)) * 32;
@@ -783,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           tc_fence_after();
           if (warp_ok) {
             const int base = tile_base(it, k);
-            const uint4 seen = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
+            const uint4 seen = *reinterpret_cast<const uint4 *>(meta[(tile + k) % C::kMetaRing].seen);
             const int hi = p - base;                  // keys c <= hi are not after the row
             const int lo = a.n_stream < 0 ? 0 : p - a.n_stream + 1 - base;   // c >= lo: in its window
             const int sk = a.n_sink - base;           // c < sk: a first token
@@ -1037,7 +1041,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         if (k < 0 || k >= T) continue;
         const int base = tile_base(it, k);
         const int back = min((x >> 1) - 1, T - 1) - k;   // V: K tiles loaded since its own
-        int page = back == 0 ? pg0 : back == 1 ? pg1 : C::kEarly && back == 2 ? pg2 : pg3;
+        int page = back == 0 ? pg0 : !C::kEarly || back == 1 ? pg1 : back == 2 ? pg2 : pg3;
         if (!value) {
           page = page_next;
           page_next = page_of(k + 1);                 // requested meanwhile
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           pg1 = pg0;
           pg0 = page;
           // the tile's visible keys
-          uint32_t *seen = meta[(tile + k) % kMetaRing].seen;
+          uint32_t *seen = meta[(tile + k) % C::kMetaRing].seen;
 #pragma unroll
           for (int q = 0; q < kKeys / 32; ++q) {
             const int c = 32 * q + lane, j = base + c;
@@ -1353,7 +1357,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
       auto convert = [&](int k, uint32_t sb_raw) -> bool {
         // (The tile's description came with its K tile, which a V converter has seen go by.  K
         // rows that no row sees need no zeroes: their scores are masked.)
-        const bool seen = !values || ((meta[(tile + k) % kMetaRing].seen[r >> 5] >> (r & 31)) & 1u);
+        const bool seen = !values || ((meta[(tile + k) % C::kMetaRing].seen[r >> 5] >> (r & 31)) & 1u);
         const int sb = seen ? static_cast<int>(sb_raw) : 127;
         // 2^e as 2^(120 + e) on the raw bits (scales above 2^7: see below); a row that is not
         // seen is multiplied by 0, one with a NaN scale (255) by NaN
@@ -1484,7 +1488,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           if (!(ok = warp_wait(&full[rp.slot], rp.phase, abort))) break;
           if (value) {
             unsigned char *v = sm + C::oRing + rp.slot * C::kTile;
-            const uint4 s4 = *reinterpret_cast<const uint4 *>(meta[(tile + k) % kMetaRing].seen);
+            const uint4 s4 = *reinterpret_cast<const uint4 *>(meta[(tile + k) % C::kMetaRing].seen);
             if ((s4.x & s4.y & s4.z & s4.w) != 0xffffffffu) {
               const int at = lane >> 3;               // eight lanes per 128-byte row
 #pragma unroll 1
