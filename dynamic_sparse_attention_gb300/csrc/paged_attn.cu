@@ -47,10 +47,10 @@
 //     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
 //     stream depend on one another, and 512 TMEM columns hold no third stream.
 //   16 tokens over 284,580 bf16 keys in all: 180 us, 6,490 GB/s (96 %): HBM.
-//   one token over 1,048,576 FP8 keys: 487 us, 4,440 GB/s (66 %): the converters' chain (a tile
+//   one token over 1,048,576 FP8 keys: 490 us, 4,415 GB/s (65 %): the converters' chain (a tile
 //     takes each of their warps 1,700 clocks of about 2,000; sixteen such warps with fewer
 //     registers are slower, 538 us, and P from TMEM in place of shared memory changes nothing).
-//   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 375 us, 830 TFLOP/s
+//   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 376 us, 829 TFLOP/s
 //     (45 %): the softmax, which reads the scores twice.
 //   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
 //     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
