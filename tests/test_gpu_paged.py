@@ -504,6 +504,30 @@ def test_waits_that_run_out():
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fp8,seqs", [(False, [(300, 900), (1, 4000)]), (True, [(300, 900), (1, 4000)]),
+                                      (True, [(1, 3000), (1, 500), (1, 9000)])])
+def test_every_kernel_gives_up_and_repeats_itself(D, fp8, seqs):
+    """Each form of the kernel: the same bits in ten calls in a row, the error word when its waits
+    may not last, and the same bits again afterwards."""
+    b = Batch(seqs, 8, 2, D, 32, fp8, seed=65).write()
+    want, wl = b.attn()
+    b.check(want, wl)
+    for out, lse in [b.attn() for _ in range(10)]:
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    torch.cuda.synchronize()
+    try:
+        dsa.set_wait_limit(1)
+        b.attn()
+        torch.cuda.synchronize()
+        assert dsa.device_error() == 8
+    finally:
+        dsa.set_wait_limit(0)
+    out, lse = b.attn()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_items_longer_than_the_wait_limit():
     """A wait is bounded per key tile, not per item: items of 160 tiles on average (some 300 us
     each) under a limit of 100 us."""
