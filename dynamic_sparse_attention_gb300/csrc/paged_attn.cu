@@ -1254,7 +1254,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         }
         const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // NaN stays NaN
         const float g0 = f0 * inv, g1 = f1 * inv;
-        const bool none = !keys || f0 == 0.f || l == 0.f;
+        // (a sum of NaN is no empty row: fmax3 passes over NaN, so m alone cannot tell)
+        const bool none = !keys || l == 0.f || (f0 == 0.f && l == l);
         const size_t orow = static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + rhead;
         const int prow = i * kRows + row;
         auto release = [&]() {                        // TMEM and (m, l) are read
@@ -1670,9 +1671,9 @@ __global__ void __launch_bounds__(D * 2) paged_merge_rows_kernel(const MergeArgs
     float4 o[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = po[(static_cast<size_t>(slot) * (D / 4) + q) * a.part_rows];
-    if (v.x == -INFINITY) continue;                   // no keys for this row in the piece
-    const float m = fmaxf(M, v.x);
-    const float old = M == -INFINITY ? 0.f : fast_exp2(M - m), w = fast_exp2(v.x - m);
+    if (v.x == -INFINITY && v.y == 0.f) continue;     // no keys for this row in the piece
+    const float m = fmaxf(M, v.x);                    // (-inf with a sum of NaN: only scores of NaN)
+    const float old = M == -INFINITY ? 0.f : fast_exp2(M - m), w = v.x == -INFINITY ? 0.f : fast_exp2(v.x - m);
     M = m;
     L = L * old + v.y * w;
 #pragma unroll

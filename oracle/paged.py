@@ -56,8 +56,10 @@ def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float, lost=None):
     """q [n, H_q, D] at positions p0 .. over k, v [T, H_kv, D] (all float64): (out, lse, spread,
     size), where spread = sum_j w_j |v_j| (what a relative error of the weights can move) and
     size = the largest scale * sum_d |q_d k_d| of a head (what a rounding of the dot product is
-    relative to).  lost [T] marks keys that are not there (their page is no page).  A NaN in a
-    key that a row sees makes the row NaN; other infinities and NaN reach only who sees them."""
+    relative to).  lost [T] marks keys that are not there (their page is no page).  A score that is
+    NaN or plus infinity (a NaN in the query or in a key that it sees, say) makes its row NaN, out
+    and lse; one of minus infinity has weight 0.  Infinities and NaN of values reach only who sees
+    them."""
     n, H_q, D = q.shape
     T, H_kv, _ = k.shape
     G = H_q // H_kv
@@ -70,11 +72,12 @@ def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float, lost=None):
     lse, size = np.full((n, H_q), -np.inf), np.zeros((n, H_q))
     for h in range(H_q):
         kk, vv = k[:, h // G], v[:, h // G]
-        s = np.where(see, scale * (q[:, h] @ np.nan_to_num(kk, posinf=0, neginf=0).T), -np.inf)
+        with np.errstate(invalid="ignore"):
+            s = scale * (q[:, h] @ kk.T)
+        nan = (see & ~(s < np.inf)).any(1)
+        s = np.where(see & (s < np.inf), s, -np.inf)
         m = s.max(1, initial=-np.inf)
         some = m > -np.inf
-        if not some.any():
-            continue
         w = np.exp(s - np.where(some, m, 0.0)[:, None])
         l = w.sum(1)
         w /= np.where(some, l, 1.0)[:, None]
@@ -83,9 +86,9 @@ def attend(q, k, v, p0: int, n_sink: int, n_stream, scale: float, lost=None):
         vz = np.where(bad, 0.0, vv)
         out[:, h], spread[:, h] = w @ vz, w @ np.abs(vz)
         for x in np.flatnonzero(bad.any(1)):          # only the rows that see the key
-            out[see[:, x], h] += np.where(bad[x], vv[x], 0.0)
-        nan = (see & np.isnan(kk).any(1)[None]).any(1)
+            out[see[:, x] & some, h] += np.where(bad[x], vv[x], 0.0)
         out[nan, h], lse[nan, h] = np.nan, np.nan
-        ab = scale * (np.abs(q[:, h]) @ np.abs(np.nan_to_num(kk, posinf=0, neginf=0)).T)
+        ab = scale * (np.abs(np.nan_to_num(q[:, h], posinf=0, neginf=0)) @
+                      np.abs(np.nan_to_num(kk, posinf=0, neginf=0)).T)
         size[:, h] = np.where(see, ab, 0.0).max(1, initial=0.0)
     return out, lse, spread, size

@@ -566,3 +566,71 @@ def test_arguments_on_the_gpu():
         dsa.kv_cache_read(c, b.kv_len, b.table)
     torch.cuda.synchronize()
     b.check(*b.attn())
+
+
+# ------------------------------------------------------------ NaN and infinite scores
+
+# items of one token, of one query tile (whole and cut), of two (whole and cut): each with its own epilogue and merge
+NAN_SEQS = [[(1, 1)], [(1, 1), (1, 300), (1, 40), (5, 5)], [(20, 20), (3, 3000)], [(60, 60), (64, 100), (40, 41)],
+            [(300, 4000)], [(1, 4000)], [(1, 9000 - 31 * i) for i in range(12)]]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_sink,n_stream", [(0, None), (40, 300)])
+@pytest.mark.parametrize("seqs", range(len(NAN_SEQS)))
+def test_nan_queries(seqs, n_sink, n_stream, D, fp8):
+    """A NaN in a query row (one head of some tokens) comes out as NaN there, and only there."""
+    b = Batch(NAN_SEQS[seqs], 8, 2, D, 32, fp8, seed=70 + seqs).write()
+    b.q[::3, 1, 5] = float("nan")
+    b.q[-1, 6, D - 1] = float("nan")
+    b.check(*b.attn(n_sink=n_sink, n_stream=n_stream), n_sink=n_sink, n_stream=n_stream)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", range(len(NAN_SEQS)))
+def test_nan_keys_alone_in_sight(seqs, D, fp8):
+    """Rows whose only key is NaN, and keys of NaN that fill whole tiles and pieces of a cut item:
+    whoever sees one is NaN, however the launch was cut."""
+    b = Batch(NAN_SEQS[seqs], 8, 2, D, 32, fp8, seed=80 + seqs)
+    for s, (_, t) in enumerate(b.seqs):
+        b.k[s][0, 1, 3] = float("nan")                     # head 1: every row
+        b.k[s][t // 4:t // 2, 0, 2] = float("nan")         # head 0: a quarter of the context
+    b.write()
+    b.check(*b.attn())
+    b.check(*b.attn(n_sink=0, n_stream=1), n_sink=0, n_stream=1)
+    b.check(*b.attn(n_sink=1, n_stream=0), n_sink=1, n_stream=0)
+    b.check(*b.attn(n_sink=0, n_stream=900), n_sink=0, n_stream=900)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", range(len(NAN_SEQS)))
+def test_infinite_scores(seqs, D):
+    """Plus infinity among a row's scores makes it NaN, minus infinity is a weight of 0; a row that
+    has nothing else is empty."""
+    b = Batch(NAN_SEQS[seqs], 8, 2, D, 32, False, seed=90 + seqs)
+    b.q.copy_(b.q.abs() + 0.01)
+    for s, (_, t) in enumerate(b.seqs):
+        b.k[s][t // 4:t // 2 + 1, 0, 2] = float("-inf")
+        b.k[s][3 * t // 4, 1, 0] = float("inf")
+    b.write()
+    b.check(*b.attn())
+    b.check(*b.attn(n_sink=0, n_stream=1), n_sink=0, n_stream=1)
+    b.check(*b.attn(n_sink=0, n_stream=900), n_sink=0, n_stream=900)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_keys_of_one_piece(D):
+    """Two or three tiles of NaN keys at every place of a context: one of them is the whole of a cut
+    item's piece, whose other pieces are finite."""
+    t = 3000
+    b = Batch([(300, t)], 8, 2, D, 32, False, seed=99)
+    good = b.k[0].clone()
+    for tiles in (2, 3):
+        for at in range(0, 2700 // 128 - tiles):
+            b.k[0].copy_(good)
+            b.k[0][128 * at:128 * (at + tiles), 1, 0] = float("nan")
+            out, lse = b.write().attn()
+            assert torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all(), (tiles, at)
+            assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse[:, :4]).all()

@@ -167,3 +167,26 @@ def test_attend_against_torch_attention():
     w = np.exp(0.2 * k[keys, h // 2] @ q[4, h])
     assert np.allclose(out[4, h], w @ v[keys, h // 2] / w.sum(), atol=1e-12) and np.isclose(lse[4, h], np.log(w.sum()))
     assert np.isneginf(paged.attend(q, k, v, 11, 0, 0, 0.2)[1]).all()
+
+
+def test_attend_of_nan_and_infinite_scores():
+    """A NaN or plus infinity among a row's scores makes it NaN, minus infinity is a weight of 0,
+    and neither touches the other rows."""
+    rng = np.random.default_rng(2)
+    q, k, v = (rng.standard_normal((n, h, 8)) for n, h in ((4, 2), (9, 1), (9, 1)))
+    plain = paged.attend(q, k, v, 5, 0, None, 0.3)[:2]
+    q1, k1 = q.copy(), k.copy()
+    q1[1, 0, 2] = np.nan                                # row 1 of head 0
+    k1[8] = np.inf * np.sign(q[3, 1])                   # seen by row 3 alone: + infinity for its head 1
+    out, lse, _, size = paged.attend(q1, k1, v, 5, 0, None, 0.3)
+    assert np.isnan(out[1, 0]).all() and np.isnan(lse[1, 0]) and np.isnan(out[3, 1]).all() and np.isnan(lse[3, 1])
+    for i, h in ((0, 0), (0, 1), (1, 1), (2, 0), (2, 1)):
+        assert np.allclose(out[i, h], plain[0][i, h]) and np.isclose(lse[i, h], plain[1][i, h])
+    k1[8] = -k1[8]                                      # - infinity: as if the key were not there
+    out, lse, _, _ = paged.attend(q, k1, v, 5, 0, None, 0.3)
+    want, wl, _, _ = paged.attend(q[3:], k[:8], v[:8], 7, 0, None, 0.3)
+    assert np.allclose(out[3, 1], want[0, 1]) and np.isclose(lse[3, 1], wl[0, 1])
+    out, lse, _, _ = paged.attend(np.full((1, 1, 8), np.nan), k[:1], v[:1], 0, 0, None, 0.3)
+    assert np.isnan(out).all() and np.isnan(lse).all()
+    out, lse, _, _ = paged.attend(np.full((1, 1, 8), np.nan), k[:1], v[:1], 0, 0, 0, 0.3)   # no window, no sinks
+    assert (out == 0).all() and np.isneginf(lse).all()  # a row that sees nothing stays empty
