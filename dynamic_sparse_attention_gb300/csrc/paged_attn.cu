@@ -78,6 +78,7 @@
 // Where some rows of an item see a key and others do not (tiles at the diagonal, at a window's
 // edge), infinities and NaN in its value row are taken out as well, and the epilogue adds them to
 // the rows that do see the key (add_lost).  Such tiles are searched for them as they arrive.
+// Where a row's weight for a key that it sees underflows to 0, an infinity there comes out as NaN.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -506,8 +507,8 @@ __device__ __forceinline__ bool seen_by_all(const Args &a, const Item &it, int b
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); }
 
 // What was taken out of a value tile (see the cleaner and the converters) goes to those of the
-// warp's n_rows rows, from row `first` of stream i's query tile on, that see it: their weight is
-// positive, so an infinity stays one of its sign, and opposite ones or a NaN make a NaN.
+// warp's n_rows rows, from row `first` of stream i's query tile on, that see it, as with a positive
+// weight: an infinity stays one of its sign, and opposite ones or a NaN make a NaN.
 // add(row - first, token, column, value) adds to a row's result or partial; a column's lane is
 // the same for every key.
 template <int D, bool FP8, class Add>
@@ -1254,8 +1255,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         }
         const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // NaN stays NaN
         const float g0 = f0 * inv, g1 = f1 * inv;
-        // (a sum of NaN is no empty row: fmax3 passes over NaN, so m alone cannot tell)
-        const bool none = !keys || l == 0.f || (f0 == 0.f && l == l);
+        // A row of this piece is empty if its sum is 0: m cannot tell, fmax3 passes over NaN, and a
+        // factor of 0 must reach O, where 0 * infinity or NaN is NaN (seen ones are never lost).
+        const bool none = !keys || l == 0.f;
         const size_t orow = static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + rhead;
         const int prow = i * kRows + row;
         auto release = [&]() {                        // TMEM and (m, l) are read
@@ -1284,7 +1286,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
             if (two) {
               tmem_ld16(o_col + D + c, o);
               tmem_wait_ld();
-              if (f1 != 0.f) {
+              if (!none) {
 #pragma unroll
                 for (int q = 0; q < 16; ++q) x[q] = fmaf(__uint_as_float(o[q]), g1, x[q]);
               }
@@ -1317,8 +1319,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           if (keys && lost[lost_at]) {                // rare
             __syncwarp();                             // the stores above come first
             const int first = (warp & 3) * 32;
+            const uint32_t empty = __ballot_sync(kFull, l == 0.f);   // (every score minus infinity)
             add_lost<D, FP8>(a, it, first, 32, i, [&](int r, int tok, int c, float v) {
               if (whole) {
+                if ((empty >> r) & 1u) return;
                 uint16_t *o = a.out + (static_cast<size_t>(it.tok0 + tok) * a.H_q + it.g * a.G + (first + r) % a.G) * D + c;
                 *o = static_cast<uint16_t>(pack_bf16x2(bf16_lo(*o) + v, 0.f));
               } else {
@@ -1610,7 +1614,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Mer
         const int src = (p + odd) & 31;
         const float f = __shfl_sync(kFull, w, src);
         const int s = __shfl_sync(kFull, slot, src);
-        if (p + odd < n && f != 0.f) {
+        if (p + odd < n && s >= 0) {                  // (f may be 0: infinities and NaN still count)
           const float4 o = po[(static_cast<size_t>(s) * (D / 4) + c4) * a.part_rows + prow];
           acc.x = fmaf(o.x, f, acc.x);
           acc.y = fmaf(o.y, f, acc.y);

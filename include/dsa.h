@@ -470,8 +470,12 @@ int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
  * kv_cache_write comes first on the stream.
  *   q [n_tok, H_q, D] bf16 with q_stride elements between tokens (a multiple of 8, at least
  *   H_q * D); out [n_tok, H_q, D] bf16; lse [n_tok, H_q] fp32, natural log (NULL to skip);
- *   scale positive and finite.  A row that attends nothing gets out = 0, lse = -inf.
- * Nothing that the pages hold at positions no row of the call attends reaches a result.
+ *   scale positive and finite.  A row that attends nothing, or whose scores are all -inf, gets
+ *   out = 0, lse = -inf; one with a score of NaN or +inf is NaN, out and lse.
+ * Nothing that the pages hold at positions no row of the call attends reaches a result, and an
+ * infinity or a NaN in a value row reaches the rows that attend it alone: their result is infinite
+ * or NaN in its column (NaN in place of an infinity where the key's weight, relative to the row's
+ * largest, is below fp32's range).
  * Deterministic: the same call gives the same bits.  Two calls (or two captured graphs) that may
  * run at the same time need workspaces of their own.
  * The launches use programmatic dependent launch and wait for the stream's previous kernel

@@ -634,3 +634,51 @@ def test_nan_keys_of_one_piece(D):
             out, lse = b.write().attn()
             assert torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all(), (tiles, at)
             assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse[:, :4]).all()
+
+
+# ------------------------------------------------------------ infinities and NaN of little weight
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs,bad,heavy", [([(1, 200)], 10, 128), ([(1, 300)], 140, 256), ([(1, 250)], 140, 0),
+                                            ([(60, 400)], 10, 256), ([(3, 9000)], 10, 8000), ([(1, 9000)], 8500, 0),
+                                            ([(300, 4000)], 10, 3600), ([(300, 4000)], 3000, 0),
+                                            ([(1, 300), (1, 400), (1, 9000)], 140, 256)])
+def test_bad_values_whose_weight_vanishes(seqs, bad, heavy, D, fp8):
+    """Key `bad` weighs less than 2^-500 of the keys from `heavy` on (of the 100 first ones), and its
+    value row holds a NaN and an infinity: there every row's result is infinite or NaN, however the
+    launch was cut, and as without it everywhere else."""
+    b = Batch(seqs, 8, 2, D, 32, fp8, seed=100)
+    b.q.fill_(1.0)
+    for s, (_, t) in enumerate(seqs):
+        b.k[s].fill_(0.0)
+        b.k[s][heavy:heavy + 100 if heavy == 0 else t] = 64.0      # scores of 64 sqrt(D) and 0
+        b.v[s][bad, 0, 7], b.v[s][bad, 0, 9] = float("nan"), float("inf")
+    b.write()
+    out, lse = b.attn()
+    at = 0
+    for s, (n, t) in enumerate(seqs):
+        k, v = b.held(s)
+        O, L, spread, _ = paged.attend(f64(b.q)[at:at + n], k, v, t - n, 0, None, D ** -0.5)
+        got, z = f64(out)[at:at + n], lse[at:at + n].cpu().numpy().astype(np.float64)
+        assert (np.isfinite(O) == np.isfinite(got)).all()
+        assert not np.isfinite(got[:, :4, 7]).any() and np.isfinite(got[:, 4:]).all()
+        # dot products are exact: the scale, log2 e, their product, its product with the score, the sum
+        # with log2 l, ln 2 and the product with that are seven roundings
+        assert (np.abs(z - L) <= 2.0 ** -19 + 7 * 2.0 ** -24 * np.abs(L)).all()
+        good = np.isfinite(O)
+        assert (np.abs(got - O)[good] <= (H * np.abs(O) + (H + 2.0 ** -18) * spread)[good]).all()
+        at += n
+
+
+def test_rows_without_weight_have_no_bad_values():
+    """Every score of a row is minus infinity: it is empty, whatever its value rows hold, in tiles that
+    the mask cuts and in others."""
+    for n in (1, 5, 70):
+        b = Batch([(n, 400), (n, n)], 4, 1, 128, 32, False, seed=101)
+        b.q.fill_(1.0)
+        for s in range(2):
+            b.k[s].fill_(float("-inf"))
+            b.v[s][0, 0, 3], b.v[s][-1, 0, 4] = float("inf"), float("nan")
+        out, lse = b.write().attn()
+        assert (out == 0).all() and torch.isneginf(lse).all()
