@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheReadArgs a
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kThreads;
         if (i < pieces) {
-          // 2^(s - 127); s = 0 reads as 0, s = 255 as NaN
-          const float f = __uint_as_float(s[u] == 255u ? 0x7fffffffu : s[u] << 23);
+          // 2^(s - 127), for s = 0 a subnormal of fp32; NaN for s = 255
+          const float f = __uint_as_float(s[u] == 255u ? 0x7fffffffu : s[u] == 0u ? 0x00400000u : s[u] << 23);
           float x[8];
           f16x2_to_f32x2(e4m3x2_to_f16x2(w[u].x), x[0], x[1]);
           f16x2_to_f32x2(e4m3x2_to_f16x2(w[u].x >> 16), x[2], x[3]);

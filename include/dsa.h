@@ -412,7 +412,9 @@ int sparse_attn_prefill(const void *q, const void *k, const void *v,
  *   k_pages, v_pages [n_pages, page_size, H_kv, D]   bf16, or FP8 E4M3 codes
  *   k_scale, v_scale [n_pages, page_size, H_kv]      FP8 only: one byte s per token and head,
  *                    the row's values are code * 2^(s - 127) (an E8M0 scale), all NaN for
- *                    s = 255; other rows never hold the codes 0x7F and 0xFF
+ *                    s = 255; other rows never hold the codes 0x7F and 0xFF.  Read and attended
+ *                    as bf16: exactly so for 3 <= s <= 246 (kv_cache_write stores 11 .. 246),
+ *                    else rounded, with infinities above bf16's range
  *   page_table [B, max_pages] int32   page that holds positions i*page_size .. of sequence b;
  *                    entries that no position below kv_len[b] needs may hold anything
  *   q_start [B + 1] int32   rows q_start[b] .. q_start[b+1]-1 of the token tensors (n_tok

@@ -682,3 +682,40 @@ def test_rows_without_weight_have_no_bad_values():
             b.v[s][0, 0, 3], b.v[s][-1, 0, 4] = float("inf"), float("nan")
         out, lse = b.write().attn()
         assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------ scales that the writer never makes
+
+def bf16_of(x):
+    """float64 -> the nearest bf16 (ties to even, subnormals and overflow as IEEE) as float64.  x has
+    few bits, so that fp32 holds it exactly unless it overflows."""
+    with np.errstate(over="ignore"):
+        return torch.from_numpy(x.astype(np.float32)).bfloat16().double().numpy()
+
+
+SCALES = [0, 1, 2, 3, 10, 11, 127, 134, 135, 246, 247, 250, 254]
+
+
+def hand_made(D):
+    """Pages of 16 rows with every scale byte of SCALES and every code but the NaN's."""
+    codes = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    rows = -(-len(codes) // D)
+    n = len(SCALES) * rows
+    pages = -(-n // 16)
+    c = np.zeros((pages * 16, D), np.uint8)
+    e = np.zeros(pages * 16, np.uint8)
+    for i, s in enumerate(SCALES):
+        c[i * rows:(i + 1) * rows].flat[:len(codes)] = codes
+        e[i * rows:(i + 1) * rows] = s
+    cache = dsa.PagedKVCache(*(torch.from_numpy(c).cuda().view(pages, 16, 1, D).clone() for _ in range(2)),
+                             *(torch.from_numpy(e).cuda().view(pages, 16, 1).clone() for _ in range(2)))
+    return cache, bf16_of(paged.dequantise(c[:n], e[:n].astype(int) - 127)), n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_scale_byte_reads_as_its_power_of_two(D):
+    cache, want, n = hand_made(D)
+    table = torch.arange(cache.k.shape[0], dtype=torch.int32, device="cuda")[None]
+    k, v = dsa.kv_cache_read(cache, torch.tensor([n], dtype=torch.int32, device="cuda"), table, T_max=n)
+    for x in (k, v):
+        assert np.array_equal(f64(x[0, :, 0]), want)
