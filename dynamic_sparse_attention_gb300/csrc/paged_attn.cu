@@ -1286,7 +1286,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
             if (two) {
               tmem_ld16(o_col + D + c, o);
               tmem_wait_ld();
-              if (!none) {
+              if (l != 0.f) {
 #pragma unroll
                 for (int q = 0; q < 16; ++q) x[q] = fmaf(__uint_as_float(o[q]), g1, x[q]);
               }
