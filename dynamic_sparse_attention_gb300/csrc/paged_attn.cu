@@ -526,8 +526,16 @@ __device__ __forceinline__ void add_lost(const Args &a, const Item &it, int firs
       if (page < 0 || page >= a.n_pages) continue;
       const size_t r = ((static_cast<size_t>(page) << a.lg_page) + (j & (a.page_size - 1))) * a.H_kv + it.g;
       uint2 v;
-      if constexpr (FP8) v.x = v.y = a.v_scale[r] == 255 ? 0x7fff7fffu : 0u;
-      else v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.v_pages) + r * D + col);
+      if constexpr (FP8) {
+        const uint32_t sb = a.v_scale[r];
+        v.x = v.y = sb == 255u ? 0x7fff7fffu : 0u;
+        if (sb > 246u && sb != 255u) {                // larger codes are infinite in bf16: 2^7 first, then the rest
+          const uint32_t f2 = ((sb - 7u) << 7) * 0x00010001u;
+          v = widen4(*reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(a.v_pages) + r * D + col), 0x7f007f00u);
+          v.x = mul_bf16x2(v.x, f2);
+          v.y = mul_bf16x2(v.y, f2);
+        }
+      } else v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.v_pages) + r * D + col);
       if (!__any_sync(kFull, not_finite(v.x) | not_finite(v.y))) continue;
 #pragma unroll 1
       for (int row = 0; row < n_rows; ++row) {
@@ -1406,17 +1414,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
           }
         }
         if (__any_sync(kFull, seen && e2 > 0)) {
-          // rare: a scale above 2^7 takes a second exact multiply, and values of NaN (255) that
-          // not every row of the item sees are taken out (see add_lost)
+          // rare: a scale above 2^7 takes a second multiply, and values that are NaN then (255) or
+          // infinite (above 246) and that not every row of the item sees are taken out (see add_lost)
           const uint32_t f2 = (static_cast<uint32_t>(e2 + 127) << 7) * 0x00010001u;
-          const bool again = seen && e2 > 0 && sb != 255;
-          const bool out = values && seen && sb == 255 && !seen_by_all(a, it, tile_base(it, k));
-          if (out) lost[lost_at] = 1;
+          const bool out = values && sb > 246 && !seen_by_all(a, it, tile_base(it, k));
 #pragma unroll 1
-          for (int q = 0; (again || out) && q < D / 8; ++q) {
+          for (int q = 0; seen && e2 > 0 && q < D / 8; ++q) {
             uint4 *o = reinterpret_cast<uint4 *>(dst + (q >> 3) * C::kHalf + (((q & 7) ^ (r & 7)) << 4));
-            *o = out ? make_uint4(0u, 0u, 0u, 0u)
-                     : make_uint4(mul_bf16x2(o->x, f2), mul_bf16x2(o->y, f2), mul_bf16x2(o->z, f2), mul_bf16x2(o->w, f2));
+            uint4 u = make_uint4(mul_bf16x2(o->x, f2), mul_bf16x2(o->y, f2), mul_bf16x2(o->z, f2), mul_bf16x2(o->w, f2));
+            if (out) {
+              const uint4 n = make_uint4(not_finite(u.x), not_finite(u.y), not_finite(u.z), not_finite(u.w));
+              if (n.x | n.y | n.z | n.w) lost[lost_at] = 1;
+              u = make_uint4(u.x & ~n.x, u.y & ~n.y, u.z & ~n.z, u.w & ~n.w);
+            }
+            *o = u;
           }
         }
         fence_proxy_async_smem();

@@ -719,3 +719,48 @@ def test_every_scale_byte_reads_as_its_power_of_two(D):
     k, v = dsa.kv_cache_read(cache, torch.tensor([n], dtype=torch.int32, device="cuda"), table, T_max=n)
     for x in (k, v):
         assert np.array_equal(f64(x[0, :, 0]), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_scale_byte_is_attended_as_it_is_read(D):
+    """Rows of one key each: their result is its value, as the cache reads back."""
+    cache, want, n = hand_made(D)
+    table = torch.arange(cache.k.shape[0], dtype=torch.int32, device="cuda")[None]
+    q = torch.zeros(n, 2, D, dtype=torch.bfloat16, device="cuda")
+    cache.k.zero_()
+    kl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for tokens in (1, n):                                   # decode form, general form
+        for at in range(0, n, tokens):
+            qs = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+            out, lse = dsa.paged_attn(q[:tokens], cache, qs, kl * 0 + at + tokens, table, n_stream=1)
+            got, w = f64(out), want[at:at + tokens, None]
+            normal = (np.abs(w) >= 2.0 ** -126) | (w == 0)  # smaller products may be flushed
+            assert np.where(normal, got == w, np.abs(got) <= 2.0 ** -126).all()
+            assert (lse == 0).all()
+
+
+@pytest.mark.parametrize("fp8_few", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_scales_reach_only_who_sees_them(D, fp8_few):
+    """Values that a large scale makes infinite in bf16: rows before them keep a finite result, rows
+    that see them get the infinity."""
+    n = 8 if fp8_few else 100
+    for T, at in ((n, n // 2), (700, 699), (700, 700 - n + 1)):
+        b = Batch([(n, T)], 4, 1, D, 32, True, seed=102).write()
+        page, slot = int(b.table[0, at // 32]), at % 32
+        b.cache.v_scale[page, slot] = 254                  # code * 2^127
+        b.cache.v[page, slot, 0] = 0x01                    # 2^-9 * 2^127
+        b.cache.v[page, slot, 0, 5] = 0x7E                 # 448 * 2^127
+        b.cache.v[page, slot, 0, D - 1] = 0xC0             # -2 * 2^127
+        out, lse = b.attn()
+        got = f64(out)
+        sees = np.arange(T - n, T) >= at
+        assert np.isposinf(got[sees][:, :, 5]).all() and np.isneginf(got[sees][:, :, D - 1]).all()
+        assert np.isfinite(np.delete(got, (5, D - 1), 2)).all() and np.isfinite(lse.cpu().numpy()).all()
+        assert np.isfinite(got[~sees]).all()
+        keep = np.flatnonzero(~sees)
+        if len(keep):
+            k, v = b.held(0)
+            O, L, spread, size = paged.attend(f64(b.q)[keep], k, v, T - n, 0, None, D ** -0.5)
+            ds = 2 * D * 2.0 ** -24 * size[..., None]
+            assert (np.abs(got[keep] - O) <= H * np.abs(O) + (H + 2 * ds + 2.0 ** -18) * spread).all()
