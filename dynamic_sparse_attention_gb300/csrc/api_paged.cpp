@@ -62,7 +62,7 @@ template <int N, int M>
 int check_apart(const Span (&outs)[N], const Span (&ins)[M]) {
   auto apart = [](const Span &x, const Span &y) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-    return !x.p || !y.p || (a < b ? static_cast<unsigned long long>(x.n) <= b - a
+    return !x.p || !y.p || x.n <= 0 || y.n <= 0 || (a < b ? static_cast<unsigned long long>(x.n) <= b - a
                                   : static_cast<unsigned long long>(y.n) <= a - b);
   };
   for (int i = 0; i < N; ++i) {
@@ -82,6 +82,12 @@ long long token_bytes(const dsa_paged_shape *s, long long stride, int heads) {
 long long page_bytes(const dsa_paged_shape *s) {
   return static_cast<long long>(s->n_pages) * s->page_size * s->H_kv * s->D * (s->dtype == DSA_BF16_FP8KV ? 1 : 2);
 }
+
+long long scale_bytes(const dsa_paged_shape *s) {   // (a bf16 cache has none, whatever the pointers)
+  return s->dtype == DSA_BF16_FP8KV ? static_cast<long long>(s->n_pages) * s->page_size * s->H_kv : 0;
+}
+
+long long table_bytes(const dsa_paged_shape *s) { return static_cast<long long>(s->B) * s->max_pages * 4; }
 
 struct PagedWs {
   float *part, *part_ml;
@@ -122,9 +128,15 @@ int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, lon
   if (shape->n_tok == 0) return DSA_OK;
   if (!aligned(k_new, 16) || !aligned(v_new, 16))
     return fail(DSA_ERR_ALIGNMENT, "k_new and v_new must be non-NULL and 16-byte aligned");
-  const Span outs[] = {{"k_pages", k_pages, page_bytes(shape)}, {"v_pages", v_pages, page_bytes(shape)}};
+  const Span outs[] = {{"k_pages", k_pages, page_bytes(shape)},
+                       {"v_pages", v_pages, page_bytes(shape)},
+                       {"k_scale", k_scale, scale_bytes(shape)},
+                       {"v_scale", v_scale, scale_bytes(shape)}};
   const Span ins[] = {{"k_new", k_new, token_bytes(shape, k_stride, shape->H_kv)},
-                      {"v_new", v_new, token_bytes(shape, v_stride, shape->H_kv)}};
+                      {"v_new", v_new, token_bytes(shape, v_stride, shape->H_kv)},
+                      {"q_start", q_start, 4ll * (shape->B + 1)},
+                      {"kv_len", kv_len, 4ll * shape->B},
+                      {"page_table", page_table, table_bytes(shape)}};
   if ((st = check_apart(outs, ins))) return st;
   CacheWriteArgs a{};
   a.k_new = static_cast<const uint16_t *>(k_new);
@@ -163,7 +175,12 @@ int kv_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_sca
     return fail(DSA_ERR_ALIGNMENT, "k_out and v_out must be non-NULL and 16-byte aligned");
   const long long rows = static_cast<long long>(shape->B) * T_max * shape->H_kv * shape->D * 2;
   const Span outs[] = {{"k_out", k_out, rows}, {"v_out", v_out, rows}};
-  const Span ins[] = {{"k_pages", k_pages, page_bytes(shape)}, {"v_pages", v_pages, page_bytes(shape)}};
+  const Span ins[] = {{"k_pages", k_pages, page_bytes(shape)},
+                      {"v_pages", v_pages, page_bytes(shape)},
+                      {"k_scale", k_scale, scale_bytes(shape)},
+                      {"v_scale", v_scale, scale_bytes(shape)},
+                      {"kv_len", kv_len, 4ll * shape->B},
+                      {"page_table", page_table, table_bytes(shape)}};
   if ((st = check_apart(outs, ins))) return st;
   CacheReadArgs a{};
   a.k_pages = k_pages;
@@ -221,7 +238,12 @@ int paged_attn(const void *q, long long q_stride, const void *k_pages, const voi
   const Span outs[] = {{"out", out, rows * shape->D * 2}, {"lse", lse, rows * 4}, {"workspace", ws, static_cast<long long>(need)}};
   const Span ins[] = {{"q", q, token_bytes(shape, q_stride, shape->H_q)},
                       {"k_pages", k_pages, page_bytes(shape)},
-                      {"v_pages", v_pages, page_bytes(shape)}};
+                      {"v_pages", v_pages, page_bytes(shape)},
+                      {"k_scale", k_scale, scale_bytes(shape)},
+                      {"v_scale", v_scale, scale_bytes(shape)},
+                      {"q_start", q_start, 4ll * (shape->B + 1)},
+                      {"kv_len", kv_len, 4ll * shape->B},
+                      {"page_table", page_table, table_bytes(shape)}};
   if ((st = check_apart(outs, ins))) return st;
   if ((st = paged_attn_ready())) return st;
   const PagedWs w = paged_layout(shape, ws);

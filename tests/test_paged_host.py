@@ -190,3 +190,36 @@ def test_attend_of_nan_and_infinite_scores():
     assert np.isnan(out).all() and np.isnan(lse).all()
     out, lse, _, _ = paged.attend(np.full((1, 1, 8), np.nan), k[:1], v[:1], 0, 0, 0, 0.3)   # no window, no sinks
     assert (out == 0).all() and np.isneginf(lse).all()  # a row that sees nothing stays empty
+
+
+def test_overlapping_scales_and_tables_are_rejected(lib):
+    """Scale arrays and index tensors count too: as outputs of a write, as inputs of the others.  (Each
+    call here overlaps somewhere, so none goes on to a launch.)"""
+    s = _shape(dtype=2, B=3)                            # scales of 64 * 64 * 2 bytes, a table of 3 * 16 entries
+    far = [OK + (i << 32) for i in range(12)]
+    last = lambda: lib.dsa_last_error().decode()
+
+    def write(k=far[2], v=far[3], ks=far[4], vs=far[5], start=far[6], lens=far[7], table=far[8], shape=s):
+        return lib.kv_cache_write(far[0], far[1], 256, 256, start, lens, table, ctypes.byref(shape), k, v, ks, vs, None)
+
+    def read(ks=far[2], vs=far[3], lens=far[4], table=far[5], ko=far[6], vo=far[7]):
+        return lib.kv_cache_read(far[0], far[1], ks, vs, lens, table, ctypes.byref(s), 100, ko, vo, None)
+
+    def attn(ks=far[2], vs=far[3], start=far[4], lens=far[5], table=far[6], out=far[7], lse=far[8], ws=far[9]):
+        return lib.paged_attn(far[11], 1024, far[0], far[1], ks, vs, start, lens, table, ctypes.byref(s), 0, -1, 0.1, out,
+                              lse, ws, 1 << 31, None)
+
+    out_bytes = 3 * 100 * 2 * 128 * 2
+    for call, kw, two in (
+            (write, dict(vs=far[4]), "v_scale and k_scale"), (write, dict(vs=far[4] + 64 * 64 * 2 - 1), "v_scale and k_scale"),
+            (write, dict(ks=far[2] + 16), "k_scale and k_pages"), (write, dict(vs=far[0] + 1), "v_scale and k_new"),
+            (write, dict(start=far[3] + 64), "v_pages and q_start"), (write, dict(start=far[4] - 12), "k_scale and q_start"),
+            (write, dict(lens=far[4] + 8), "k_scale and kv_len"), (write, dict(table=far[5] - 3 * 16 * 4 + 4), "v_scale and page_table"),
+            (read, dict(ks=far[6] + 16), "k_out and k_scale"), (read, dict(vs=far[7] - 1), "v_out and v_scale"),
+            (read, dict(lens=far[6] + out_bytes - 4), "k_out and kv_len"), (read, dict(table=far[7] + 4), "v_out and page_table"),
+            (attn, dict(ks=far[9] + 5), "workspace and k_scale"), (attn, dict(vs=far[7] + 5), "out and v_scale"),
+            (attn, dict(start=far[8] - 12), "lse and q_start"), (attn, dict(lens=far[9] - 8), "workspace and kv_len"),
+            (attn, dict(table=far[7] + 1024), "out and page_table")):
+        assert call(**kw) == -1 and last().endswith(f"{two} overlap"), (kw, last())
+    # a bf16 cache has no scales: whatever stands there overlaps nothing (the next pair does)
+    assert write(ks=far[2], vs=far[2], lens=far[3], shape=_shape(B=3)) == -1 and "v_pages and kv_len" in last()
