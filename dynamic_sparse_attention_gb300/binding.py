@@ -851,13 +851,21 @@ def _current_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev) if torch._C._cuda_getDevice() == dev else None
 
 
+def _call_stream(dev, stream):
+    """Raw stream of a call on device `dev`, None if the device or the stream has to be switched
+    first (_on).  Handles say nothing about the device: every default stream's is 0."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream is on device {stream.device_index}, the cache on device {dev}")
+    st = _current_stream(dev)
+    return st if stream is None or stream.cuda_stream == st else None
+
+
 class _on:
     """Device `dev` as the current one and `stream` (None: its current stream) as the stream
     that outputs and workspaces are allocated and a call is enqueued on."""
 
     def __init__(self, dev, stream):
-        if stream is not None and stream.device_index != dev:
-            raise ValueError(f"stream is on device {stream.device_index}, the cache on device {dev}")
+        _call_stream(dev, stream)   # refuses another device's
         self.device_ctx = torch.cuda.device(dev)
         self.stream = stream
 
@@ -878,11 +886,10 @@ def kv_cache_write(cache: PagedKVCache, k_new, v_new, q_start, kv_len, page_tabl
     q_start[b + 1] - 1 and holds its last positions; kv_len counts the chunk."""
     lib = _lib or load()
     k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
-    st = _current_stream(dev)
-    if stream is not None or st is None:
-        if stream is None or stream.cuda_stream != st:
-            with _on(dev, stream):
-                return kv_cache_write(cache, k_new, v_new, q_start, kv_len, page_table)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return kv_cache_write(cache, k_new, v_new, q_start, kv_len, page_table)
     table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
     n_tok, k_stride = _token_rows(k_new, "k_new", H_kv, D, dev)
     n_v, v_stride = _token_rows(v_new, "v_new", H_kv, D, dev)
@@ -903,11 +910,10 @@ def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None 
     (default: max_pages * page_size) rows."""
     lib = _lib or load()
     k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
-    st = _current_stream(dev)
-    if stream is not None or st is None:
-        if stream is None or stream.cuda_stream != st:
-            with _on(dev, stream):
-                return kv_cache_read(cache, kv_len, page_table, T_max=T_max, out=out)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return kv_cache_read(cache, kv_len, page_table, T_max=T_max, out=out)
     table, lens, _, B, max_pages = _table_args(page_table, kv_len, None, dev)
     shape, _ = _paged_shape(B, 0, max_pages, n_pages, page_size, H_kv, H_kv, D, dtype)
     if out is None:
@@ -942,12 +948,11 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
     the first n_sink.  Returns (out [n_tok, H_q, D], lse [n_tok, H_q] or None)."""
     lib = _lib or load()
     k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
-    st = _current_stream(dev)
-    if stream is not None or st is None:
-        if stream is None or stream.cuda_stream != st:
-            with _on(dev, stream):
-                return paged_attn(q, cache, q_start, kv_len, page_table, n_sink=n_sink, n_stream=n_stream,
-                                  scale=scale, out=out, lse=lse, want_lse=want_lse, workspace=workspace)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return paged_attn(q, cache, q_start, kv_len, page_table, n_sink=n_sink, n_stream=n_stream,
+                              scale=scale, out=out, lse=lse, want_lse=want_lse, workspace=workspace)
     table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
     n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
     H_q = q.shape[1]

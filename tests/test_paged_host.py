@@ -223,3 +223,23 @@ def test_overlapping_scales_and_tables_are_rejected(lib):
         assert call(**kw) == -1 and last().endswith(f"{two} overlap"), (kw, last())
     # a bf16 cache has no scales: whatever stands there overlaps nothing (the next pair does)
     assert write(ks=far[2], vs=far[2], lens=far[3], shape=_shape(B=3)) == -1 and "v_pages and kv_len" in last()
+
+
+def test_default_stream_of_another_device(lib, monkeypatch):
+    """Every device's default stream has the handle 0: each entry point tells them apart by the device,
+    before it looks at anything else."""
+    class Default:
+        cuda_stream, device_index = 0, 1
+    c = dsa.PagedKVCache.empty(4, 16, 2, 64, device="cpu")
+    monkeypatch.setattr(binding, "_cache_args", lambda cache: (OK, OK, None, None, cache.k.shape, 0, 0))
+    monkeypatch.setattr(binding, "_current_stream", lambda dev: 0)
+    one, table = torch.ones(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    start, q = torch.tensor([0, 1], dtype=torch.int32), torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: dsa.kv_cache_write(c, q[:, :2], q[:, :2], start, one, table, stream=Default()),
+                 lambda: dsa.kv_cache_read(c, one, table, stream=Default()),
+                 lambda: dsa.paged_attn(q, c, start, one, table, stream=Default())):
+        with pytest.raises(ValueError, match="stream is on device 1, the cache on device 0"):
+            call()
+    Default.device_index = 0                            # the cache's own: on to the next check
+    with pytest.raises(ValueError, match="page_table must be contiguous and on the cache's device"):
+        dsa.paged_attn(q, c, start, one, table, stream=Default())
