@@ -956,6 +956,8 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
     table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
     n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
     H_q = q.shape[1]
+    if n_sink < 0:                                      # (ctypes would cut a large negative one to 32 bits)
+        raise ValueError("n_sink must be >= 0")
     if n_stream is None:
         n_stream = -1
     elif n_stream < 0:

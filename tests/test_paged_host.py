@@ -243,3 +243,16 @@ def test_default_stream_of_another_device(lib, monkeypatch):
     Default.device_index = 0                            # the cache's own: on to the next check
     with pytest.raises(ValueError, match="page_table must be contiguous and on the cache's device"):
         dsa.paged_attn(q, c, start, one, table, stream=Default())
+
+
+@pytest.mark.parametrize("kw", [dict(n_sink=-1), dict(n_sink=-2 ** 32), dict(n_sink=1 - 2 ** 40), dict(n_stream=-1),
+                                dict(n_stream=-2 ** 32)])
+def test_negative_windows_of_any_size(lib, monkeypatch, kw):
+    """-2^32 is 0 in 32 bits.  (Pages of 24 rows: the library would refuse the call as well.)"""
+    c = dsa.PagedKVCache.empty(4, 24, 2, 64, device="cpu")
+    monkeypatch.setattr(binding, "_cache_args", lambda cache: (OK, OK, None, None, cache.k.shape, 0, -1))
+    monkeypatch.setattr(binding, "_current_stream", lambda dev: 0)
+    one, table = torch.ones(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    start, q = torch.tensor([0, 1], dtype=torch.int32), torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="must be >= 0"):
+        dsa.paged_attn(q, c, start, one, table, **kw)
