@@ -907,7 +907,8 @@ def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None 
     """The sequences' rows as contiguous bf16 (k, v) [B, T_max, H_kv, D], the layout that
     hip_select, sparse_attn_decode and the index builders read.  `out`: (k, v) to write into
     (rows behind a sequence's end stay as they are); else new tensors, zero there, of T_max
-    (default: max_pages * page_size) rows."""
+    (default: max_pages * page_size) rows, whose zeroes take more time than the rows: 131,072 FP8
+    tokens of 8 heads of 128 in 263 us, with `out` in 122."""
     lib = _lib or load()
     k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
     st = _call_stream(dev, stream)

@@ -12,9 +12,10 @@
 // back as NaN throughout.
 //
 // Both kernels are bound by HBM: a row is read once and written once.  Measured (of 6,773 GB/s):
-// writing 48,549 tokens of 8 heads of 128 to an FP8 cache (299 MB) 50.6 us, 5,900 GB/s (87 %);
+// writing 48,549 tokens of 8 heads of 128 to an FP8 cache (299 MB) 50 to 52 us, 5,800 GB/s (85 %);
 // 10,764 tokens of 16 heads of 64 in bf16 (88 MB) 18 us; reading 131,072 tokens of 8 heads of 128
-// back from FP8 (807 MB) 121 us, 6,670 GB/s (98 %); a decode step's few rows take a launch, 2.4 us.
+// back from FP8 (807 MB) 120 to 122 us, 6,600 GB/s (98 %); a decode step's few rows take a launch,
+// 2.4 us.
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"

@@ -25,9 +25,9 @@
 // FP8 decode steps (FEW, a kernel of their own: items of at most 32 rows) hold the query rows four
 // times in the tile, once in each softmax warp's TMEM lanes: each warp takes the exponentials of
 // 32 of a tile's keys (one warp would take all of them otherwise) and P goes through shared memory
-// (1M-key FP8 token: 550 us without, 497 with; 16 sequences of up to 32,768 FP8
-// keys: 163 and 146).  Chosen by the launch, not by the item: both in one
-// kernel cost the larger items a tenth (mixed FP8 step 417 us against 378).
+// (1M-key FP8 token: 556 us without, 485 with; 16 sequences of up to 32,768 FP8
+// keys: 170 and 150, with 64-wide heads 152 and 127).  Chosen by the launch, not by the item: both in
+// one kernel cost the larger items a tenth (mixed FP8 step 417 us against 378).
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (one thread per row), 8 producer (schedule and
 // TMA), 9 and 10 MMA issuers of stream 0 and 1 (one issuer for both spent 1,800 clocks a turn
 // on waits, 16 MMAs and commits against 1,024 in the tensor core), 11 cleaner (bf16 caches),
@@ -42,19 +42,21 @@
 // place of 32 cost the 8K window 159 -> 188 us, and 16 made the FP8 cases 4 % faster).
 //
 // What bounds it (one GB300, 6,773 GB/s and 1,849 TFLOP/s measured):
-//   2,048 tokens against 131,072 bf16 keys, 32/8 heads of 128: 3.15 ms, 1,384 TFLOP/s, 75 % of the
-//     tensor core's burst and 83 % of its sustained rate (the card is at its power limit).  Beside
+//   2,048 tokens against 131,072 bf16 keys, 32/8 heads of 128: 3.0 to 3.45 ms as the card's power
+//     limit has it, 3.34 as a rule: 1,307 TFLOP/s, 71 % of the tensor core's burst and 79 % of its
+//     sustained rate (in FP8 3.78 ms, 62 % of burst).  Beside
 //     2,048 clocks of MMAs a turn of both streams takes 3,500: softmax and the two products of a
 //     stream depend on one another, and 512 TMEM columns hold no third stream.
-//   16 tokens over 284,580 bf16 keys in all: 180 us, 6,490 GB/s (96 %): HBM.
-//   one token over 1,048,576 FP8 keys: 490 us, 4,415 GB/s (65 %): the converters' chain (a tile
+//   16 tokens over 284,580 bf16 keys in all: 180 to 186 us, 6,290 to 6,490 GB/s (93 to 96 %): HBM;
+//     64-wide heads 125 us, 4,650 GB/s (69 %); in FP8 150 and 127 us, 3,920 and 2,330 GB/s.
+//   one token over 1,048,576 FP8 keys: 485 to 506 us, 4,460 GB/s (66 %): the converters' chain (a tile
 //     takes each of their warps 1,700 clocks of about 2,000; sixteen such warps with fewer
 //     registers are slower, 538 us, and P from TMEM in place of shared memory changes nothing).
 //   16 sequences, 5 prompts in progress and 11 decoding, 160,300 FP8 keys: 376 us, 829 TFLOP/s
 //     (45 %): the softmax, which reads the scores twice.
-//   8,192 tokens, window 1,024 and 256 first keys, bf16: 157 us, 1,008 TFLOP/s of the attended
+//   8,192 tokens, window 1,024 and 256 first keys, bf16: 158 us, 1,004 TFLOP/s of the attended
 //     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
-//     pass between two items.
+//     pass between two items (in FP8 206 us, 41 %).
 //   one token over 2,048 keys: 15 us, a chain of latencies (share, page, Q and K, two products,
 //     partials, merge) with 1.2 us of bytes in it.
 //
@@ -66,12 +68,16 @@
 // Q K^T of the next tile goes out as soon as the softmax holds a tile's scores, and P V of the tile
 // before is waited for before its O is scaled or its P written over (5,703 tokens of two prompts,
 // 16 heads of 64: 78 -> 68 us; the softmax warps are then busy for 2,700 clocks of a 2,900-clock
-// turn).
+// turn; in FP8, without that, 98.5 us).
 //
 // Softmax: the reference m follows the running maximum lazily, moving only when the maximum
 // exceeds it by more than 2^kSlack; P <= 2^kSlack is rounded to bf16 for the tensor core
-// (relative half step 2^-8 of each probability, as fine as the output's own rounding), the
-// row sum l adds the unrounded fp32 values, O accumulates in fp32.
+// (relative half step 2^-8 of each probability, as fine as the output's own rounding; fp16 would keep
+// three bits more, but both operands of a product have one type, and values with their scale do
+// not fit fp16), the row sum l adds the unrounded fp32 values, O accumulates in fp32.  Against
+// float64 the results of normal inputs are off by 0.0019 to 0.0022 relative to their size, where
+// the same formulas with P in fp32 and the one rounding of the result give 0.0017.  O is not divided
+// by l before the end: values times 2^kSlack, summed over the keys, have to fit fp32.
 //
 // Keys that no row of the item sees (behind the sequence, before the window, bad pages) have
 // their value rows zeroed, so whatever the pages hold there cannot reach the sums as 0 * NaN.
@@ -108,8 +114,12 @@ constexpr int kKeys = 128;         // keys per tile
 // of a one-tile item in bf16 (bound by its bytes) and FP8, what an item costs beside its tiles
 // (the pipeline runs empty between two items, results leave), and the least that a share is worth
 // cutting for.  With as many tiles for every CTA, whatever their items, CTAs took 296,000 to
-// 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.  FP8 tiles of one-tile
-// items at 5, 6 and 7: mixed FP8 step 434, 377 and 387 us.
+// 491,000 clocks (7 to 39 items, 68 tiles, 8K window): 252 us against 163.  One-tile items' tiles, with
+// 2 less, as they are and with 2 more, in us: mixed FP8 step of 32/8 heads of 128 510, 376, 399; 32/4
+// heads 472, 339, 349; 8/8 heads 208, 173, 195; 64-wide 467, 343, 357; the same steps in bf16 494,
+// 396, 336; 465, 347, 297; 221, 191, 177; 357, 282, 241 (bf16 tiles of long one-tile items cost nearer
+// 9); 64-wide prompts 74, 68, 69.  An item at 10, 20 and 30: 8K window 169, 158, 159, with
+// 64-wide heads 127, 119, 122, 64-wide prompts 71, 68, 69, the mixed steps within 1 %.
 constexpr int kUnitsTwo = 10, kUnitsOne = 7, kUnitsOne8 = 6, kUnitsItem = 20, kUnitsMin = 24;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -477,8 +487,9 @@ __device__ __forceinline__ uint32_t prmt(uint32_t x) {
 // seven magnitude bits at bits 4..10 of a bf16 read as its value times 2^-120 (bias 127 against
 // 7, subnormal codes as bf16 subnormals), so one exact multiply gives code * 2^e.  Bytes are
 // spread over halves with their sign replicated, moved up by 4 and cut to sign and magnitude:
-// three integer operations for two codes, one of which can run as a multiply on the FMA pipe
-// (the ALU pipe, at half rate, is what bounds this).
+// three integer operations for two codes, one of which can run as a multiply on the FMA pipe (the
+// ALU pipe, at half rate, is the busiest one of the FP8 launches, at 48 %; what bounds the long token
+// is the chain of waits around this).
 __device__ __forceinline__ uint2 widen4(uint32_t c, uint32_t f) {
   const uint32_t x0 = (prmt<0x9180>(c) * 16u) & 0x87f087f0u, x1 = (prmt<0xb3a2>(c) * 16u) & 0x87f087f0u;
   return make_uint2(mul_bf16x2(x0, f), mul_bf16x2(x1, f));

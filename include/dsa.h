@@ -453,8 +453,8 @@ int kv_cache_write(const void *k_new, const void *v_new, long long k_stride, lon
 
 /* kv_cache_read -- the rows of every sequence as contiguous bf16: k_out, v_out [B, T_max,
  * H_kv, D] (the layout hip_select, sparse_attn_decode and the prefill index builders read);
- * row t of sequence b for t < min(kv_len[b], T_max), exactly the values the cache stands for
- * (finite ones).  Rows behind a sequence's end, and those of pages outside the cache, are left
+ * row t of sequence b for t < min(kv_len[b], T_max), the values the cache stands for (see the
+ * scales above).  Rows behind a sequence's end, and those of pages outside the cache, are left
  * as they were.  shape->n_tok and H_q are not used but checked. */
 int kv_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_scale,
                   const uint8_t *v_scale, const int32_t *kv_len, const int32_t *page_table,
@@ -472,7 +472,10 @@ int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
  * kv_cache_write comes first on the stream.
  *   q [n_tok, H_q, D] bf16 with q_stride elements between tokens (a multiple of 8, at least
  *   H_q * D); out [n_tok, H_q, D] bf16; lse [n_tok, H_q] fp32, natural log (NULL to skip);
- *   scale positive and finite.  A row that attends nothing, or whose scores are all -inf, gets
+ *   scale positive and finite.  Softmax statistics and sums are fp32; probabilities are rounded
+ *   to bf16 before they multiply the values (half a step of 2^-8 each).  The sums are divided by
+ *   their weight at the end: 2^8 times the values, summed over the keys, has to fit fp32, else the
+ *   result is infinite or NaN.  A row that attends nothing, or whose scores are all -inf, gets
  *   out = 0, lse = -inf; one with a score of NaN or +inf is NaN, out and lse.
  * Nothing that the pages hold at positions no row of the call attends reaches a result, and an
  * infinity or a NaN in a value row reaches the rows that attend it alone: their result is infinite
@@ -480,6 +483,9 @@ int paged_attn_workspace(const dsa_paged_shape *shape, size_t *bytes);
  * largest, is below fp32's range).
  * Deterministic: the same call gives the same bits.  Two calls (or two captured graphs) that may
  * run at the same time need workspaces of their own.
+ * An FP8 call of no more tokens than sequences (or of at most 32 rows a KV head) is taken for a
+ * decode step: a sequence that brings many tokens all the same has its keys read once for every 32
+ * rows of a KV head.
  * The launches use programmatic dependent launch and wait for the stream's previous kernel
  * before they read anything.
  * Errors: INVALID_ARG / UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA; where a CTA's bounded waits ran
