@@ -24,10 +24,16 @@ from .binding import (  # noqa: F401
     hip_select_workspace_bytes,
     kv_cache_read,
     kv_cache_write,
+    kv_cache_write_rope,
+    kv_pages_copy,
     library_path,
     mixed_index_build,
     mixed_index_build_workspace_bytes,
     load,
+    page_digest_update,
+    page_select,
+    PageDigest,
+    PageSelection,
     paged_attn,
     paged_attn_workspace_bytes,
     PagedKVCache,

@@ -71,6 +71,15 @@ class PagedShape(ctypes.Structure):
                 ("dtype", _c_int)]
 
 
+class RopeCfg(ctypes.Structure):
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("weight_f32", _c_int), ("eps", ctypes.c_float),
+                ("inv_freq", _vp), ("rot", _c_int), ("interleaved", _c_int), ("rope_scale", ctypes.c_float)]
+
+
+class PageSelectCfg(ctypes.Structure):
+    _fields_ = [("keep", _c_int), ("n_sink", _c_int), ("n_local", _c_int), ("q_block", _c_int)]
+
+
 class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", _c_int), ("total_ms", ctypes.c_double)]
 
@@ -121,6 +130,14 @@ _SIGNATURES = {
     "paged_attn_workspace": (_c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
     "paged_attn": (_c_int, [_vp, ctypes.c_longlong, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int,
                             _c_int, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "paged_attn_lists": (_c_int, [_vp, ctypes.c_longlong, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int,
+                                  _c_int, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "kv_cache_write_rope": (_c_int, [_vp, ctypes.c_longlong, _vp, ctypes.c_longlong, _vp, ctypes.c_longlong,
+                                     _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_longlong, _vp, _vp, _vp, _vp, _vp]),
+    "page_digest_update": (_c_int, [_vp] * 9),
+    "page_select_sizes": (_c_int, [_vp, _vp, ctypes.POINTER(_c_int), ctypes.POINTER(_c_int)]),
+    "page_select": (_c_int, [_vp, ctypes.c_longlong] + [_vp] * 12),
+    "kv_pages_copy": (_c_int, [_vp, _vp, _c_int] + [_vp] * 8),
     "dsa_device_error": (_c_int, [ctypes.POINTER(_c_int)]),
     "dsa_set_wait_limit": (_c_int, [ctypes.c_ulonglong]),
     "dsa_profile_enable": (_c_int, [_c_int]),
@@ -819,10 +836,18 @@ def _cache_args(cache: PagedKVCache):
     return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape, BF16_FP8KV, dev
 
 
-def _table_args(page_table, kv_len, q_start, dev):
-    """(pointers of page_table, kv_len, q_start, B, max_pages), checked."""
-    B, max_pages = page_table.shape if page_table.dim() == 2 else (-1, -1)
-    table, lens = _index(page_table, "page_table", 2, dev), _index(kv_len, "kv_len", 1, dev)
+def _table_args(page_table, kv_len, q_start, dev, heads=0):
+    """(pointers of page_table, kv_len, q_start, B, max_pages), checked; with `heads` the table is
+    [B, heads, max_pages]."""
+    if heads:
+        table = _index(page_table, "page_table", 3, dev)
+        B, h, max_pages = page_table.shape
+        if h != heads:
+            raise ValueError(f"a page table for each KV head must be [B, {heads}, max_pages]")
+    else:
+        B, max_pages = page_table.shape if page_table.dim() == 2 else (-1, -1)
+        table = _index(page_table, "page_table", 2, dev)
+    lens = _index(kv_len, "kv_len", 1, dev)
     if kv_len.shape[0] != B:
         raise ValueError("kv_len must be [B], page_table [B, max_pages]")
     if q_start is None:
@@ -936,7 +961,7 @@ def kv_cache_read(cache: PagedKVCache, kv_len, page_table, *, T_max: int | None 
 
 def paged_attn_workspace_bytes(q, cache: PagedKVCache, page_table) -> int:
     n_pages, page_size, H_kv, D = cache.k.shape
-    return _paged_shape(page_table.shape[0], q.shape[0], page_table.shape[1], n_pages, page_size,
+    return _paged_shape(page_table.shape[0], q.shape[0], page_table.shape[-1], n_pages, page_size,
                         q.shape[1], H_kv, D, BF16_FP8KV if cache.fp8 else BF16)[1]
 
 
@@ -946,7 +971,8 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
     """Causal attention of the chunks q (bf16 [n_tok, H_q, D], tokens may be strided) over the
     cache, which holds their own keys already (kv_cache_write).  A row at position p attends
     every key j <= p, or with n_stream the n_stream newest of them (its own included) beside
-    the first n_sink.  Returns (out [n_tok, H_q, D], lse [n_tok, H_q] or None)."""
+    the first n_sink.  page_table [B, max_pages], or [B, H_kv, max_pages] with a list of pages for each
+    KV head (page_select's), whose places are then the positions.  Returns (out [n_tok, H_q, D], lse [n_tok, H_q] or None)."""
     lib = _lib or load()
     k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
     st = _call_stream(dev, stream)
@@ -954,7 +980,8 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
         with _on(dev, stream):
             return paged_attn(q, cache, q_start, kv_len, page_table, n_sink=n_sink, n_stream=n_stream,
                               scale=scale, out=out, lse=lse, want_lse=want_lse, workspace=workspace)
-    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    lists = page_table.dim() == 3
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev, H_kv if lists else 0)
     n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
     H_q = q.shape[1]
     if n_sink < 0:                                      # (ctypes would cut a large negative one to 32 bits)
@@ -981,10 +1008,220 @@ def paged_attn(q, cache: PagedKVCache, q_start, kv_len, page_table, *, n_sink: i
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the cache's device")
-    status = lib.paged_attn(q.data_ptr(), q_stride, k, v, ks, vs, start, lens, table, shape, n_sink, n_stream,
-                            D ** -0.5 if scale is None else scale, out.data_ptr(),
-                            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), st)
+    call = lib.paged_attn_lists if lists else lib.paged_attn
+    status = call(q.data_ptr(), q_stride, k, v, ks, vs, start, lens, table, shape, n_sink, n_stream,
+                  D ** -0.5 if scale is None else scale, out.data_ptr(),
+                  None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size(), st)
     if status:
-        _check("paged_attn", status)
+        _check("paged_attn_lists" if lists else "paged_attn", status)
     return out, lse
+
+
+# ----------------------------------------------------------------------------- the pages' sparse path
+
+def kv_cache_write_rope(cache: PagedKVCache, q, k_new, v_new, q_start, kv_len, page_table, inv_freq, *,
+                        interleaved: bool = False, rope_scale: float = 1.0, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, q_out=None, stream=None):
+    """kv_cache_write with each head's norm and the rotation by position in the same pass, for
+    the queries too; returns the rotated queries [n_tok, H_q, D] (`q_out`, which may be q itself, else a
+    new tensor).  q, k_new, v_new: bf16 [n_tok, heads, D], tokens may be strided (slices of a
+    fused projection).  q_weight, k_weight [D] (bf16 or fp32, both alike): the rows are divided by their
+    root mean square (eps added to the square) and multiplied by it; None: no norm.  inv_freq: float64
+    [rot / 2] on the device, radians per position of the pairs (i, i + rot / 2), or (2 i, 2 i + 1) when
+    interleaved, of the first `rot` dimensions (a multiple of 16); None: no rotation."""
+    lib = _lib or load()
+    k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return kv_cache_write_rope(cache, q, k_new, v_new, q_start, kv_len, page_table, inv_freq,
+                                       interleaved=interleaved, rope_scale=rope_scale, q_weight=q_weight,
+                                       k_weight=k_weight, eps=eps, q_out=q_out)
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
+    n_k, k_stride = _token_rows(k_new, "k_new", H_kv, D, dev)
+    n_v, v_stride = _token_rows(v_new, "v_new", H_kv, D, dev)
+    if n_k != n_tok or n_v != n_tok:
+        raise ValueError("q, k_new and v_new must have the same tokens")
+    H_q = q.shape[1]
+    wtype = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if w.dtype not in (torch.bfloat16, torch.float32) or (wtype or w.dtype) != w.dtype or w.shape != (D,):
+            raise ValueError(f"{name} must be a [{D}] tensor, bfloat16 or float32 and both alike")
+        if w.get_device() != dev or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and on the cache's device")
+        wtype = w.dtype
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be a 1-dimensional float64 tensor")
+        if inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous and on the cache's device")
+        rot = 2 * inv_freq.shape[0]
+    if q_out is None:
+        q_out = torch.empty((n_tok, H_q, D), dtype=torch.bfloat16, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    n_o, o_stride = _token_rows(q_out, "q_out", H_q, D, dev)
+    shape, _ = _paged_shape(B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D, dtype)
+    cfg = RopeCfg(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                  wtype == torch.float32, eps, inv_freq.data_ptr() if rot else None, rot, bool(interleaved), rope_scale)
+    status = lib.kv_cache_write_rope(q.data_ptr(), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+                                     start, lens, table, shape, ctypes.byref(cfg), q_out.data_ptr(), o_stride,
+                                     k, v, ks, vs, st)
+    if status:
+        _check("kv_cache_write_rope", status)
+    return q_out
+
+
+@dataclass
+class PageDigest:
+    """8-bit bounds of the keys of a cache's pages: bounds int8 [n_pages, H_kv, 2, D] (smallest,
+    largest of each channel, rounded outwards) times 2**exp, exp int8 [n_pages, H_kv].  The
+    tensors are the caller's; `empty` allocates them for a cache."""
+    bounds: torch.Tensor
+    exp: torch.Tensor
+    page_size: int
+
+    @classmethod
+    def empty(cls, cache: PagedKVCache) -> "PageDigest":
+        n_pages, page_size, H_kv, D = cache.k.shape
+        return cls(torch.zeros(n_pages, H_kv, 2, D, dtype=torch.int8, device=cache.k.device),
+                   torch.zeros(n_pages, H_kv, dtype=torch.int8, device=cache.k.device), page_size)
+
+
+def _digest_args(digest: PageDigest):
+    """(pointers of bounds and exp, n_pages, H_kv, D, device index), checked."""
+    bounds, exp = digest.bounds, digest.exp
+    dev, shape = bounds.get_device(), bounds.shape
+    if dev < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if len(shape) != 4 or shape[2] != 2 or exp.shape != shape[:2]:
+        raise ValueError("bounds must be [n_pages, H_kv, 2, D] and exp [n_pages, H_kv]")
+    if bounds.dtype != torch.int8 or exp.dtype != torch.int8:
+        raise TypeError("bounds and exp must be int8")
+    if exp.get_device() != dev or not bounds.is_contiguous() or not exp.is_contiguous():
+        raise ValueError("bounds and exp must be contiguous CUDA tensors on one device")
+    return bounds.data_ptr(), exp.data_ptr(), shape[0], shape[1], shape[3], dev
+
+
+def _digest_of_cache(digest, n_pages, page_size, H_kv, D, dev):
+    """Pointers of a digest that has to belong to a cache."""
+    bounds, exp, n, h, d, ddev = _digest_args(digest)
+    if (n, h, d, digest.page_size) != (n_pages, H_kv, D, page_size):
+        raise ValueError("the digest is of another cache's shape")
+    if ddev != dev:
+        raise ValueError("the digest must be on the cache's device")
+    return bounds, exp
+
+
+def page_digest_update(cache: PagedKVCache, digest: PageDigest, n_tok: int, q_start, kv_len, page_table, *,
+                       stream=None) -> None:
+    """Digest again the pages that the chunks touch, over all of their keys below kv_len: after every
+    write of new tokens.  n_tok: rows of the chunks' token tensors (at least q_start[-1])."""
+    lib = _lib or load()
+    k, _, ks, _, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return page_digest_update(cache, digest, n_tok, q_start, kv_len, page_table)
+    bounds, exp = _digest_of_cache(digest, n_pages, page_size, H_kv, D, dev)
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    shape, _ = _paged_shape(B, int(n_tok), max_pages, n_pages, page_size, H_kv, H_kv, D, dtype)
+    status = lib.page_digest_update(k, ks, start, lens, table, shape, bounds, exp, st)
+    if status:
+        _check("page_digest_update", status)
+
+
+@dataclass
+class PageSelection:
+    """Lists of pages for blocks of queries, as paged_attn takes them: rows q_start[j] ..
+    q_start[j + 1] - 1 of the queries attend kv_len[j] keys in the pages page_table[j, h] (-1
+    behind the end).  index: the same lists as places in the sequences' tables, if asked for."""
+    q_start: torch.Tensor
+    kv_len: torch.Tensor
+    page_table: torch.Tensor
+    index: torch.Tensor | None = None
+
+
+@functools.lru_cache(maxsize=1024)
+def _select_sizes(keep, n_sink, n_local, q_block, *sizes):
+    """(ctypes shape, ctypes cfg, n_blocks, max_list) of a page_select call."""
+    shape, cfg = PagedShape(*sizes), PageSelectCfg(keep, n_sink, n_local, q_block)
+    n, m = _c_int(), _c_int()
+    _check("page_select_sizes", load().page_select_sizes(ctypes.byref(shape), ctypes.byref(cfg), ctypes.byref(n),
+                                                         ctypes.byref(m)))
+    return ctypes.byref(shape), ctypes.byref(cfg), n.value, m.value
+
+
+def page_select(q, digest: PageDigest, q_start, kv_len, page_table, *, keep: int, n_sink: int = 1,
+                n_local: int = 1, q_block: int = 1, want_index: bool = False, out: PageSelection | None = None,
+                stream=None) -> PageSelection:
+    """Which pages each block of q_block queries (bf16 [n_tok, H_q, D], tokens may be strided) attends, for
+    each KV head: the first n_sink, the `keep` with the largest bound on a score (from the digest), the
+    n_local before the block's own ones, and those.  The result goes to paged_attn:
+        sel = page_select(q, digest, q_start, kv_len, page_table, keep=60)
+        out, lse = paged_attn(q, cache, sel.q_start, sel.kv_len, sel.page_table)
+    `out`: a PageSelection to write into (its index, if it has one, as well)."""
+    lib = _lib or load()
+    bounds, exp, n_pages, H_kv, D, dev = _digest_args(digest)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return page_select(q, digest, q_start, kv_len, page_table, keep=keep, n_sink=n_sink, n_local=n_local,
+                               q_block=q_block, want_index=want_index, out=out)
+    for name, x in (("keep", keep), ("n_sink", n_sink), ("n_local", n_local), ("q_block", q_block)):
+        if not 0 <= x <= _MAX_KEYS:                     # (ctypes would cut a larger one to 32 bits)
+            raise ValueError(f"{name}={x} must be in [0, 2^30]")
+    table, lens, start, B, max_pages = _table_args(page_table, kv_len, q_start, dev)
+    n_tok, q_stride = _token_rows(q, "q", 0, D, dev)
+    shape, cfg, n_blocks, max_list = _select_sizes(keep, n_sink, n_local, q_block, B, n_tok, max_pages, n_pages,
+                                                   digest.page_size, q.shape[1], H_kv, D, BF16)
+    dims = (n_blocks, H_kv, max_list)
+    if out is None:
+        def new(*size):
+            return torch.empty(size, dtype=torch.int32, device=q.device)
+        if n_tok == 0:                                  # (nothing is launched)
+            return PageSelection(torch.zeros(1, dtype=torch.int32, device=q.device), new(0), new(*dims),
+                                 new(*dims) if want_index else None)
+        out = PageSelection(new(n_blocks + 1), new(n_blocks), new(*dims), new(*dims) if want_index else None)
+    else:
+        for name, t, size in (("q_start", out.q_start, (n_blocks + 1,)), ("kv_len", out.kv_len, (n_blocks,)),
+                              ("page_table", out.page_table, dims), ("index", out.index, dims)):
+            if t is None and name == "index":
+                continue
+            if _index(t, "out." + name, len(size), dev) and tuple(t.shape) != size:
+                raise ValueError(f"out.{name} must be {list(size)}")
+    status = lib.page_select(q.data_ptr(), q_stride, bounds, exp, start, lens, table, shape, cfg,
+                             out.q_start.data_ptr(), out.kv_len.data_ptr(), out.page_table.data_ptr(),
+                             None if out.index is None else out.index.data_ptr(), st)
+    if status:
+        _check("page_select", status)
+    return out
+
+
+def kv_pages_copy(cache: PagedKVCache, src, dst, *, digest: PageDigest | None = None, stream=None) -> None:
+    """Page dst[i] becomes a copy of page src[i] (int32 [n] on the device): keys, values, scales, and
+    the digest if given.  A fork copies the partly filled last page of a sequence and shares the others in
+    its table; a compaction moves pages and rewrites the tables.  Each page stands in dst at most once, and
+    none of them in src; entries outside the cache are skipped."""
+    lib = _lib or load()
+    k, v, ks, vs, (n_pages, page_size, H_kv, D), dtype, dev = _cache_args(cache)
+    st = _call_stream(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return kv_pages_copy(cache, src, dst, digest=digest)
+    bounds = exp = None
+    if digest is not None:
+        bounds, exp = _digest_of_cache(digest, n_pages, page_size, H_kv, D, dev)
+    s, d = _index(src, "src", 1, dev), _index(dst, "dst", 1, dev)
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError("src and dst must have the same length")
+    shape, _ = _paged_shape(1, 0, 1, n_pages, page_size, H_kv, H_kv, D, dtype)
+    status = lib.kv_pages_copy(s, d, n, shape, k, v, ks, vs, bounds, exp, st)
+    if status:
+        _check("kv_pages_copy", status)

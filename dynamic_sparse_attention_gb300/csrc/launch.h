@@ -271,6 +271,60 @@ struct CacheReadArgs {
 };
 cudaError_t launch_kv_read(const CacheReadArgs &a, cudaStream_t s);
 int kv_cache_check_word();
+// The same write with head norms and rotation on the way, queries to q_out (kv_rope.cu).
+struct RopeWriteArgs {
+  const uint16_t *q, *k_new, *v_new;   // token strides in elements
+  long long q_stride, k_stride, v_stride, qo_stride;
+  const int32_t *q_start, *kv_len, *page_table;
+  int B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D;
+  bool fp8;
+  dsa_rope_cfg cfg;
+  uint16_t *q_out;
+  void *k_pages, *v_pages;
+  uint8_t *k_scale, *v_scale;
+  int tpc, wpt, lg_page;               // tokens per CTA, warps per token, log2 of page_size (launcher)
+};
+cudaError_t launch_kv_write_rope(const RopeWriteArgs &a, cudaStream_t s);
+int kv_rope_check_word();
+
+// Digests of pages, and the choice of pages by them (page_select.cu).
+struct DigestArgs {
+  const void *k_pages;
+  const uint8_t *k_scale;
+  const int32_t *q_start, *kv_len, *page_table;
+  int B, n_tok, max_pages, n_pages, page_size, H_kv, D;
+  bool fp8;
+  int8_t *bounds, *exp;
+  int window, lg_page;                 // token rows per CTA, log2 of page_size (launcher)
+};
+cudaError_t launch_page_digest(const DigestArgs &a, cudaStream_t s);
+struct PageSelectArgs {
+  const uint16_t *q;
+  long long q_stride;
+  const int8_t *bounds, *exp;
+  const int32_t *q_start, *kv_len, *page_table;
+  int B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D;
+  dsa_page_select_cfg cfg;
+  int n_blocks, max_list;
+  int32_t *sel_q_start, *sel_kv_len, *sel_table, *sel_index;
+  int lg_page, slice;                  // (launcher) log2 of page_size, keys a CTA has room for
+};
+constexpr int kSelectMaxPages = 262144;
+cudaError_t launch_page_select(const PageSelectArgs &a, cudaStream_t s);
+int page_select_check_word();
+
+// Copies of pages (page_copy.cu).
+struct PageCopyArgs {
+  const int32_t *src, *dst;
+  int n, n_pages;
+  char *big[2];                        // keys and values: big_bytes a page
+  char *small[4];                      // scales, digest bounds and exponents (NULL: none)
+  long long big_bytes;
+  int small_bytes[4];
+  int chunks;                          // (launcher) CTAs per array of a pair
+};
+cudaError_t launch_page_copy(const PageCopyArgs &a, cudaStream_t s);
+int page_copy_check_word();
 
 // Chunk attention over the paged cache (paged_attn.cu).
 constexpr int kPagedMaxCtas = 152;   // shares of a launch, at most (GB300's SMs)
@@ -290,6 +344,7 @@ struct PagedAttnArgs {
   const uint8_t *k_scale, *v_scale;
   const int32_t *q_start, *kv_len, *page_table;
   int B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D;
+  bool per_head;                   // page_table [B, H_kv, max_pages], else [B, max_pages]
   bool fp8;
   int n_sink, n_stream;
   float scale;

@@ -1,0 +1,789 @@
+// Digests of cache pages and the choice of pages by them (page_digest_update, page_select).
+//
+// Mathematics.  A page's digest holds, for each KV head, every channel's smallest and largest key
+// as whole numbers lo_d <= k_d 2^-e <= hi_d in [-127, 127] (rounded outwards).  For a query row
+// q' 2^(e_q), q' whole in [-127, 127],
+//   q' . k 2^-e <= sum_d max(q'_d lo_d, q'_d hi_d) = sum_d (min(q'_d, 0) lo_d + max(q'_d, 0) hi_d),
+// a bound on the row's score with any key of the page, and two dot products of 8-bit integers.
+// The sum is below 128 * 127^2 < 2^21 in size and the scales are powers of two in [2^-50, 2^50], so
+// the score is exact in fp32 in whatever order it is summed, by integer or tensor-core
+// arithmetic alike (products below 2^14 and sums below 2^21 are whole in fp32's 24 bits): the
+// selection has one answer, the same for every kernel and every split of the work.
+//
+// The digest is bound by reading the keys; a decode step's selection by reading the digests
+// (2 D + 1 bytes a page and head), a prompt chunk's by the products.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "mma_sync.cuh"
+#include "profile.h"
+
+namespace dsa {
+
+DSA_CHECK_WORD(page_select_check_word)
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+// ------------------------------------------------------------------ digests
+
+constexpr int kDigestThreads = 256, kDigestWarps = kDigestThreads / 32;
+constexpr int kMaxWindow = 64;
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN loses
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Least e in [-50, 50] with a * 2^-e <= 127 for the finite a with fp32 bits `u`: a = 1.m * 2^x
+// takes x - 6 while 1.m <= 127 / 64, else x - 5; 0 for a = 0.
+__device__ __forceinline__ int exponent127(uint32_t u) {
+  if (u == 0u) return 0;
+  const int e = static_cast<int>(u >> 23) - 133 + ((u & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return min(max(e, -50), 50);
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The 8 keys' channels of lane's 16-byte piece (bf16) or 8-byte piece (E4M3 with the row's scale
+// byte, as the bf16 values that they stand for).
+template <bool FP8>
+__device__ __forceinline__ uint4 load_keys(const DigestArgs &a, size_t row, int D, int piece) {
+  if constexpr (FP8) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.k_pages) + row * D) + piece);
+    const uint32_t s = __ldg(a.k_scale + row);
+    // 2^(s - 127), for s = 0 a subnormal of fp32; NaN for s = 255
+    const float f = __uint_as_float(s == 255u ? 0x7fffffffu : s == 0u ? 0x00400000u : s << 23);
+    float x[8];
+    f16x2_to_f32x2(e4m3x2_to_f16x2(w.x), x[0], x[1]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(w.x >> 16), x[2], x[3]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(w.y), x[4], x[5]);
+    f16x2_to_f32x2(e4m3x2_to_f16x2(w.y >> 16), x[6], x[7]);
+    return make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                      pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
+  } else {
+    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.k_pages) + row * D) + piece);
+  }
+}
+
+__device__ __forceinline__ bool is_inf(uint32_t w) {
+  return (w & 0x7fffu) == 0x7f80u || ((w >> 16) & 0x7fffu) == 0x7f80u;
+}
+
+// A warp digests one page of one head: D / 8 lanes hold 8 channels of a token each, the warp's
+// 256 / D groups of them take the page's tokens in turn, with running bounds in registers.
+template <int D, bool FP8>
+__device__ void digest_page(const DigestArgs &a, int page, int head, int keys) {
+  constexpr int LPT = D / 8, TPW = 32 / LPT, U = 8;   // lanes per token, tokens per step, steps in flight
+  const int lane = threadIdx.x & 31, piece = lane % LPT, t0 = lane / LPT;
+  const size_t row0 = (static_cast<size_t>(page) << a.lg_page) * a.H_kv + head;
+  constexpr uint32_t kNan2 = 0x7fff7fffu;
+  uint32_t lo[4] = {kNan2, kNan2, kNan2, kNan2}, hi[4] = {kNan2, kNan2, kNan2, kNan2};
+  for (int t = t0; t < keys; t += U * TPW) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      u[i] = t + i * TPW < keys ? load_keys<FP8>(a, row0 + static_cast<size_t>(t + i * TPW) * a.H_kv, D, piece)
+                                : make_uint4(kNan2, kNan2, kNan2, kNan2);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lo[c] = min2(lo[c], w[c]);
+        hi[c] = max2(hi[c], w[c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      lo[c] = min2(lo[c], __shfl_xor_sync(kFull, lo[c], o));
+      hi[c] = max2(hi[c], __shfl_xor_sync(kFull, hi[c], o));
+    }
+  // the largest finite magnitude; where a bound is infinite the finite keys behind it are looked
+  // for again
+  uint32_t m = 0;
+  bool inf = false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    inf |= is_inf(lo[c]) || is_inf(hi[c]);
+    const uint32_t x[4] = {lo[c] << 16, lo[c], hi[c] << 16, hi[c]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = x[i] & 0x7fff0000u;
+      m = max(m, v < 0x7f800000u ? v : 0u);
+    }
+  }
+  if (__any_sync(kFull, inf)) {
+    for (int t = t0; t < keys; t += TPW) {
+      const uint4 u = load_keys<FP8>(a, row0 + static_cast<size_t>(t) * a.H_kv, D, piece);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = (w[c] << 16) & 0x7fff0000u, y = w[c] & 0x7fff0000u;
+        m = max(m, max(x < 0x7f800000u ? x : 0u, y < 0x7f800000u ? y : 0u));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  const int e = exponent127(m);
+  const float inv = two_to(-e);
+  // (a NaN bound, a channel without numbers, becomes 0; the conversion saturates infinities)
+  uint32_t b[4] = {0, 0, 0, 0};              // lo of channels 0-3, 4-7, then hi
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x = h ? bf16_hi(lo[c]) : bf16_lo(lo[c]), y = h ? bf16_hi(hi[c]) : bf16_lo(hi[c]);
+      const int v = min(max(__float2int_rd(x * inv), -127), 127), w = min(max(__float2int_ru(y * inv), -127), 127);
+      b[c >> 1] |= (static_cast<uint32_t>(v) & 0xffu) << (16 * (c & 1) + 8 * h);
+      b[2 + (c >> 1)] |= (static_cast<uint32_t>(w) & 0xffu) << (16 * (c & 1) + 8 * h);
+    }
+  }
+  if (t0 == 0) {
+    const size_t out = static_cast<size_t>(page) * a.H_kv + head;
+    uint2 *dst = reinterpret_cast<uint2 *>(a.bounds + out * 2 * D);
+    dst[piece] = make_uint2(b[0], b[1]);
+    dst[LPT + piece] = make_uint2(b[2], b[3]);
+    if (lane == 0) a.exp[out] = static_cast<int8_t>(e);
+  }
+}
+
+// A CTA takes the pages whose first row of a chunk lies in its `window` token rows, every head of
+// them a warp's work; gridDim.y CTAs share the heads.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kDigestThreads) digest_kernel(const DigestArgs a) {
+  __shared__ int s_seq[kMaxWindow];
+  __shared__ int s_page[kMaxWindow], s_keys[kMaxWindow];
+  __shared__ int s_n;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int n0 = blockIdx.x * a.window, n1 = min(a.n_tok, n0 + a.window);
+  grid_dep_wait();
+  if (tid < kMaxWindow) s_seq[tid] = -1;
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kDigestThreads) {
+    const int qs = a.q_start[b], qe = a.q_start[b + 1];
+    DSA_CHECK(qs >= 0 && qe <= a.n_tok);
+    for (int n = max(qs, n0); n < min(qe, n1); ++n) s_seq[n - n0] = b;
+  }
+  __syncthreads();
+  if (tid < n1 - n0 && s_seq[tid] >= 0) {
+    const int b = s_seq[tid], n = n0 + tid;
+    const int qs = a.q_start[b], qe = a.q_start[b + 1], cap = a.max_pages << a.lg_page;
+    const int kv = min(max(a.kv_len[b], 0), cap);
+    DSA_CHECK(kv == a.kv_len[b]);
+    const long long pos = kv - (static_cast<long long>(qe) - n);
+    if (pos >= 0 && ((pos & (a.page_size - 1)) == 0 || n == qs)) {
+      const int i = static_cast<int>(pos >> a.lg_page);
+      const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + i];
+      DSA_CHECK(page >= 0 && page < a.n_pages);
+      if (page >= 0 && page < a.n_pages) {
+        const int at = atomicAdd(&s_n, 1);   // (any order: each page is its own work)
+        s_page[at] = page;
+        s_keys[at] = min(a.page_size, kv - (i << a.lg_page));
+      }
+    }
+  }
+  __syncthreads();
+  const int work = s_n * a.H_kv;
+  for (int i = blockIdx.y * kDigestWarps + warp; i < work; i += gridDim.y * kDigestWarps)
+    digest_page<D, FP8>(a, s_page[i / a.H_kv], i % a.H_kv, s_keys[i / a.H_kv]);
+}
+
+// ------------------------------------------------------------------ selection
+
+// A block of queries and what its lists are made of.
+struct Block {
+  int b, lo, n;        // sequence, first token row, tokens
+  int s0, first;       // candidates: pages [s0, first) of the sequence
+  int own1;            // last own page (-1: no keys)
+  int picked;          // candidates listed
+  int keys;            // length of a list in keys
+};
+
+__device__ __forceinline__ int clamp_row(const PageSelectArgs &a, int x) { return min(max(x, 0), a.n_tok); }
+
+// Block j: a scan over the sequences' counts of blocks, a run of them per thread.
+template <int NT>
+__device__ Block find_block(const PageSelectArgs &a, int j, int *s_scan /* [NT / 32 + 1] */, int *s_found /* [2] */) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int qb = a.cfg.q_block;
+  const int per = (a.B + NT - 1) / NT, b0 = tid * per, b1 = min(a.B, b0 + per);
+  auto blocks = [&](int b) -> int {
+    return (max(clamp_row(a, a.q_start[b + 1]) - clamp_row(a, a.q_start[b]), 0) + qb - 1) / qb;
+  };
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += blocks(b);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  if (tid == 0) s_found[0] = -1;
+  __syncthreads();
+  int at = incl - sum;
+  for (int w = 0; w < warp; ++w) at += s_scan[w];
+  if (j >= at && j < at + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const int x = blocks(b);
+      if (j < at + x) {
+        s_found[0] = b;
+        s_found[1] = j - at;
+        break;
+      }
+      at += x;
+    }
+  }
+  __syncthreads();
+  Block k;
+  k.b = s_found[0];
+  k.s0 = k.first = k.picked = k.keys = 0;
+  k.own1 = -1;
+  if (k.b < 0) {                              // behind the last block: no rows, no keys
+    k.b = a.B - 1;
+    k.lo = clamp_row(a, a.q_start[a.B]);
+    k.n = 0;
+    return k;
+  }
+  const int qs = clamp_row(a, a.q_start[k.b]), qe = clamp_row(a, a.q_start[k.b + 1]);
+  k.lo = qs + s_found[1] * qb;
+  k.n = min(qb, qe - k.lo);
+  const int cap = a.max_pages << a.lg_page, kv = min(max(a.kv_len[k.b], 0), cap);
+  DSA_CHECK(kv == a.kv_len[k.b] && kv >= qe - qs);
+  const int p0 = kv - (qe - k.lo), p1 = p0 + k.n - 1, pc = max(p0, 0);
+  if (p1 < 0) return k;
+  const int own0 = pc >> a.lg_page;
+  k.own1 = p1 >> a.lg_page;
+  k.first = max(0, own0 - min(a.cfg.n_local, own0));
+  k.s0 = min(a.cfg.n_sink, k.first);
+  k.picked = min(a.cfg.keep, k.first - k.s0);
+  k.keys = ((k.s0 + k.picked + own0 - k.first) << a.lg_page) + (pc & (a.page_size - 1)) + p1 - pc + 1;
+  return k;
+}
+
+// entry i of the list of (block j, head g)
+__device__ __forceinline__ void put(const PageSelectArgs &a, int j, int g, int i, int page, int index) {
+  const size_t at = (static_cast<size_t>(j) * a.H_kv + g) * a.max_list + i;
+  a.sel_table[at] = page;
+  if (a.sel_index) a.sel_index[at] = index;
+}
+
+// What a list holds beside its picks, by one CTA.
+template <int NT>
+__device__ void put_fixed(const PageSelectArgs &a, int j, int g, const Block &k) {
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages;
+  const int count = k.own1 < 0 ? 0 : k.s0 + k.picked + k.own1 + 1 - k.first;
+  for (int i = threadIdx.x; i < a.max_list; i += NT) {
+    if (i >= k.s0 && i < k.s0 + k.picked) continue;
+    const int index = i >= count ? -1 : i < k.s0 ? i : k.first + i - k.s0 - k.picked;
+    put(a, j, g, i, index < 0 ? -1 : table[index], index);
+  }
+  if (g == 0 && threadIdx.x == 0) {
+    a.sel_q_start[j] = k.lo;
+    a.sel_kv_len[j] = k.keys;
+    if (j == a.n_blocks - 1) a.sel_q_start[j + 1] = k.lo + k.n;
+  }
+}
+
+// bf16 query elements of a lane -> fp32, the row's exponent
+template <int D>
+__device__ __forceinline__ int row_of(const PageSelectArgs &a, const Block &k, int g, int r, float *x) {
+  constexpr int E = D / 32;                   // elements per lane
+  const int lane = threadIdx.x & 31, G = a.H_q / a.H_kv;
+  const uint16_t *src = a.q + static_cast<size_t>(k.lo + r / G) * a.q_stride + static_cast<size_t>(g * G + r % G) * D;
+  uint32_t w[E / 2];
+  if constexpr (E == 4) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    x[i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    const uint32_t v = __float_as_uint(x[i]) & 0x7fffffffu;
+    m = max(m, v < 0x7f800000u ? v : 0u);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  return exponent127(m);
+}
+// whole number of a scaled element (a NaN: 0)
+__device__ __forceinline__ int whole(float x) { return min(max(__float2int_rn(x), -127), 127); }
+
+struct SelectShared {
+  uint32_t hist[4][256];   // of each digit, read by the whole cluster
+  uint32_t tot[256];
+  int scan[17], found[2];
+  uint32_t res[2];
+  int kept[2];             // keys above the threshold, equal to it
+  int scan2[2][17];
+};
+
+// The `k.picked` best of the cluster's keys (each CTA holds nl of them, of pages p_first ..) into the
+// list: an 8-bit radix select whose histograms the CTAs read from each other, then every CTA writes
+// its own picks behind those of the lower ranks.
+template <int NT>
+__device__ void pick(const PageSelectArgs &a, cg::cluster_group &cluster, SelectShared &sh, const uint32_t *key, int nl,
+                     int p_first, int j, int g, const Block &k) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  uint32_t prefix = 0, mask = 0, left = static_cast<uint32_t>(k.picked);
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < nl; i += NT) {
+      const uint32_t x = key[i];
+      if ((x & mask) == prefix) atomicAdd(&sh.hist[pass][(x >> shift) & 255u], 1u);
+    }
+    cluster.sync();
+    if (tid < 256) {
+      uint32_t t = 0;
+      for (int c = 0; c < C; ++c) t += *cluster.map_shared_rank(&sh.hist[pass][tid], c);
+      sh.tot[tid] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int top = 255 - lane * 8;         // lane's bins, from the top down
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) sum += c[t] = sh.tot[top - t];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
+      }
+      uint32_t run = incl - sum;
+      if (run < left && left <= incl) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (run + c[t] >= left) {
+            sh.res[0] = static_cast<uint32_t>(top - t);
+            sh.res[1] = run;
+            break;
+          }
+          run += c[t];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= sh.res[0] << shift;
+    mask |= 255u << shift;
+    left -= sh.res[1];
+  }
+  // keys above `prefix` are in, and the first `left` of those equal to it
+  const int per = (nl + NT - 1) / NT, i0 = min(nl, tid * per), i1 = min(nl, i0 + per);
+  int gt = 0, eq = 0;
+  for (int i = i0; i < i1; ++i) {
+    gt += key[i] > prefix;
+    eq += key[i] == prefix;
+  }
+  int ig = gt, ie = eq;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, ig, o), w = __shfl_up_sync(kFull, ie, o);
+    if (lane >= o) {
+      ig += v;
+      ie += w;
+    }
+  }
+  if (lane == 31) {
+    sh.scan2[0][warp] = ig;
+    sh.scan2[1][warp] = ie;
+  }
+  __syncthreads();
+  int og = ig - gt, oe = ie - eq;             // before this thread's
+  int tg = 0, te = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w == warp) {
+      og += tg;
+      oe += te;
+    }
+    tg += sh.scan2[0][w];
+    te += sh.scan2[1][w];
+  }
+  if (tid == 0) {
+    sh.kept[0] = tg;
+    sh.kept[1] = te;
+  }
+  cluster.sync();
+  for (int c = 0; c < rank; ++c) {
+    const int *o = cluster.map_shared_rank(sh.kept, c);
+    og += o[0];
+    oe += o[1];
+  }
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages;
+  for (int i = i0; i < i1; ++i) {
+    const bool is_eq = key[i] == prefix;
+    if (key[i] > prefix || (is_eq && oe < static_cast<int>(left))) {
+      const int at = og + min(oe, static_cast<int>(left));
+      put(a, j, g, k.s0 + at, table[p_first + i], p_first + i);
+    }
+    og += key[i] > prefix;
+    oe += is_eq;
+  }
+  cluster.sync();                             // shared memory stays until every reader is done
+}
+
+// Every candidate is listed.
+template <int NT>
+__device__ void pick_all(const PageSelectArgs &a, int rank, int C, int j, int g, const Block &k) {
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages;
+  for (int i = rank * NT + threadIdx.x; i < k.picked; i += C * NT)
+    put(a, j, g, k.s0 + i, table[k.s0 + i], k.s0 + i);
+}
+
+// Few rows (a decode step's): a thread takes a page, its digest in registers, and the rows'
+// integers come from shared memory, the same word for the whole warp.
+constexpr int kFewThreads = 256, kFewRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSelectArgs a) {
+  constexpr int W = D / 4;                    // words of a row's integers
+  extern __shared__ uint32_t s_key[];         // [a.slice]
+  __shared__ __align__(16) int s_neg[kFewRows][W], s_pos[kFewRows][W];
+  __shared__ float s_unit[kFewRows];
+  __shared__ SelectShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = blockIdx.x / C, j = item / a.H_kv, g = item % a.H_kv;
+  grid_dep_wait();
+  const Block k = find_block<kFewThreads>(a, j, sh.scan, sh.found);
+  if (rank == 0) put_fixed<kFewThreads>(a, j, g, k);
+  const int n = k.first - k.s0;               // candidates
+  if (k.picked == n || k.picked == 0) {       // (the same for the whole cluster)
+    pick_all<kFewThreads>(a, rank, C, j, g, k);
+    return;
+  }
+  for (int i = tid; i < 4 * 256; i += kFewThreads) sh.hist[0][i] = 0;
+  const int R = k.n * (a.H_q / a.H_kv);
+  for (int r = warp; r < (R + 3) / 4 * 4; r += kFewThreads / 32) {   // to a multiple of 4, with copies of row 0
+    constexpr int E = D / 32;
+    float x[E];
+    const int e = row_of<D>(a, k, g, r < R ? r : 0, x);
+    const float inv = two_to(-e);
+    uint32_t pos = 0, neg = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int v = whole(x[i] * inv);
+      pos |= (static_cast<uint32_t>(max(v, 0)) & 0xffu) << (8 * i);
+      neg |= (static_cast<uint32_t>(min(v, 0)) & 0xffu) << (8 * i);
+    }
+    if constexpr (E == 4) {
+      s_pos[r][lane] = static_cast<int>(pos);
+      s_neg[r][lane] = static_cast<int>(neg);
+    } else {
+      reinterpret_cast<uint16_t *>(s_pos[r])[lane] = static_cast<uint16_t>(pos);
+      reinterpret_cast<uint16_t *>(s_neg[r])[lane] = static_cast<uint16_t>(neg);
+    }
+    if (lane == 0) s_unit[r] = two_to(e);
+  }
+  __syncthreads();
+  const int per = (n + C - 1) / C;
+  const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
+  for (int i = tid; i < nl; i += kFewThreads) {
+    const int page = table[i];
+    DSA_CHECK(page >= 0 && page < a.n_pages);
+    uint32_t key = 0;                         // no page: below every score
+    if (page >= 0 && page < a.n_pages) {
+      const size_t row = static_cast<size_t>(page) * a.H_kv + g;
+      const int4 *src = reinterpret_cast<const int4 *>(a.bounds + row * 2 * D);
+      int4 lo[W / 4], hi[W / 4];
+#pragma unroll
+      for (int w = 0; w < W / 4; ++w) lo[w] = __ldg(src + w);
+#pragma unroll
+      for (int w = 0; w < W / 4; ++w) hi[w] = __ldg(src + W / 4 + w);
+      const int e = a.exp[row];
+      float best = -INFINITY;
+      for (int r = 0; r < R; r += 4) {
+        int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < W / 4; ++w) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int4 u = *reinterpret_cast<const int4 *>(&s_neg[r + x][4 * w]);
+            const int4 v = *reinterpret_cast<const int4 *>(&s_pos[r + x][4 * w]);
+            acc[x] = __dp4a(u.x, lo[w].x, acc[x]);
+            acc[x] = __dp4a(u.y, lo[w].y, acc[x]);
+            acc[x] = __dp4a(u.z, lo[w].z, acc[x]);
+            acc[x] = __dp4a(u.w, lo[w].w, acc[x]);
+            acc[x] = __dp4a(v.x, hi[w].x, acc[x]);
+            acc[x] = __dp4a(v.y, hi[w].y, acc[x]);
+            acc[x] = __dp4a(v.z, hi[w].z, acc[x]);
+            acc[x] = __dp4a(v.w, hi[w].w, acc[x]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) best = fmaxf(best, static_cast<float>(acc[x]) * s_unit[r + x]);
+      }
+      key = ordered_key(best * two_to(e));
+    }
+    s_key[i] = key;
+  }
+  __syncthreads();
+  pick<kFewThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
+}
+
+// Many rows (a chunk's blocks): the products on the tensor cores, the integers as fp16, pages in
+// tiles of 64 that are widened once for all rows.
+constexpr int kManyThreads = 512, kManyWarps = kManyThreads / 32, kManyRows = 256, kTilePages = 64;
+
+// four signed bytes -> fp16 pairs (exact): 1024 + (x + 128) has x + 128 in its low mantissa bits
+__device__ __forceinline__ uint2 widen_s8(uint32_t w) {
+  w ^= 0x80808080u;
+  uint32_t lo, hi;
+  asm("prmt.b32 %0, %1, %2, 0x4140;\n" : "=r"(lo) : "r"(w), "r"(0x64646464u));
+  asm("prmt.b32 %0, %1, %2, 0x4342;\n" : "=r"(hi) : "r"(w), "r"(0x64646464u));
+  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(lo) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(hi) : "r"(0x64806480u));
+  return make_uint2(lo, hi);
+}
+
+template <int D>
+struct Many {
+  static constexpr int kPitch = 4 * D + 16;                    // bytes of a widened digest row (2 D fp16, padded)
+  static constexpr int oTile = 0;                              // [2][kTilePages] of them
+  static constexpr int oQ = oTile + 2 * kTilePages * kPitch;   // [kManyRows][D] int8
+  static constexpr int oUnit = oQ + kManyRows * D;             // [kManyRows] 2^e_q
+  static constexpr int oExp = oUnit + kManyRows * 4;           // [2][kTilePages] 2^e
+  static constexpr int oKey = oExp + 2 * kTilePages * 4;       // [slice]
+};
+
+// RW warps share the rows, 16 each, and 16 / RW warps the pages of a tile.
+template <int D, int RW>
+__global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const PageSelectArgs a) {
+  using M = Many<D>;
+  constexpr int NT8 = RW / 2;                 // 8-page columns of a tile per warp
+  constexpr int KS = 2 * D / 16;              // steps of a product
+  extern __shared__ __align__(16) unsigned char sm[];
+  __shared__ SelectShared sh;
+  float *s_unit = reinterpret_cast<float *>(sm + M::oUnit), *s_exp = reinterpret_cast<float *>(sm + M::oExp);
+  uint32_t *s_key = reinterpret_cast<uint32_t *>(sm + M::oKey);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = blockIdx.x / C, j = item / a.H_kv, g = item % a.H_kv;
+  grid_dep_wait();
+  const Block k = find_block<kManyThreads>(a, j, sh.scan, sh.found);
+  if (rank == 0) put_fixed<kManyThreads>(a, j, g, k);
+  const int n = k.first - k.s0;
+  if (k.picked == n || k.picked == 0) {
+    pick_all<kManyThreads>(a, rank, C, j, g, k);
+    return;
+  }
+  for (int i = tid; i < 4 * 256; i += kManyThreads) sh.hist[0][i] = 0;
+  const int per = (n + C - 1) / C;
+  const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
+  for (int i = tid; i < nl; i += kManyThreads) s_key[i] = 0;
+  const int R = k.n * (a.H_q / a.H_kv);
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
+  const int tiles = (nl + kTilePages - 1) / kTilePages;
+  const int rw = warp % RW, split = warp / RW;
+  const int gq = lane >> 2, t = lane & 3;
+
+  // this thread's part of a tile: 4 D bytes of 512 threads over 64 pages
+  constexpr int TPP = kManyThreads / kTilePages, V = 2 * D / TPP / 16;   // threads per page, 16-byte pieces each
+  const int my = tid / TPP, part = tid % TPP;
+  uint4 dig[V];
+  float my_exp = 0.f;
+  auto fetch = [&](int tile) {
+    const int i = tile * kTilePages + my;
+    int page = -1;
+    if (i < nl) page = table[i];
+    DSA_CHECK(i >= nl || (page >= 0 && page < a.n_pages));
+    const bool ok = page >= 0 && page < a.n_pages;
+    const size_t row = static_cast<size_t>(ok ? page : 0) * a.H_kv + g;
+    my_exp = 0.f;                             // (2^e is never 0: none)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      dig[v] = ok ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + row * 2 * D) + part * V + v) : make_uint4(0, 0, 0, 0);
+    if (ok) my_exp = two_to(a.exp[row]);
+  };
+  auto store = [&](int buf) {
+    unsigned char *dst = sm + M::oTile + (buf * kTilePages + my) * M::kPitch + part * V * 32;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint2 x = widen_s8(dig[v].x), y = widen_s8(dig[v].y), z = widen_s8(dig[v].z), w = widen_s8(dig[v].w);
+      reinterpret_cast<uint4 *>(dst)[2 * v] = make_uint4(x.x, x.y, y.x, y.y);
+      reinterpret_cast<uint4 *>(dst)[2 * v + 1] = make_uint4(z.x, z.y, w.x, w.y);
+    }
+    if (part == 0) s_exp[buf * kTilePages + my] = my_exp;
+  };
+
+  for (int r0 = 0; r0 < R; r0 += RW * 16) {
+    const int rows = min(RW * 16, R - r0);
+    __syncthreads();                          // the rows before are read
+    for (int r = warp; r < rows; r += kManyWarps) {
+      constexpr int E = D / 32;
+      float x[E];
+      const int e = row_of<D>(a, k, g, r0 + r, x);
+      const float inv = two_to(-e);
+      uint32_t v = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) v |= (static_cast<uint32_t>(whole(x[i] * inv)) & 0xffu) << (8 * i);
+      if constexpr (E == 4) reinterpret_cast<uint32_t *>(sm + M::oQ + r * D)[lane] = v;
+      else reinterpret_cast<uint16_t *>(sm + M::oQ + r * D)[lane] = static_cast<uint16_t>(v);
+      if (lane == 0) s_unit[r] = two_to(e);
+    }
+    fetch(0);
+    store(0);
+    __syncthreads();
+    // A: the rows' integers below zero against lo, those above against hi
+    uint32_t af[KS][4];
+    const int ra = rw * 16 + gq, rb = ra + 8;
+    const bool va = ra < rows, vb = rb < rows;
+    auto pair = [&](int r, bool ok, int d, bool pos) -> uint32_t {
+      if (!ok) return 0u;
+      const char2 c = *reinterpret_cast<const char2 *>(sm + M::oQ + r * D + d);
+      const int x = pos ? max(static_cast<int>(c.x), 0) : min(static_cast<int>(c.x), 0);
+      const int y = pos ? max(static_cast<int>(c.y), 0) : min(static_cast<int>(c.y), 0);
+      return pack_f16x2(static_cast<float>(x), static_cast<float>(y));
+    };
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const bool pos = ks >= KS / 2;
+      const int d = (ks % (KS / 2)) * 16 + 2 * t;
+      af[ks][0] = pair(ra, va, d, pos);
+      af[ks][1] = pair(rb, vb, d, pos);
+      af[ks][2] = pair(ra, va, d + 8, pos);
+      af[ks][3] = pair(rb, vb, d + 8, pos);
+    }
+    const float ua = va ? s_unit[ra] : 0.f, ub = vb ? s_unit[rb] : 0.f;
+    const bool live = rw * 16 < rows;         // the warp has rows
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int buf = tile & 1;
+      if (tile + 1 < tiles) fetch(tile + 1);
+      if (live) {
+        float acc[NT8][4];
+#pragma unroll
+        for (int c = 0; c < NT8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+        const unsigned char *base = sm + M::oTile + (buf * kTilePages + split * NT8 * 8 + (lane & 7)) * M::kPitch + (lane >> 3) * 16;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+#pragma unroll
+          for (int c = 0; c < NT8; ++c) {
+            uint32_t bf[4];
+            ldsm_x4(bf, base + c * 8 * M::kPitch + ks * 32);
+            mma_16816_f16(acc[c], af[ks], bf[0], bf[1]);
+            mma_16816_f16(acc[c], af[ks + 1], bf[2], bf[3]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NT8; ++c) {
+          float x = -INFINITY, y = -INFINITY;   // columns 2 t, 2 t + 1 over the warp's rows
+          if (va) {
+            x = acc[c][0] * ua;
+            y = acc[c][1] * ua;
+          }
+          if (vb) {
+            x = fmaxf(x, acc[c][2] * ub);
+            y = fmaxf(y, acc[c][3] * ub);
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+            y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
+          }
+          if (gq == c) {
+            const int col = (split * NT8 + c) * 8 + 2 * t, i = tile * kTilePages + col;
+            const float ex = s_exp[buf * kTilePages + col], ey = s_exp[buf * kTilePages + col + 1];
+            if (i < nl && ex > 0.f) atomicMax(&s_key[i], ordered_key(x * ex));
+            if (i + 1 < nl && ey > 0.f) atomicMax(&s_key[i + 1], ordered_key(y * ey));
+          }
+        }
+      }
+      if (tile + 1 < tiles) store(buf ^ 1);
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  pick<kManyThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
+}
+
+template <typename Kern>
+cudaError_t launch_cluster(Kern kern, int items, int C, int threads, size_t smem, cudaStream_t s, const PageSelectArgs &a) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items) * C);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  ProfScope ps("page_select", s);
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int D>
+cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
+  const int items = a.n_blocks * a.H_kv, rows = a.cfg.q_block * (a.H_q / a.H_kv);
+  const bool few = rows <= kFewRows;
+  // CTAs of an item: until the launch has two per SM, or a CTA a page per thread
+  const int least = few ? kFewThreads : 2 * kTilePages;
+  int C = 1;
+  while (C < 16 && items * C < 152 && a.max_pages > C * least) C *= 2;
+  a.slice = (a.max_pages + C - 1) / C;
+  while (C < 16 && a.slice > kSelectMaxPages / 16) {
+    C *= 2;
+    a.slice = (a.max_pages + C - 1) / C;
+  }
+  const size_t keys = static_cast<size_t>(a.slice) * 4;
+  if (few) return launch_cluster(select_few_kernel<D>, items, C, kFewThreads, keys, s, a);
+  const size_t smem = Many<D>::oKey + keys;
+  if (rows <= 32) return launch_cluster(select_many_kernel<D, 2>, items, C, kManyThreads, smem, s, a);
+  if (rows <= 64) return launch_cluster(select_many_kernel<D, 4>, items, C, kManyThreads, smem, s, a);
+  if (rows <= 128) return launch_cluster(select_many_kernel<D, 8>, items, C, kManyThreads, smem, s, a);
+  return launch_cluster(select_many_kernel<D, 16>, items, C, kManyThreads, smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_page_digest(const DigestArgs &a0, cudaStream_t s) {
+  DigestArgs a = a0;
+  while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
+  // token rows per CTA: a page's worth in a long chunk, fewer where each row may be a page of its
+  // own and the launch would not fill the GPU
+  a.window = 1;
+  while (a.window < kMaxWindow && a.window < a.page_size && a.n_tok / (2 * a.window) >= 152) a.window *= 2;
+  const dim3 grid((a.n_tok + a.window - 1) / a.window, (a.H_kv + kDigestWarps - 1) / kDigestWarps);
+  ProfScope ps("page_digest", s);
+  if (a.fp8)
+    return a.D == 128 ? launch_pdl(digest_kernel<128, true>, grid, dim3(kDigestThreads), 0, s, a)
+                      : launch_pdl(digest_kernel<64, true>, grid, dim3(kDigestThreads), 0, s, a);
+  return a.D == 128 ? launch_pdl(digest_kernel<128, false>, grid, dim3(kDigestThreads), 0, s, a)
+                    : launch_pdl(digest_kernel<64, false>, grid, dim3(kDigestThreads), 0, s, a);
+}
+
+cudaError_t launch_page_select(const PageSelectArgs &a0, cudaStream_t s) {
+  PageSelectArgs a = a0;
+  while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
+  return a.D == 128 ? launch_select_d<128>(a, s) : launch_select_d<64>(a, s);
+}
+
+}  // namespace dsa

@@ -219,6 +219,7 @@ struct Args {
   float *part_ml;        // [2 * max_ctas][part_rows][2]
   PagedPiece *piece;     // [max_ctas]
   int B, n_tok, max_pages, n_pages, page_size, lg_page, H_q, H_kv, G, TT;
+  long long table_b, table_g;   // entries of page_table between sequences, between KV heads (0: one table)
   int TE;                // tokens of an entry: two query tiles' (FEW: one's)
   int part_rows;
   int n_sink, n_stream;  // n_stream < 0: no window
@@ -355,6 +356,11 @@ __device__ __forceinline__ void walk_settle(const Args &a, Walk &w) {
 __device__ __forceinline__ void walk_next(const Args &a, Walk &w) {
   w.u0 = max(w.u0, w.item_u0 + units_of(w.e.n, w.e.u));   // this item is done
   walk_settle(a, w);
+}
+
+// the page table of a piece's sequence (and KV head)
+__device__ __forceinline__ const int32_t *table_of(const Args &a, const Item &it) {
+  return a.page_table + it.b * a.table_b + it.g * a.table_g;
 }
 
 // first key of tile k of a piece
@@ -525,7 +531,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return __vcmpgeu2(w
 template <int D, bool FP8, class Add>
 __device__ __forceinline__ void add_lost(const Args &a, const Item &it, int first, int n_rows, int i, Add add) {
   const int lane = threadIdx.x & 31;
-  const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+  const int32_t *table = table_of(a, it);
   const int col = (lane % (D / 4)) * 4;
 #pragma unroll 1
   for (int k = 0; k < it.T; ++k) {
@@ -1038,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
                         it.tok0 + (FEW ? 0 : t * a.TT), 0);
       }
       __syncwarp();
-      const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+      const int32_t *table = table_of(a, it);
       // the page of this lane's part of tile k (n_pages: none, reads as zero)
       auto page_of = [&](int k) -> int {
         int page = a.n_pages;
@@ -1457,7 +1463,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, FEW>::kThreads, 1) paged_attn_kern
         const int T = it.T;
         // the row's page two tiles ahead and its scale byte one tile ahead of the conversion,
         // so that neither load's latency is waited for
-        const int32_t *table = a.page_table + static_cast<size_t>(it.b) * a.max_pages;
+        const int32_t *table = table_of(a, it);
         const uint8_t *scales = values ? a.v_scale : a.k_scale;
         auto page_of = [&](int k) -> int {
           const int pos = tile_base(it, k) + r;
@@ -1806,6 +1812,8 @@ cudaError_t launch_d(const PagedAttnArgs &pa, cudaStream_t s) {
   a.B = pa.B;
   a.n_tok = pa.n_tok;
   a.max_pages = pa.max_pages;
+  a.table_b = static_cast<long long>(pa.max_pages) * (pa.per_head ? pa.H_kv : 1);
+  a.table_g = pa.per_head ? pa.max_pages : 0;
   a.n_pages = pa.n_pages;
   a.page_size = pa.page_size;
   while ((1 << a.lg_page) < pa.page_size) ++a.lg_page;

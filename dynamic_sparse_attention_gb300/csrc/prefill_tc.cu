@@ -910,9 +910,10 @@ extern "C" int dsa_device_error(int *code) {
   if (pg < 0) return fail(DSA_ERR_CUDA, "reading the paged attention's device error word");
   // checked builds: out-of-range device-side inputs met by the kernels
   int chk = 0;
-  const int words[7] = {decode_check_word(),     decode_mma_check_word(), hip_select_check_word(),
-                        stage_tc_check_word(),   prefill_tc_check_word(), kv_cache_check_word(),
-                        paged_attn_check_word()};
+  const int words[10] = {decode_check_word(),     decode_mma_check_word(), hip_select_check_word(),
+                         stage_tc_check_word(),   prefill_tc_check_word(), kv_cache_check_word(),
+                         paged_attn_check_word(), kv_rope_check_word(),    page_select_check_word(),
+                         page_copy_check_word()};
   for (int x : words) {
     if (x < 0) return fail(DSA_ERR_CUDA, "reading a device check word");
     chk |= x;

@@ -18,8 +18,15 @@
  *   cache  : kv_cache_write      -- new keys and values into a paged cache, as bf16 or
  *                                   quantised to FP8
  *            kv_cache_read       -- pages back into contiguous bf16
+ *            kv_cache_write_rope -- the same write with the norm of each head and the
+ *                                   rotation by position on the way, for the queries too
  *            paged_attn          -- attention of chunks of new tokens (or single tokens)
  *                                   over the cache, optionally window + sinks only
+ *            page_digest_update  -- 8-bit channel bounds of the keys of each page
+ *            page_select         -- the pages that each block of queries attends, by a
+ *                                   bound on their scores made from the digests
+ *            paged_attn_lists    -- paged_attn over a list of pages for each KV head
+ *            kv_pages_copy       -- pages onto others (forks, compactions)
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers owned by the caller.  Layouts are
@@ -495,6 +502,111 @@ int paged_attn(const void *q, long long q_stride, const void *k_pages, const voi
                const int32_t *kv_len, const int32_t *page_table, const dsa_paged_shape *shape,
                int n_sink, int n_stream, float scale, void *out, float *lse, void *ws,
                size_t ws_bytes, void *stream);
+
+/* Head norm and rotation of kv_cache_write_rope.
+ *   q_weight, k_weight [D]   bf16 (weight_f32 = 0) or fp32 (1); NULL: that side has no norm
+ *   eps      added to the mean square, >= 0 and finite
+ *   inv_freq [rot / 2] fp64  radians per position of each pair; rot: rotated dimensions, a
+ *            multiple of 16 in [0, D] (0: no rotation, inv_freq is not read)
+ *   interleaved   0: pairs are dimensions (i, i + rot / 2), 1: (2 i, 2 i + 1)
+ *   rope_scale    factor of cosine and sine, finite (1 for a plain rotation) */
+typedef struct {
+  const void *q_weight, *k_weight;
+  int weight_f32;
+  float eps;
+  const double *inv_freq;
+  int rot, interleaved;
+  float rope_scale;
+} dsa_rope_cfg;
+
+/* kv_cache_write_rope -- kv_cache_write with what comes before it in one pass: each head of q and
+ * k_new, x [D], becomes y = x * rsqrt(mean(x^2) + eps) * weight, its first `rot` dimensions are
+ * rotated by the token's position p (the one that kv_cache_write stores it at):
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) * rope_scale, angle p * inv_freq[i],
+ * and queries go to q_out [n_tok, H_q, D] bf16 (qo_stride elements between tokens), keys to their
+ * pages, values to theirs as kv_cache_write has them.  All of it in fp32 with one rounding at the
+ * end (an FP8 cache is quantised from the fp32 values); angles are held as 64-bit fractions of a
+ * turn, so far positions lose nothing.  q_out may be q itself (same pointer and stride).  A token
+ * whose page is no page still gets its query; tokens outside every chunk are left alone.
+ * Errors: INVALID_ARG / UNSUPPORTED (shape, strides, cfg), ALIGNMENT, CUDA. */
+int kv_cache_write_rope(const void *q, long long q_stride, const void *k_new, long long k_stride,
+                        const void *v_new, long long v_stride, const int32_t *q_start,
+                        const int32_t *kv_len, const int32_t *page_table,
+                        const dsa_paged_shape *shape, const dsa_rope_cfg *cfg, void *q_out,
+                        long long qo_stride, void *k_pages, void *v_pages, uint8_t *k_scale,
+                        uint8_t *v_scale, void *stream);
+
+/* page_digest_update -- the digests of the pages that the chunks touch (those that hold a
+ * position of rows q_start[b] .. q_start[b+1]-1), over all of their keys below kv_len[b]:
+ *   bounds [n_pages, H_kv, 2, D] int8   lo_d = floor(min_t k_d * 2^-e), hi_d = ceil(max_t k_d *
+ *          2^-e), kept in [-127, 127]: k_d lies in [lo_d, hi_d] * 2^e
+ *   exp    [n_pages, H_kv] int8         e, the least integer in [-50, 50] with a * 2^-e <= 127 for
+ *          a = the page's largest finite magnitude of this head (0 if a is 0)
+ * An infinity counts as the largest of its sign, a NaN as nothing (bounds 0 where nothing else
+ * is).  Pages of the table that no chunk touches keep their digests.  bounds 16-byte aligned.
+ * shape->n_tok bounds the rows of the chunks; H_q is not used but checked. */
+int page_digest_update(const void *k_pages, const uint8_t *k_scale, const int32_t *q_start,
+                       const int32_t *kv_len, const int32_t *page_table,
+                       const dsa_paged_shape *shape, int8_t *bounds, int8_t *exp, void *stream);
+
+/* What page_select lists: the first n_sink pages, the `keep` best of those behind them, the
+ * n_local pages before the block's own ones, and those.  One list for q_block tokens. */
+typedef struct {
+  int keep, n_sink, n_local, q_block;
+} dsa_page_select_cfg;
+
+/* Blocks of queries (n_blocks = (n_tok + B (q_block - 1)) / q_block, at least as many as there
+ * are) and entries of a list (max_list = n_sink + keep + n_local + the most pages that a block's
+ * own tokens lie in) of a page_select call; host only. */
+int page_select_sizes(const dsa_paged_shape *shape, const dsa_page_select_cfg *cfg, int *n_blocks,
+                      int *max_list);
+
+/* page_select -- which pages each block of queries attends.  The rows of a chunk are cut into
+ * blocks of q_block tokens (the last one of a sequence may be shorter).  For a block whose tokens
+ * stand at positions p0 .. p1, with pages own0 = p0 / page_size .. own1 = p1 / page_size and first =
+ * max(0, own0 - n_local), every KV head lists, ascending,
+ *   pages 0 .. min(n_sink, first) - 1,
+ *   of pages min(n_sink, first) .. first - 1 the `keep` with the largest scores (ties: the
+ *     earlier page; all of them if there are no more), and
+ *   pages first .. own1.
+ * Score of a page: the largest over the block's tokens and the KV head's query heads of
+ *   2^(e_q + e) * sum_d max(q'_d lo_d, q'_d hi_d),  q' = rint(q * 2^-e_q) in [-127, 127],
+ * with e_q the least integer in [-50, 50] that keeps the row's finite q there (0 for zeros; a NaN
+ * counts as 0), lo, hi and e the page's digest: an upper bound of q' . k.  The sums are whole
+ * numbers below 2^21, so scores, and with them the lists, are the same in any order of summation.
+ *   q      [n_tok, H_q, D] bf16, q_stride elements between tokens
+ *   sel_q_start [n_blocks + 1], sel_kv_len [n_blocks], sel_table [n_blocks, H_kv, max_list]: the
+ *          blocks as sequences of their own for paged_attn_lists: their rows, the keys of their
+ *          lists up to the last token's, and the lists as page ids (-1 behind their end).  Blocks
+ *          behind the last one hold no rows and no keys
+ *   sel_index [n_blocks, H_kv, max_list]  the lists as places in the sequence's table (NULL to
+ *          skip), -1 behind their end
+ * A page outside [0, n_pages) scores lowest.  q_block in [1, 256], max_pages <= 262144, n_blocks <=
+ * 4096, else UNSUPPORTED.  shape->dtype is not used but checked. */
+int page_select(const void *q, long long q_stride, const int8_t *bounds, const int8_t *exp,
+                const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
+                const dsa_paged_shape *shape, const dsa_page_select_cfg *cfg, int32_t *sel_q_start,
+                int32_t *sel_kv_len, int32_t *sel_table, int32_t *sel_index, void *stream);
+
+/* paged_attn_lists -- paged_attn with a list of pages for each KV head: page_table [B, H_kv,
+ * max_pages], the lists of page_select or others.  Positions, kv_len, n_sink and n_stream are
+ * those of the list: entry i holds positions i * page_size .. .  Everything else as paged_attn
+ * (workspace: paged_attn_workspace of the same shape). */
+int paged_attn_lists(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
+                     const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *q_start,
+                     const int32_t *kv_len, const int32_t *page_table, const dsa_paged_shape *shape,
+                     int n_sink, int n_stream, float scale, void *out, float *lse, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* kv_pages_copy -- page dst[i] becomes page src[i], for i < n: keys, values, the scales of an FP8
+ * cache and, unless NULL, the digests.  src, dst [n] int32 on the device.  Pairs with an entry
+ * outside [0, n_pages) are skipped.  A page may be the source of many copies, but stands in dst at
+ * most once, and no page of dst stands in src (its copies else have several contents to choose
+ * from).  shape: n_pages, page_size, H_kv, D and dtype are used, the rest is checked.
+ * n in [0, 2^24]. */
+int kv_pages_copy(const int32_t *src, const int32_t *dst, int n, const dsa_paged_shape *shape,
+                  void *k_pages, void *v_pages, uint8_t *k_scale, uint8_t *v_scale, int8_t *bounds,
+                  int8_t *exp, void *stream);
 
 /* ------------------------------------------------------------------ timing */
 

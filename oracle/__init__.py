@@ -15,6 +15,8 @@ Modules:
            block/column format, and sparse causal prefill attention.
   patterns -- MInference A-shape (static initial blocks + diagonal band) and
            Block-Sparse (mean-pooled block attention, top-k_b blocks) lists.
+  paged -- the paged cache (write, read back) and the attention over it.
+  pages -- norm and rotation on the way into the cache, page digests, page selection.
   numerics -- exact widening of the stored bit patterns to float64.
 
 Pinning status (what each function is checked against) is listed in the
