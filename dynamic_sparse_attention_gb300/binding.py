@@ -148,8 +148,8 @@ _SIGNATURES = {
 def device_error() -> int:
     """Read and clear the library's device error words: 0 = none; bit 0 / bit 1: a
     prefill-attention / vertical-slash-estimate CTA gave up a wait; bit 2 (checked
-    build): a kernel met out-of-range device-side input; bit 3: a paged-attention CTA gave
-    up a wait."""
+    build): a kernel met out-of-range device-side input; bit 3 / bit 4: a paged-attention /
+    page-selection CTA gave up a wait."""
     lib = load()
     c = _c_int()
     st = lib.dsa_device_error(ctypes.byref(c))

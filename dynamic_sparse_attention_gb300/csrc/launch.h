@@ -307,11 +307,15 @@ struct PageSelectArgs {
   dsa_page_select_cfg cfg;
   int n_blocks, max_list;
   int32_t *sel_q_start, *sel_kv_len, *sel_table, *sel_index;
-  int lg_page, slice;                  // (launcher) log2 of page_size, keys a CTA has room for
+  // (launcher) log2 of page_size, scores a CTA has room for, rows it holds at a time, limit of a wait
+  int lg_page, slice, rows;
+  unsigned long long wait_ns;
 };
 constexpr int kSelectMaxPages = 262144;
 cudaError_t launch_page_select(const PageSelectArgs &a, cudaStream_t s);
 int page_select_check_word();
+int page_select_device_error();
+void page_select_set_wait_limit(unsigned long long ns);
 
 // Copies of pages (page_copy.cu).
 struct PageCopyArgs {

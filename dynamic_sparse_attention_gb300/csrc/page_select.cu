@@ -14,10 +14,14 @@
 // (2 D + 1 bytes a page and head), a prompt chunk's by the products.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
 #include "profile.h"
+#include "tc_ptx.cuh"
 
 namespace dsa {
 
@@ -26,6 +30,11 @@ DSA_CHECK_WORD(page_select_check_word)
 namespace cg = cooperative_groups;
 
 namespace {
+
+using namespace tc;
+
+static __device__ int g_select_error;   // sticky error word, read by dsa_device_error
+std::atomic<unsigned long long> g_wait_limit_ns{500000000ull};   // of later launches
 
 // ------------------------------------------------------------------ digests
 
@@ -542,9 +551,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
   pick<kFewThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
 }
 
-// Many rows (a chunk's blocks): the products on the tensor cores, the integers as fp16, pages in
-// tiles of 64 that are widened once for all rows.
-constexpr int kManyThreads = 512, kManyWarps = kManyThreads / 32, kManyRows = 256, kTilePages = 64;
+// Many rows (a chunk's blocks): the products on tcgen05, the integers as fp16.  Pages lie on the
+// TMEM lanes (M = 128) and the block's rows on its columns (N = up to 256), so a thread owns a page
+// and takes the largest score of its row of columns without talking to another.  The rows' integers
+// stay in shared memory, those below zero against lo and those above against hi (K = 2 D); digests
+// come in tiles of 128 pages, widened to fp16 on their way into a ring of 64-element steps of K.
+constexpr int kManyConv = 8, kManyEpi = 8;                       // warps: epilogue, MMA issuer, converters
+constexpr int kManyThreads = (kManyEpi + 1 + kManyConv) * 32;
+constexpr int kTilePages = 128, kSlots = 4;
+constexpr uint32_t kSlotBytes = kTilePages * 128;
 
 // four signed bytes -> fp16 pairs (exact): 1024 + (x + 128) has x + 128 in its low mantissa bits
 __device__ __forceinline__ uint2 widen_s8(uint32_t w) {
@@ -557,26 +572,46 @@ __device__ __forceinline__ uint2 widen_s8(uint32_t w) {
   return make_uint2(lo, hi);
 }
 
-template <int D>
-struct Many {
-  static constexpr int kPitch = 4 * D + 16;                    // bytes of a widened digest row (2 D fp16, padded)
-  static constexpr int oTile = 0;                              // [2][kTilePages] of them
-  static constexpr int oQ = oTile + 2 * kTilePages * kPitch;   // [kManyRows][D] int8
-  static constexpr int oUnit = oQ + kManyRows * D;             // [kManyRows] 2^e_q
-  static constexpr int oExp = oUnit + kManyRows * 4;           // [2][kTilePages] 2^e
-  static constexpr int oKey = oExp + 2 * kTilePages * 4;       // [slice]
-};
+// The whole warp waits, at most `limit` ns; the outcome is warp-uniform.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit) {
+  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+  do {
+    if (__any_sync(kFull, *abort || global_ns() - t0 > limit)) {
+      *abort = 1;
+      return false;
+    }
+  } while (!__all_sync(kFull, mbar_try_wait(bar, parity)));
+  return true;
+}
 
-// RW warps share the rows, 16 each, and 16 / RW warps the pages of a tile.
-template <int D, int RW>
+// Shared memory of a launch whose CTAs hold `rows` rows (a multiple of 64, at most 256) at a time.
+struct ManyLayout {
+  uint32_t oSlots, oUnit, oBar, oShared, oKey;
+};
+__host__ __device__ inline ManyLayout many_layout(int D, int rows) {
+  ManyLayout m;
+  m.oSlots = static_cast<uint32_t>(rows) * 4 * D;               // rows of 2 D fp16, in blocks of 64
+  m.oUnit = m.oSlots + kSlots * kSlotBytes;
+  m.oBar = m.oUnit + rows * 4;
+  m.oShared = m.oBar + 256;
+  m.oKey = m.oShared + (sizeof(SelectShared) + 15) / 16 * 16;
+  return m;
+}
+
+template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const PageSelectArgs a) {
-  using M = Many<D>;
-  constexpr int NT8 = RW / 2;                 // 8-page columns of a tile per warp
-  constexpr int KS = 2 * D / 16;              // steps of a product
-  extern __shared__ __align__(16) unsigned char sm[];
-  __shared__ SelectShared sh;
-  float *s_unit = reinterpret_cast<float *>(sm + M::oUnit), *s_exp = reinterpret_cast<float *>(sm + M::oExp);
-  uint32_t *s_key = reinterpret_cast<uint32_t *>(sm + M::oKey);
+  constexpr int KB = 2 * D / 64;              // 64-element steps of K
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const int RN = a.rows;                      // rows held at a time
+  const ManyLayout L = many_layout(D, RN);
+  SelectShared &sh = *reinterpret_cast<SelectShared *>(sm + L.oShared);
+  float *s_unit = reinterpret_cast<float *>(sm + L.oUnit);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L.oBar), *empty = full + kSlots, *d_full = empty + kSlots,
+           *d_empty = d_full + 2, *drained = d_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+  volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint32_t *s_key = reinterpret_cast<uint32_t *>(sm + L.oKey);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -596,127 +631,182 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   const int R = k.n * (a.H_q / a.H_kv);
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
   const int tiles = (nl + kTilePages - 1) / kTilePages;
-  const int rw = warp % RW, split = warp / RW;
-  const int gq = lane >> 2, t = lane & 3;
-
-  // this thread's part of a tile: 4 D bytes of 512 threads over 64 pages
-  constexpr int TPP = kManyThreads / kTilePages, V = 2 * D / TPP / 16;   // threads per page, 16-byte pieces each
-  const int my = tid / TPP, part = tid % TPP;
-  uint4 dig[V];
-  float my_exp = 0.f;
-  auto fetch = [&](int tile) {
-    const int i = tile * kTilePages + my;
-    int page = -1;
-    if (i < nl) page = table[i];
-    DSA_CHECK(i >= nl || (page >= 0 && page < a.n_pages));
-    const bool ok = page >= 0 && page < a.n_pages;
-    const size_t row = static_cast<size_t>(ok ? page : 0) * a.H_kv + g;
-    my_exp = 0.f;                             // (2^e is never 0: none)
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      dig[v] = ok ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + row * 2 * D) + part * V + v) : make_uint4(0, 0, 0, 0);
-    if (ok) my_exp = two_to(a.exp[row]);
-  };
-  auto store = [&](int buf) {
-    unsigned char *dst = sm + M::oTile + (buf * kTilePages + my) * M::kPitch + part * V * 32;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint2 x = widen_s8(dig[v].x), y = widen_s8(dig[v].y), z = widen_s8(dig[v].z), w = widen_s8(dig[v].w);
-      reinterpret_cast<uint4 *>(dst)[2 * v] = make_uint4(x.x, x.y, y.x, y.y);
-      reinterpret_cast<uint4 *>(dst)[2 * v + 1] = make_uint4(z.x, z.y, w.x, w.y);
+  const uint32_t cols = RN <= 64 ? 128u : RN <= 128 ? 256u : 512u;   // TMEM: two buffers
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], kManyConv);
+      mbar_init(&empty[s], 1);
     }
-    if (part == 0) s_exp[buf * kTilePages + my] = my_exp;
-  };
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&d_full[s], 1);
+      mbar_init(&d_empty[s], kManyEpi);
+    }
+    mbar_init(drained, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kManyEpi) {
+    tmem_alloc(tmem_slot, cols);
+    tmem_relinquish();
+  }
+  // what a role carries over from one set of rows to the next
+  Ring<kSlots> ring;
+  Ring<2> buf;
+  bool ok = true;
 
-  for (int r0 = 0; r0 < R; r0 += RW * 16) {
-    const int rows = min(RW * 16, R - r0);
-    __syncthreads();                          // the rows before are read
-    for (int r = warp; r < rows; r += kManyWarps) {
+  for (int r0 = 0; r0 < R; r0 += RN) {
+    __syncthreads();                          // the rows before are read (and the barriers are there)
+    const int rows = min(RN, R - r0);
+    const int rn = (rows + 63) & ~63;         // columns in use; those behind the last row repeat it
+    for (int r = warp; r < rn; r += kManyThreads / 32) {
       constexpr int E = D / 32;
       float x[E];
-      const int e = row_of<D>(a, k, g, r0 + r, x);
+      const int e = row_of<D>(a, k, g, r0 + min(r, rows - 1), x);
       const float inv = two_to(-e);
-      uint32_t v = 0;
+      uint32_t neg[E / 2], pos[E / 2];
 #pragma unroll
-      for (int i = 0; i < E; ++i) v |= (static_cast<uint32_t>(whole(x[i] * inv)) & 0xffu) << (8 * i);
-      if constexpr (E == 4) reinterpret_cast<uint32_t *>(sm + M::oQ + r * D)[lane] = v;
-      else reinterpret_cast<uint16_t *>(sm + M::oQ + r * D)[lane] = static_cast<uint16_t>(v);
+      for (int i = 0; i < E; i += 2) {
+        const int v = whole(x[i] * inv), w = whole(x[i + 1] * inv);
+        neg[i / 2] = pack_f16x2(static_cast<float>(min(v, 0)), static_cast<float>(min(w, 0)));
+        pos[i / 2] = pack_f16x2(static_cast<float>(max(v, 0)), static_cast<float>(max(w, 0)));
+      }
+      // 128-byte rows of 64 elements, 16-byte pieces swizzled by the row; blocks of K RN rows apart
+      constexpr int LB = 64 / E;              // lanes per block
+      const int byte = (lane % LB) * E * 2;
+      unsigned char *dst = sm + (lane / LB) * RN * 128 + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+      if constexpr (E == 4) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(neg[0], neg[1]);
+        *reinterpret_cast<uint2 *>(dst + (KB / 2) * RN * 128) = make_uint2(pos[0], pos[1]);
+      } else {
+        *reinterpret_cast<uint32_t *>(dst) = neg[0];
+        *reinterpret_cast<uint32_t *>(dst + (KB / 2) * RN * 128) = pos[0];
+      }
       if (lane == 0) s_unit[r] = two_to(e);
     }
-    fetch(0);
-    store(0);
+    fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
-    // A: the rows' integers below zero against lo, those above against hi
-    uint32_t af[KS][4];
-    const int ra = rw * 16 + gq, rb = ra + 8;
-    const bool va = ra < rows, vb = rb < rows;
-    auto pair = [&](int r, bool ok, int d, bool pos) -> uint32_t {
-      if (!ok) return 0u;
-      const char2 c = *reinterpret_cast<const char2 *>(sm + M::oQ + r * D + d);
-      const int x = pos ? max(static_cast<int>(c.x), 0) : min(static_cast<int>(c.x), 0);
-      const int y = pos ? max(static_cast<int>(c.y), 0) : min(static_cast<int>(c.y), 0);
-      return pack_f16x2(static_cast<float>(x), static_cast<float>(y));
-    };
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < kManyEpi) {
+      // ---- epilogue: page (lane) x half of the columns
+      const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+      auto exp_of = [&](int tile) -> float {   // 2^e of this thread's page (0: no page)
+        const int i = tile * kTilePages + row;
+        if (i >= nl) return 0.f;
+        const int page = table[i];
+        DSA_CHECK(page >= 0 && page < a.n_pages);
+        return page >= 0 && page < a.n_pages ? two_to(a.exp[static_cast<size_t>(page) * a.H_kv + g]) : 0.f;
+      };
+      float e_next = exp_of(0);
+      for (int tile = 0; ok && tile < tiles; ++tile, buf.step()) {
+        const float e = e_next;
+        e_next = exp_of(tile + 1);
+        if (!(ok = warp_wait(&d_full[buf.slot], buf.phase, abort, a.wait_ns))) break;
+        tc_fence_after();
+        const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf.slot * (cols / 2) + half * (rn / 2);
+        const float4 *unit = reinterpret_cast<const float4 *>(s_unit + half * (rn / 2));
+        float b0 = -INFINITY, b1 = -INFINITY;
+        for (int c = 0; c < rn / 2; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(src + c, s);
+          tmem_wait_ld();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const bool pos = ks >= KS / 2;
-      const int d = (ks % (KS / 2)) * 16 + 2 * t;
-      af[ks][0] = pair(ra, va, d, pos);
-      af[ks][1] = pair(rb, vb, d, pos);
-      af[ks][2] = pair(ra, va, d + 8, pos);
-      af[ks][3] = pair(rb, vb, d + 8, pos);
-    }
-    const float ua = va ? s_unit[ra] : 0.f, ub = vb ? s_unit[rb] : 0.f;
-    const bool live = rw * 16 < rows;         // the warp has rows
-    for (int tile = 0; tile < tiles; ++tile) {
-      const int buf = tile & 1;
-      if (tile + 1 < tiles) fetch(tile + 1);
-      if (live) {
-        float acc[NT8][4];
-#pragma unroll
-        for (int c = 0; c < NT8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-        const unsigned char *base = sm + M::oTile + (buf * kTilePages + split * NT8 * 8 + (lane & 7)) * M::kPitch + (lane >> 3) * 16;
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += 2) {
-#pragma unroll
-          for (int c = 0; c < NT8; ++c) {
-            uint32_t bf[4];
-            ldsm_x4(bf, base + c * 8 * M::kPitch + ks * 32);
-            mma_16816_f16(acc[c], af[ks], bf[0], bf[1]);
-            mma_16816_f16(acc[c], af[ks + 1], bf[2], bf[3]);
+          for (int x = 0; x < 32; x += 4) {
+            const float4 u = unit[(c + x) / 4];
+            const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
+            const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
+            b0 = fmax3(b0, y.x, y.y);
+            b1 = fmax3(b1, z.x, z.y);
           }
         }
-#pragma unroll
-        for (int c = 0; c < NT8; ++c) {
-          float x = -INFINITY, y = -INFINITY;   // columns 2 t, 2 t + 1 over the warp's rows
-          if (va) {
-            x = acc[c][0] * ua;
-            y = acc[c][1] * ua;
-          }
-          if (vb) {
-            x = fmaxf(x, acc[c][2] * ub);
-            y = fmaxf(y, acc[c][3] * ub);
-          }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-            y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
-          }
-          if (gq == c) {
-            const int col = (split * NT8 + c) * 8 + 2 * t, i = tile * kTilePages + col;
-            const float ex = s_exp[buf * kTilePages + col], ey = s_exp[buf * kTilePages + col + 1];
-            if (i < nl && ex > 0.f) atomicMax(&s_key[i], ordered_key(x * ex));
-            if (i + 1 < nl && ey > 0.f) atomicMax(&s_key[i + 1], ordered_key(y * ey));
-          }
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[buf.slot]);
+        if (e > 0.f) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * e));
       }
-      if (tile + 1 < tiles) store(buf ^ 1);
-      __syncthreads();
+    } else if (warp == kManyEpi) {
+      // ---- MMA issuer
+      const uint32_t leader = lane == 0 ? 1u : 0u;
+      const uint32_t id = idesc_f16_f32(kTilePages, rn);
+      const uint64_t da = sdesc_sw128(smem_u32(sm + L.oSlots), 16, 1024), db = sdesc_sw128(smem_u32(sm), 16, 1024);
+      for (int tile = 0; ok && tile < tiles; ++tile, buf.step()) {
+        if (!(ok = warp_wait(&d_empty[buf.slot], buf.phase ^ 1u, abort, a.wait_ns))) break;
+        tc_fence_after();
+        for (int b = 0; b < KB; ++b, ring.step()) {
+          if (!(ok = warp_wait(&full[ring.slot], ring.phase, abort, a.wait_ns))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < 4; ++s)         // (descriptors count 16 bytes)
+            mma_ss(leader, tmem + buf.slot * (cols / 2), da + ring.slot * (kSlotBytes >> 4) + 2 * s,
+                   db + static_cast<uint64_t>(b * RN * 8 + 2 * s), id, b + s > 0);
+          commit_if(leader, &empty[ring.slot]);
+        }
+        if (ok) commit_if(leader, &d_full[buf.slot]);
+      }
+    } else {
+      // ---- converters: a thread brings alternate 16-byte pieces of one page's digest row
+      const int ct = tid - (kManyEpi + 1) * 32, row = ct >> 1, hf = ct & 1;
+      auto page_of = [&](int tile) -> int {
+        const int i = tile * kTilePages + row;
+        return i < nl ? table[i] : -1;
+      };
+      uint4 dig[KB][2];
+      auto fetch = [&](int b, int page) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          dig[b][v] = make_uint4(0, 0, 0, 0);
+          if (page >= 0 && page < a.n_pages)
+            dig[b][v] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + (static_cast<size_t>(page) * a.H_kv + g) * 2 * D +
+                                                              b * 64 + v * 32 + hf * 16));
+        }
+      };
+      const int page0 = page_of(0);
+      int page = page_of(1);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) fetch(b, page0);
+      for (int tile = 0; ok && tile < tiles; ++tile) {
+        const int page_next = page_of(tile + 2);
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          if (!ok || !(ok = warp_wait(&empty[ring.slot], ring.phase ^ 1u, abort, a.wait_ns))) break;
+          unsigned char *dst = sm + L.oSlots + ring.slot * kSlotBytes + row * 128;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint2 x = widen_s8(dig[b][v].x), y = widen_s8(dig[b][v].y), z = widen_s8(dig[b][v].z),
+                        w = widen_s8(dig[b][v].w);
+            const int c = v * 4 + hf * 2;
+            *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+            *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, w.x, w.y);
+          }
+          if (tile + 1 < tiles) fetch(b, page);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[ring.slot]);
+          ring.step();
+        }
+        page = page_next;
+      }
     }
+    ok = __syncthreads_and(ok);               // (also: every score of these rows is in)
+    if (!ok) break;
+  }
+  if (warp == kManyEpi) {
+    // the tensor core is idle before its memory goes, also where a wait ran out
+    commit_if(lane == 0, drained);
+    const uint64_t t0 = global_ns();
+    while (!__all_sync(kFull, mbar_try_wait(drained, 0)))
+      if (__any_sync(kFull, global_ns() - t0 > 200000000ull)) break;
+    tmem_dealloc(*tmem_slot, cols);
+    if (lane == 0 && !ok) atomicOr(&g_select_error, 1);
   }
   __syncthreads();
   pick<kManyThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
 }
+
+constexpr size_t kManyBytes = 227 * 1024;   // dynamic shared memory, at most
+static_assert(128 * 4 * 128 + kSlots * kSlotBytes + 128 * 4 + 256 + sizeof(SelectShared) + 16 + kSelectMaxPages / 16 * 4 <= kManyBytes, "widest table");
 
 template <typename Kern>
 cudaError_t launch_cluster(Kern kern, int items, int C, int threads, size_t smem, cudaStream_t s, const PageSelectArgs &a) {
@@ -744,8 +834,8 @@ template <int D>
 cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   const int items = a.n_blocks * a.H_kv, rows = a.cfg.q_block * (a.H_q / a.H_kv);
   const bool few = rows <= kFewRows;
-  // CTAs of an item: until the launch has two per SM, or a CTA a page per thread
-  const int least = few ? kFewThreads : 2 * kTilePages;
+  // CTAs of an item: until the launch has one per SM, or a CTA a page per thread (a tile)
+  const int least = few ? kFewThreads : kTilePages;
   int C = 1;
   while (C < 16 && items * C < 152 && a.max_pages > C * least) C *= 2;
   a.slice = (a.max_pages + C - 1) / C;
@@ -755,11 +845,11 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   }
   const size_t keys = static_cast<size_t>(a.slice) * 4;
   if (few) return launch_cluster(select_few_kernel<D>, items, C, kFewThreads, keys, s, a);
-  const size_t smem = Many<D>::oKey + keys;
-  if (rows <= 32) return launch_cluster(select_many_kernel<D, 2>, items, C, kManyThreads, smem, s, a);
-  if (rows <= 64) return launch_cluster(select_many_kernel<D, 4>, items, C, kManyThreads, smem, s, a);
-  if (rows <= 128) return launch_cluster(select_many_kernel<D, 8>, items, C, kManyThreads, smem, s, a);
-  return launch_cluster(select_many_kernel<D, 16>, items, C, kManyThreads, smem, s, a);
+  // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
+  a.rows = std::min((rows + 63) & ~63, 256);
+  if (many_layout(D, a.rows).oKey + keys > kManyBytes) a.rows = 128;
+  a.wait_ns = g_wait_limit_ns;
+  return launch_cluster(select_many_kernel<D>, items, C, kManyThreads, many_layout(D, a.rows).oKey + keys, s, a);
 }
 
 }  // namespace
@@ -785,5 +875,14 @@ cudaError_t launch_page_select(const PageSelectArgs &a0, cudaStream_t s) {
   while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
   return a.D == 128 ? launch_select_d<128>(a, s) : launch_select_d<64>(a, s);
 }
+
+int page_select_device_error() {
+  int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_select_error, sizeof(int)) != cudaSuccess) return -1;
+  if (cudaMemcpyToSymbol(g_select_error, &zero, sizeof(int)) != cudaSuccess) return -1;
+  return v;
+}
+
+void page_select_set_wait_limit(unsigned long long ns) { g_wait_limit_ns = std::min(ns, 1ull << 40); }
 
 }  // namespace dsa

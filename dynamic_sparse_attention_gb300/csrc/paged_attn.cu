@@ -432,18 +432,6 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
     if (global_ns() - t0 > limit_ns) return;
 }
 
-// The tensor-core instructions of the MMA warp, executed by the whole warp with the leader's
-// predicate inside: the warp stays converged, so descriptors and addresses live in uniform
-// registers.  (In a branch that only lane 0 takes, every operand is moved there first, about
-// 125 clocks an instruction against the 64 that the tensor core needs for it.)
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -452,28 +440,6 @@ __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
-// arrive on `bar` when every tensor-core instruction issued so far has completed
-__device__ __forceinline__ void commit_if(uint32_t pred, uint64_t *bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(pred)
-      : "memory");
-}
-
-// a ring position: slot and phase parity
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void step() {
-    if (++slot == N) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 // ------------------------------------------------------------------ FP8 -> bf16
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {

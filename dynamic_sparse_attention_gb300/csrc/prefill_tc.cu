@@ -908,6 +908,8 @@ extern "C" int dsa_device_error(int *code) {
   if (w < 0) return fail(DSA_ERR_CUDA, "reading the estimate's device error word");
   const int pg = paged_attn_device_error();   // the paged attention's word
   if (pg < 0) return fail(DSA_ERR_CUDA, "reading the paged attention's device error word");
+  const int sel = page_select_device_error();   // the page selection's word
+  if (sel < 0) return fail(DSA_ERR_CUDA, "reading the page selection's device error word");
   // checked builds: out-of-range device-side inputs met by the kernels
   int chk = 0;
   const int words[10] = {decode_check_word(),     decode_mma_check_word(), hip_select_check_word(),
@@ -918,7 +920,7 @@ extern "C" int dsa_device_error(int *code) {
     if (x < 0) return fail(DSA_ERR_CUDA, "reading a device check word");
     chk |= x;
   }
-  *code = v | (w << 1) | (chk ? 4 : 0) | (pg << 3);
+  *code = v | (w << 1) | (chk ? 4 : 0) | (pg << 3) | (sel << 4);
   if (chk)
     return fail(DSA_ERR_DEVICE_CHECK, "a kernel met a device-side input outside its range "
                                       "(length, count, selected position or list entry)");
@@ -935,6 +937,7 @@ extern "C" int dsa_set_wait_limit(unsigned long long ns) {
   using namespace dsa;
   clear_error();
   const unsigned long long v = ns ? ns : kWaitLimitNs;
+  page_select_set_wait_limit(v);
   if (prefill_tc_set_wait_limit(v) || vs_tc_set_wait_limit(v) || paged_attn_set_wait_limit(v))
     return fail(DSA_ERR_CUDA, "setting the wait limit of the tensor-core kernels");
   return DSA_OK;

@@ -582,7 +582,8 @@ int page_select_sizes(const dsa_paged_shape *shape, const dsa_page_select_cfg *c
  *   sel_index [n_blocks, H_kv, max_list]  the lists as places in the sequence's table (NULL to
  *          skip), -1 behind their end
  * A page outside [0, n_pages) scores lowest.  q_block in [1, 256], max_pages <= 262144, n_blocks <=
- * 4096, else UNSUPPORTED.  shape->dtype is not used but checked. */
+ * 4096, else UNSUPPORTED.  shape->dtype is not used but checked.  Where a CTA's bounded waits ran
+ * out, bit 4 of dsa_device_error is set and the lists are some pages of the sequences. */
 int page_select(const void *q, long long q_stride, const int8_t *bounds, const int8_t *exp,
                 const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
                 const dsa_paged_shape *shape, const dsa_page_select_cfg *cfg, int32_t *sel_q_start,
@@ -628,20 +629,21 @@ int dsa_profile_collect(dsa_kernel_stat *out, int max_out, int *n_out);
 
 /* ------------------------------------------------------------------ diagnostics */
 
-/* Every wait inside the tensor-core kernels (the prefill attention, the paged attention and
- * the two passes of the vertical-slash estimate) is bounded; a CTA that gives up stops issuing work,
+/* Every wait inside the tensor-core kernels (the prefill attention, the paged attention, the page
+ * selection and the two passes of the vertical-slash estimate) is bounded; a CTA that gives up stops issuing work,
  * frees its resources and sets a device error word (the prefill CTA also writes zero
  * output).  dsa_device_error copies the words to *code (0 = none; bit 0: the prefill
  * attention, bit 1: the estimate; bit 2: in a checked build, a kernel met a kv_len,
  * count, selected position or list entry outside its documented range -- the call then
- * returns DSA_ERR_DEVICE_CHECK; bit 3: the paged attention) and clears them.  It synchronises with the device
+ * returns DSA_ERR_DEVICE_CHECK; bit 3: the paged attention; bit 4: the page selection) and clears
+ * them.  It synchronises with the device
  * (cudaMemcpyFromSymbol); call it between steps, not on a hot path.  Not a
  * source-page operation. */
 int dsa_device_error(int *code);
 
 /* Sets the limit of those bounded waits to `ns` nanoseconds (0: back to the default of
- * half a second) for every later launch (captured launches of the paged attention keep the
- * one they were captured with); it synchronises (cudaMemcpyToSymbol).  A test
+ * half a second) for every later launch (captured launches of the paged attention and the page
+ * selection keep the one they were captured with); it synchronises (cudaMemcpyToSymbol).  A test
  * aid: a limit of a few nanoseconds makes the waits run out, so that the give-up path
  * (stop, drain, free, error word) can be exercised without any fault.  Not a
  * source-page operation. */
