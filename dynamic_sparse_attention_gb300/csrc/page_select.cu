@@ -225,15 +225,19 @@ __device__ __forceinline__ int clamp_row(const PageSelectArgs &a, int x) { retur
 
 // Block j: a scan over the sequences' counts of blocks, a run of them per thread.
 template <int NT>
-__device__ Block find_block(const PageSelectArgs &a, int j, int *s_scan /* [NT / 32 + 1] */, int *s_found /* [2] */) {
+__device__ Block find_block(const PageSelectArgs &a, int j, int *s_scan /* [NT / 32 + 1] */, int *s_found /* [5] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qb = a.cfg.q_block;
   const int per = (a.B + NT - 1) / NT, b0 = tid * per, b1 = min(a.B, b0 + per);
-  auto blocks = [&](int b) -> int {
-    return (max(clamp_row(a, a.q_start[b + 1]) - clamp_row(a, a.q_start[b]), 0) + qb - 1) / qb;
-  };
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += blocks(b);
+  int sum = 0, qs = 0, qe = 0, kv = 0;        // of the run's first sequence, asked for with the rest
+  if (b0 < b1) {
+    kv = a.kv_len[b0];
+    qs = clamp_row(a, a.q_start[b0]);
+    qe = clamp_row(a, a.q_start[b0 + 1]);
+    sum = (max(qe - qs, 0) + qb - 1) / qb;
+    for (int b = b0 + 1; b < b1; ++b)
+      sum += (max(clamp_row(a, a.q_start[b + 1]) - clamp_row(a, a.q_start[b]), 0) + qb - 1) / qb;
+  }
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -247,10 +251,18 @@ __device__ Block find_block(const PageSelectArgs &a, int j, int *s_scan /* [NT /
   for (int w = 0; w < warp; ++w) at += s_scan[w];
   if (j >= at && j < at + sum) {
     for (int b = b0; b < b1; ++b) {
-      const int x = blocks(b);
+      if (b > b0) {
+        qs = clamp_row(a, a.q_start[b]);
+        qe = clamp_row(a, a.q_start[b + 1]);
+        kv = a.kv_len[b];
+      }
+      const int x = (max(qe - qs, 0) + qb - 1) / qb;
       if (j < at + x) {
         s_found[0] = b;
         s_found[1] = j - at;
+        s_found[2] = qs;
+        s_found[3] = qe;
+        s_found[4] = kv;
         break;
       }
       at += x;
@@ -267,11 +279,13 @@ __device__ Block find_block(const PageSelectArgs &a, int j, int *s_scan /* [NT /
     k.n = 0;
     return k;
   }
-  const int qs = clamp_row(a, a.q_start[k.b]), qe = clamp_row(a, a.q_start[k.b + 1]);
+  qs = s_found[2];
+  qe = s_found[3];
   k.lo = qs + s_found[1] * qb;
   k.n = min(qb, qe - k.lo);
-  const int cap = a.max_pages << a.lg_page, kv = min(max(a.kv_len[k.b], 0), cap);
-  DSA_CHECK(kv == a.kv_len[k.b] && kv >= qe - qs);
+  const int cap = a.max_pages << a.lg_page;
+  DSA_CHECK(s_found[4] >= qe - qs && s_found[4] <= cap);
+  kv = min(max(s_found[4], 0), cap);
   const int p0 = kv - (qe - k.lo), p1 = p0 + k.n - 1, pc = max(p0, 0);
   if (p1 < 0) return k;
   const int own0 = pc >> a.lg_page;
@@ -290,40 +304,42 @@ __device__ __forceinline__ void put(const PageSelectArgs &a, int j, int g, int i
   if (a.sel_index) a.sel_index[at] = index;
 }
 
-// What a list holds beside its picks, by one CTA.
-template <int NT>
+// What a list holds beside its picks, by one warp.
 __device__ void put_fixed(const PageSelectArgs &a, int j, int g, const Block &k) {
+  const int lane = threadIdx.x & 31;
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages;
   const int count = k.own1 < 0 ? 0 : k.s0 + k.picked + k.own1 + 1 - k.first;
-  for (int i = threadIdx.x; i < a.max_list; i += NT) {
+  for (int i = lane; i < a.max_list; i += 32) {
     if (i >= k.s0 && i < k.s0 + k.picked) continue;
     const int index = i >= count ? -1 : i < k.s0 ? i : k.first + i - k.s0 - k.picked;
     put(a, j, g, i, index < 0 ? -1 : table[index], index);
   }
-  if (g == 0 && threadIdx.x == 0) {
+  if (g == 0 && lane == 0) {
     a.sel_q_start[j] = k.lo;
     a.sel_kv_len[j] = k.keys;
     if (j == a.n_blocks - 1) a.sel_q_start[j + 1] = k.lo + k.n;
   }
 }
 
-// bf16 query elements of a lane -> fp32, the row's exponent
+// A lane's D / 32 elements of row r of a block (bf16 words), and what they are in fp32 with the row's
+// exponent.
 template <int D>
-__device__ __forceinline__ int row_of(const PageSelectArgs &a, const Block &k, int g, int r, float *x) {
-  constexpr int E = D / 32;                   // elements per lane
+__device__ __forceinline__ void load_row(const PageSelectArgs &a, const Block &k, int g, int r, uint32_t *w) {
   const int lane = threadIdx.x & 31, G = a.H_q / a.H_kv;
   const uint16_t *src = a.q + static_cast<size_t>(k.lo + r / G) * a.q_stride + static_cast<size_t>(g * G + r % G) * D;
-  uint32_t w[E / 2];
-  if constexpr (E == 4) {
+  if constexpr (D == 128) {
     const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
     w[0] = u.x;
     w[1] = u.y;
   } else {
     w[0] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
   }
+}
+template <int D>
+__device__ __forceinline__ int row_of(const uint32_t *w, float *x) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
+  for (int i = 0; i < D / 32; ++i) {
     x[i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
     const uint32_t v = __float_as_uint(x[i]) & 0x7fffffffu;
     m = max(m, v < 0x7f800000u ? v : 0u);
@@ -336,72 +352,107 @@ __device__ __forceinline__ int row_of(const PageSelectArgs &a, const Block &k, i
 __device__ __forceinline__ int whole(float x) { return min(max(__float2int_rn(x), -127), 127); }
 
 struct SelectShared {
-  uint32_t hist[4][256];   // of each digit, read by the whole cluster
-  uint32_t tot[256];
-  int scan[17], found[2];
-  uint32_t res[2];
-  int kept[2];             // keys above the threshold, equal to it
+  uint32_t hist[4][256];   // of each pass, read by the whole cluster
+  uint32_t tot[2][256];
+  uint32_t low, high;      // of the CTA's keys
+  int kept[2];             // keys above the threshold, within it
+  int scan[17], found[5];
   int scan2[2][17];
 };
 
+template <int NT>
+__device__ __forceinline__ void clear_shared(SelectShared &sh) {
+  for (int i = threadIdx.x; i < 4 * 256; i += NT) (&sh.hist[0][0])[i] = 0;
+  if (threadIdx.x == 0) {
+    sh.low = 0xffffffffu;
+    sh.high = 0;
+  }
+}
+
 // The `k.picked` best of the cluster's keys (each CTA holds nl of them, of pages p_first ..) into the
-// list: an 8-bit radix select whose histograms the CTAs read from each other, then every CTA writes
-// its own picks behind those of the lower ranks.
+// list.  The interval of keys that holds the last pick is narrowed 256 times at a time, from the least
+// and largest key on, by histograms that the CTAs read from each other, until all of its keys are
+// picks or all are equal; then every CTA writes its own picks behind those of the lower ranks.
+// (Digits of the whole 32 bits, four passes whose first two put nearly all keys into a bin or two:
+// 1.2 us a pass.)
 template <int NT>
 __device__ void pick(const PageSelectArgs &a, cg::cluster_group &cluster, SelectShared &sh, const uint32_t *key, int nl,
                      int p_first, int j, int g, const Block &k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  uint32_t prefix = 0, mask = 0, left = static_cast<uint32_t>(k.picked);
+  {
+    uint32_t low = 0xffffffffu, high = 0;
+    for (int i = tid; i < nl; i += NT) {
+      low = min(low, key[i]);
+      high = max(high, key[i]);
+    }
+    low = __reduce_min_sync(kFull, low);
+    high = __reduce_max_sync(kFull, high);
+    if (lane == 0) {
+      atomicMin(&sh.low, low);
+      atomicMax(&sh.high, high);
+    }
+  }
+  cluster.sync();
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for (int c = 0; c < C; ++c) {
+    lo = min(lo, *cluster.map_shared_rank(&sh.low, c));
+    hi = max(hi, *cluster.map_shared_rank(&sh.high, c));
+  }
+  uint32_t left = static_cast<uint32_t>(k.picked);   // picks in [lo, hi]; every key above is one
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
+    const int shift = max(0, 24 - __clz(hi - lo | 1u));
     for (int i = tid; i < nl; i += NT) {
-      const uint32_t x = key[i];
-      if ((x & mask) == prefix) atomicAdd(&sh.hist[pass][(x >> shift) & 255u], 1u);
+      const uint32_t x = key[i] - lo;
+      if (x <= hi - lo) atomicAdd(&sh.hist[pass][x >> shift], 1u);
     }
     cluster.sync();
     if (tid < 256) {
       uint32_t t = 0;
       for (int c = 0; c < C; ++c) t += *cluster.map_shared_rank(&sh.hist[pass][tid], c);
-      sh.tot[tid] = t;
+      sh.tot[pass & 1][tid] = t;
     }
     __syncthreads();
-    if (warp == 0) {
-      const int top = 255 - lane * 8;         // lane's bins, from the top down
-      uint32_t c[8], sum = 0;
+    // every warp finds the bin that holds the last pick: lane's bins from the top down
+    const int top = 255 - lane * 8;
+    uint32_t c[8], sum = 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) sum += c[t] = sh.tot[top - t];
-      uint32_t incl = sum;
+    for (int t = 0; t < 8; ++t) sum += c[t] = sh.tot[pass & 1][top - t];
+    uint32_t incl = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      uint32_t run = incl - sum;
-      if (run < left && left <= incl) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    uint32_t run = incl - sum, bin = 0, in = 0;
+    const bool mine = run < left && left <= incl;
+    if (mine) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < 8; ++t) {
+        if (in == 0) {
           if (run + c[t] >= left) {
-            sh.res[0] = static_cast<uint32_t>(top - t);
-            sh.res[1] = run;
-            break;
+            bin = static_cast<uint32_t>(top - t);
+            in = c[t];
+          } else {
+            run += c[t];
           }
-          run += c[t];
         }
       }
     }
-    __syncthreads();
-    prefix |= sh.res[0] << shift;
-    mask |= 255u << shift;
-    left -= sh.res[1];
+    const int who = __ffs(__ballot_sync(kFull, mine)) - 1;   // (the histograms hold `left` keys at least)
+    left -= __shfl_sync(kFull, run, who);
+    lo += __shfl_sync(kFull, bin, who) << shift;
+    in = __shfl_sync(kFull, in, who);
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    if (shift == 0 || in == left) break;      // (the same for every warp of the cluster)
   }
-  // keys above `prefix` are in, and the first `left` of those equal to it
+  // keys above `hi` are in, and the first `left` of those from `lo` on
   const int per = (nl + NT - 1) / NT, i0 = min(nl, tid * per), i1 = min(nl, i0 + per);
   int gt = 0, eq = 0;
   for (int i = i0; i < i1; ++i) {
-    gt += key[i] > prefix;
-    eq += key[i] == prefix;
+    gt += key[i] > hi;
+    eq += key[i] >= lo && key[i] <= hi;
   }
   int ig = gt, ie = eq;
 #pragma unroll
@@ -419,6 +470,7 @@ __device__ void pick(const PageSelectArgs &a, cg::cluster_group &cluster, Select
   __syncthreads();
   int og = ig - gt, oe = ie - eq;             // before this thread's
   int tg = 0, te = 0;
+#pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w == warp) {
       og += tg;
@@ -427,27 +479,29 @@ __device__ void pick(const PageSelectArgs &a, cg::cluster_group &cluster, Select
     tg += sh.scan2[0][w];
     te += sh.scan2[1][w];
   }
-  if (tid == 0) {
-    sh.kept[0] = tg;
-    sh.kept[1] = te;
-  }
-  cluster.sync();
-  for (int c = 0; c < rank; ++c) {
-    const int *o = cluster.map_shared_rank(sh.kept, c);
-    og += o[0];
-    oe += o[1];
+  if (C > 1) {
+    if (tid == 0) {
+      sh.kept[0] = tg;
+      sh.kept[1] = te;
+    }
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const int *o = cluster.map_shared_rank(sh.kept, c);
+      og += o[0];
+      oe += o[1];
+    }
   }
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages;
   for (int i = i0; i < i1; ++i) {
-    const bool is_eq = key[i] == prefix;
-    if (key[i] > prefix || (is_eq && oe < static_cast<int>(left))) {
+    const bool is_eq = key[i] >= lo && key[i] <= hi;
+    if (key[i] > hi || (is_eq && oe < static_cast<int>(left))) {
       const int at = og + min(oe, static_cast<int>(left));
       put(a, j, g, k.s0 + at, table[p_first + i], p_first + i);
     }
-    og += key[i] > prefix;
+    og += key[i] > hi;
     oe += is_eq;
   }
-  cluster.sync();                             // shared memory stays until every reader is done
+  if (C > 1) cluster.sync();                  // shared memory stays until every reader is done
 }
 
 // Every candidate is listed.
@@ -457,109 +511,6 @@ __device__ void pick_all(const PageSelectArgs &a, int rank, int C, int j, int g,
   for (int i = rank * NT + threadIdx.x; i < k.picked; i += C * NT)
     put(a, j, g, k.s0 + i, table[k.s0 + i], k.s0 + i);
 }
-
-// Few rows (a decode step's): a thread takes a page, its digest in registers, and the rows'
-// integers come from shared memory, the same word for the whole warp.
-constexpr int kFewThreads = 256, kFewRows = 16;
-
-template <int D>
-__global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSelectArgs a) {
-  constexpr int W = D / 4;                    // words of a row's integers
-  extern __shared__ uint32_t s_key[];         // [a.slice]
-  __shared__ __align__(16) int s_neg[kFewRows][W], s_pos[kFewRows][W];
-  __shared__ float s_unit[kFewRows];
-  __shared__ SelectShared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int item = blockIdx.x / C, j = item / a.H_kv, g = item % a.H_kv;
-  grid_dep_wait();
-  const Block k = find_block<kFewThreads>(a, j, sh.scan, sh.found);
-  if (rank == 0) put_fixed<kFewThreads>(a, j, g, k);
-  const int n = k.first - k.s0;               // candidates
-  if (k.picked == n || k.picked == 0) {       // (the same for the whole cluster)
-    pick_all<kFewThreads>(a, rank, C, j, g, k);
-    return;
-  }
-  for (int i = tid; i < 4 * 256; i += kFewThreads) sh.hist[0][i] = 0;
-  const int R = k.n * (a.H_q / a.H_kv);
-  for (int r = warp; r < (R + 3) / 4 * 4; r += kFewThreads / 32) {   // to a multiple of 4, with copies of row 0
-    constexpr int E = D / 32;
-    float x[E];
-    const int e = row_of<D>(a, k, g, r < R ? r : 0, x);
-    const float inv = two_to(-e);
-    uint32_t pos = 0, neg = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int v = whole(x[i] * inv);
-      pos |= (static_cast<uint32_t>(max(v, 0)) & 0xffu) << (8 * i);
-      neg |= (static_cast<uint32_t>(min(v, 0)) & 0xffu) << (8 * i);
-    }
-    if constexpr (E == 4) {
-      s_pos[r][lane] = static_cast<int>(pos);
-      s_neg[r][lane] = static_cast<int>(neg);
-    } else {
-      reinterpret_cast<uint16_t *>(s_pos[r])[lane] = static_cast<uint16_t>(pos);
-      reinterpret_cast<uint16_t *>(s_neg[r])[lane] = static_cast<uint16_t>(neg);
-    }
-    if (lane == 0) s_unit[r] = two_to(e);
-  }
-  __syncthreads();
-  const int per = (n + C - 1) / C;
-  const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
-  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
-  for (int i = tid; i < nl; i += kFewThreads) {
-    const int page = table[i];
-    DSA_CHECK(page >= 0 && page < a.n_pages);
-    uint32_t key = 0;                         // no page: below every score
-    if (page >= 0 && page < a.n_pages) {
-      const size_t row = static_cast<size_t>(page) * a.H_kv + g;
-      const int4 *src = reinterpret_cast<const int4 *>(a.bounds + row * 2 * D);
-      int4 lo[W / 4], hi[W / 4];
-#pragma unroll
-      for (int w = 0; w < W / 4; ++w) lo[w] = __ldg(src + w);
-#pragma unroll
-      for (int w = 0; w < W / 4; ++w) hi[w] = __ldg(src + W / 4 + w);
-      const int e = a.exp[row];
-      float best = -INFINITY;
-      for (int r = 0; r < R; r += 4) {
-        int acc[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < W / 4; ++w) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int4 u = *reinterpret_cast<const int4 *>(&s_neg[r + x][4 * w]);
-            const int4 v = *reinterpret_cast<const int4 *>(&s_pos[r + x][4 * w]);
-            acc[x] = __dp4a(u.x, lo[w].x, acc[x]);
-            acc[x] = __dp4a(u.y, lo[w].y, acc[x]);
-            acc[x] = __dp4a(u.z, lo[w].z, acc[x]);
-            acc[x] = __dp4a(u.w, lo[w].w, acc[x]);
-            acc[x] = __dp4a(v.x, hi[w].x, acc[x]);
-            acc[x] = __dp4a(v.y, hi[w].y, acc[x]);
-            acc[x] = __dp4a(v.z, hi[w].z, acc[x]);
-            acc[x] = __dp4a(v.w, hi[w].w, acc[x]);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) best = fmaxf(best, static_cast<float>(acc[x]) * s_unit[r + x]);
-      }
-      key = ordered_key(best * two_to(e));
-    }
-    s_key[i] = key;
-  }
-  __syncthreads();
-  pick<kFewThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
-}
-
-// Many rows (a chunk's blocks): the products on tcgen05, the integers as fp16.  Pages lie on the
-// TMEM lanes (M = 128) and the block's rows on its columns (N = up to 256), so a thread owns a page
-// and takes the largest score of its row of columns without talking to another.  The rows' integers
-// stay in shared memory, those below zero against lo and those above against hi (K = 2 D); digests
-// come in tiles of 128 pages, widened to fp16 on their way into a ring of 64-element steps of K.
-constexpr int kManyConv = 8, kManyEpi = 8;                       // warps: epilogue, MMA issuer, converters
-constexpr int kManyThreads = (kManyEpi + 1 + kManyConv) * 32;
-constexpr int kTilePages = 128, kSlots = 4;
-constexpr uint32_t kSlotBytes = kTilePages * 128;
 
 // four signed bytes -> fp16 pairs (exact): 1024 + (x + 128) has x + 128 in its low mantissa bits
 __device__ __forceinline__ uint2 widen_s8(uint32_t w) {
@@ -571,6 +522,158 @@ __device__ __forceinline__ uint2 widen_s8(uint32_t w) {
   asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(hi) : "r"(0x64806480u));
   return make_uint2(lo, hi);
 }
+
+// Few rows (a decode step's): a launch is bound by gathering the digests, 256 bytes a page and head.
+// A warp takes 16 pages at a time, the lanes' 16-byte pieces covering whole sectors of their rows,
+// and multiplies them from registers: the 4 bytes of a lane's word are its elements of one
+// 16-element step of mma.sync, in the same order on both sides, so nothing is moved between lanes.
+// (A page per thread with dp4a: 32 rows a load, each a line of its own: 38 us for a token over 1M
+// keys.)
+constexpr int kFewThreads = 256, kFewRows = 16;
+
+template <int D, int NT8>                     // NT8: 8-row columns of queries
+__global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSelectArgs a) {
+  constexpr int P = D / 32;                   // 16-byte pieces of a row per lane (4 lanes a row)
+  extern __shared__ uint32_t s_key[];         // [a.slice]
+  __shared__ __align__(16) unsigned char s_q[8 * NT8][2 * D];   // whole numbers below zero, above zero
+  __shared__ float s_unit[8 * NT8];
+  __shared__ SelectShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
+  const int item = blockIdx.x / C, j = item / a.H_kv, g = item % a.H_kv;
+  clear_shared<kFewThreads>(sh);
+  grid_dep_wait();
+  const Block k = find_block<kFewThreads>(a, j, sh.scan, sh.found);
+  const int n = k.first - k.s0;               // candidates
+  if (k.picked == n || k.picked == 0) {       // (the same for the whole cluster)
+    if (rank == 0 && warp == 0) put_fixed(a, j, g, k);
+    pick_all<kFewThreads>(a, rank, C, j, g, k);
+    return;
+  }
+  const int per = (n + C - 1) / C;
+  const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
+  const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
+  const int tasks = (nl + 15) / 16;
+  // digests (and 2^e of the page that the lane writes the key of) of a task, requested ahead
+  auto ids_of = [&](int task) -> int {
+    const int i = task * 16 + (lane & 15);
+    return i < nl ? table[i] : -1;
+  };
+  uint4 ra[P], rb[P];
+  float e_next = 0.f;
+  auto fetch = [&](int ids) {
+    const int pa = __shfl_sync(kFull, ids, gr), pb = __shfl_sync(kFull, ids, gr + 8);
+    const bool oka = pa >= 0 && pa < a.n_pages, okb = pb >= 0 && pb < a.n_pages;
+    const size_t rowa = static_cast<size_t>(pa) * a.H_kv + g, rowb = static_cast<size_t>(pb) * a.H_kv + g;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      ra[i] = oka ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + rowa * 2 * D) + i * 4 + t) : make_uint4(0, 0, 0, 0);
+      rb[i] = okb ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + rowb * 2 * D) + i * 4 + t) : make_uint4(0, 0, 0, 0);
+    }
+    e_next = 0.f;
+    if (t < 2 && (t ? okb : oka)) e_next = two_to(a.exp[t ? rowb : rowa]);
+  };
+  const int ids0 = ids_of(warp);
+  int ids = ids_of(warp + kFewThreads / 32);
+  const int R = k.n * (a.H_q / a.H_kv);
+  for (int r = warp; r < 8 * NT8; r += kFewThreads / 32) {   // (rows behind the last repeat the first)
+    constexpr int E = D / 32;
+    uint32_t w[E / 2];
+    float x[E];
+    load_row<D>(a, k, g, r < R ? r : 0, w);
+    if (r == warp) fetch(ids0);               // behind the row's own load
+    const int e = row_of<D>(w, x);
+    const float inv = two_to(-e);
+    uint32_t pos = 0, neg = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int v = whole(x[i] * inv);
+      pos |= (static_cast<uint32_t>(max(v, 0)) & 0xffu) << (8 * i);
+      neg |= (static_cast<uint32_t>(min(v, 0)) & 0xffu) << (8 * i);
+    }
+    if constexpr (E == 4) {
+      reinterpret_cast<uint32_t *>(s_q[r])[lane] = neg;
+      reinterpret_cast<uint32_t *>(s_q[r] + D)[lane] = pos;
+    } else {
+      reinterpret_cast<uint16_t *>(s_q[r])[lane] = static_cast<uint16_t>(neg);
+      reinterpret_cast<uint16_t *>(s_q[r] + D)[lane] = static_cast<uint16_t>(pos);
+    }
+    if (lane == 0) s_unit[r] = two_to(e);
+  }
+  __syncthreads();
+  uint32_t bq[NT8][P][8];                     // the queries' fragments: row gr of a column, the lane's bytes
+  float u0[NT8], u1[NT8];
+#pragma unroll
+  for (int c = 0; c < NT8; ++c) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(s_q[8 * c + gr] + (i * 4 + t) * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint2 h = widen_s8(w[x]);
+        bq[c][i][2 * x] = h.x;
+        bq[c][i][2 * x + 1] = h.y;
+      }
+    }
+    u0[c] = s_unit[8 * c + 2 * t];
+    u1[c] = s_unit[8 * c + 2 * t + 1];
+  }
+  for (int task = warp; task < tasks; task += kFewThreads / 32) {
+    float acc[NT8][2][4];
+#pragma unroll
+    for (int c = 0; c < NT8; ++c)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[c][x >> 2][x & 3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint32_t wa[4] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w}, wb[4] = {rb[i].x, rb[i].y, rb[i].z, rb[i].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint2 va = widen_s8(wa[x]), vb = widen_s8(wb[x]);
+        const uint32_t af[4] = {va.x, vb.x, va.y, vb.y};
+#pragma unroll
+        for (int c = 0; c < NT8; ++c) mma_16816_f16(acc[c][x & 1], af, bq[c][i][2 * x], bq[c][i][2 * x + 1]);
+      }
+    }
+    const float e = e_next;
+    const int next = ids;
+    ids = ids_of(task + 2 * (kFewThreads / 32));
+    fetch(next);                              // (all -1 behind the last task: nothing is read)
+    float sa = -INFINITY, sb = -INFINITY;     // pages gr and gr + 8 over the lane's rows
+#pragma unroll
+    for (int c = 0; c < NT8; ++c) {
+      float s[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] = acc[c][0][x] + acc[c][1][x];   // (whole numbers: exact)
+      sa = fmaxf(sa, fmaxf(s[0] * u0[c], s[1] * u1[c]));
+      sb = fmaxf(sb, fmaxf(s[2] * u0[c], s[3] * u1[c]));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      sa = fmaxf(sa, __shfl_xor_sync(kFull, sa, o));
+      sb = fmaxf(sb, __shfl_xor_sync(kFull, sb, o));
+    }
+    const int i = task * 16 + gr + 8 * t;
+    if (t < 2 && i < nl) s_key[i] = e > 0.f ? ordered_key((t ? sb : sa) * e) : 0u;   // no page: below every score
+  }
+  if (rank == 0 && warp == kFewThreads / 32 - 1) put_fixed(a, j, g, k);
+  __syncthreads();
+  pick<kFewThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
+}
+
+// Many rows (a chunk's blocks): the products on tcgen05, the integers as fp16.  Pages lie on the
+// TMEM lanes (M = 128) and the block's rows on its columns (N = up to 256, in two halves), so a thread
+// owns a page and takes the largest score of its row of columns without talking to another.  The
+// rows' integers stay in shared memory, those below zero against lo and those above against hi (K =
+// 2 D).  Digests come in tiles of 128 pages by cp.async and go, widened to fp16, to TMEM as the A
+// operand: with A in shared memory as well, reading both and writing A took its whole bandwidth (96 + 32
+// of 128 bytes a clock; a tile 4,000 clocks where the products need 2,048).  While one half's scores
+// are read, the other half is computed.
+constexpr int kManyEpi = 8, kManyConv = 8;                       // warps: epilogue, converters, MMA issuer
+constexpr int kManyThreads = (kManyEpi + kManyConv + 1) * 32;
+constexpr int kTilePages = 128;
 
 // The whole warp waits, at most `limit` ns; the outcome is warp-uniform.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit) {
@@ -587,27 +690,34 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 
 // Shared memory of a launch whose CTAs hold `rows` rows (a multiple of 64, at most 256) at a time.
 struct ManyLayout {
-  uint32_t oSlots, oUnit, oBar, oShared, oKey;
+  uint32_t oRaw, oUnit, oBar, oShared, oKey;
 };
-__host__ __device__ inline ManyLayout many_layout(int D, int rows) {
-  ManyLayout m;
-  m.oSlots = static_cast<uint32_t>(rows) * 4 * D;               // rows of 2 D fp16, in blocks of 64
-  m.oUnit = m.oSlots + kSlots * kSlotBytes;
+__host__ __device__ constexpr ManyLayout many_layout(int D, int rows) {
+  ManyLayout m{};
+  m.oRaw = static_cast<uint32_t>(rows) * 4 * D;                 // rows of 2 D fp16, in blocks of 64
+  m.oUnit = m.oRaw + 2 * kTilePages * 2 * D;                    // two tiles of digests
   m.oBar = m.oUnit + rows * 4;
-  m.oShared = m.oBar + 256;
+  m.oShared = m.oBar + 128;
   m.oKey = m.oShared + (sizeof(SelectShared) + 15) / 16 * 16;
   return m;
 }
 
+// 16 bytes to shared memory, zeros where there is nothing to read
+__device__ __forceinline__ void cp_async_16_or_0(void *dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 16 : 0));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const PageSelectArgs a) {
-  constexpr int KB = 2 * D / 64;              // 64-element steps of K
+  constexpr int KB = 2 * D / 64;              // 64-element blocks of K
+  constexpr int A = D;                        // TMEM columns of a tile's digests (2 D fp16)
+  constexpr int PP = 2 * D / 16;              // 16-byte pieces of a digest row
   extern __shared__ __align__(1024) unsigned char sm[];
   const int RN = a.rows;                      // rows held at a time
   const ManyLayout L = many_layout(D, RN);
   SelectShared &sh = *reinterpret_cast<SelectShared *>(sm + L.oShared);
   float *s_unit = reinterpret_cast<float *>(sm + L.oUnit);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L.oBar), *empty = full + kSlots, *d_full = empty + kSlots,
+  uint64_t *a_full = reinterpret_cast<uint64_t *>(sm + L.oBar), *a_empty = a_full + 2, *d_full = a_empty + 2,
            *d_empty = d_full + 2, *drained = d_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -616,28 +726,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = blockIdx.x / C, j = item / a.H_kv, g = item % a.H_kv;
+  clear_shared<kManyThreads>(sh);
   grid_dep_wait();
   const Block k = find_block<kManyThreads>(a, j, sh.scan, sh.found);
-  if (rank == 0) put_fixed<kManyThreads>(a, j, g, k);
   const int n = k.first - k.s0;
   if (k.picked == n || k.picked == 0) {
+    if (rank == 0 && warp == 0) put_fixed(a, j, g, k);
     pick_all<kManyThreads>(a, rank, C, j, g, k);
     return;
   }
-  for (int i = tid; i < 4 * 256; i += kManyThreads) sh.hist[0][i] = 0;
   const int per = (n + C - 1) / C;
   const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
   for (int i = tid; i < nl; i += kManyThreads) s_key[i] = 0;
   const int R = k.n * (a.H_q / a.H_kv);
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
   const int tiles = (nl + kTilePages - 1) / kTilePages;
-  const uint32_t cols = RN <= 64 ? 128u : RN <= 128 ? 256u : 512u;   // TMEM: two buffers
+  const uint32_t cols = RN + 2 * A <= 256 ? 256u : 512u;          // TMEM: scores of RN rows, two tiles
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], kManyConv);
-      mbar_init(&empty[s], 1);
-    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&a_full[s], kManyConv);
+      mbar_init(&a_empty[s], 1);
       mbar_init(&d_full[s], 1);
       mbar_init(&d_empty[s], kManyEpi);
     }
@@ -645,53 +753,64 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == kManyEpi) {
+  if (warp == kManyEpi + kManyConv) {
     tmem_alloc(tmem_slot, cols);
     tmem_relinquish();
   }
   // what a role carries over from one set of rows to the next
-  Ring<kSlots> ring;
-  Ring<2> buf;
+  Ring<2> buf;                                // the digests' buffer
+  uint32_t d_phase = 0;
   bool ok = true;
 
   for (int r0 = 0; r0 < R; r0 += RN) {
     __syncthreads();                          // the rows before are read (and the barriers are there)
     const int rows = min(RN, R - r0);
     const int rn = (rows + 63) & ~63;         // columns in use; those behind the last row repeat it
-    for (int r = warp; r < rn; r += kManyThreads / 32) {
+    constexpr int U = 8, W = kManyThreads / 32;   // rows a warp asks for at once
+    for (int r1 = warp; r1 < rn; r1 += U * W) {
       constexpr int E = D / 32;
-      float x[E];
-      const int e = row_of<D>(a, k, g, r0 + min(r, rows - 1), x);
-      const float inv = two_to(-e);
-      uint32_t neg[E / 2], pos[E / 2];
+      uint32_t w[U][E / 2];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const int v = whole(x[i] * inv), w = whole(x[i + 1] * inv);
-        neg[i / 2] = pack_f16x2(static_cast<float>(min(v, 0)), static_cast<float>(min(w, 0)));
-        pos[i / 2] = pack_f16x2(static_cast<float>(max(v, 0)), static_cast<float>(max(w, 0)));
+      for (int u = 0; u < U; ++u)
+        if (r1 + u * W < rn) load_row<D>(a, k, g, r0 + min(r1 + u * W, rows - 1), w[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r1 + u * W;
+        if (r >= rn) break;
+        float x[E];
+        const int e = row_of<D>(w[u], x);
+        const float inv = two_to(-e);
+        uint32_t neg[E / 2], pos[E / 2];
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const int v = whole(x[i] * inv), y = whole(x[i + 1] * inv);
+          neg[i / 2] = pack_f16x2(static_cast<float>(min(v, 0)), static_cast<float>(min(y, 0)));
+          pos[i / 2] = pack_f16x2(static_cast<float>(max(v, 0)), static_cast<float>(max(y, 0)));
+        }
+        // 128-byte rows of 64 elements, 16-byte pieces swizzled by the row; blocks of K RN rows apart
+        constexpr int LB = 64 / E;            // lanes per block
+        const int byte = (lane % LB) * E * 2;
+        unsigned char *dst = sm + (lane / LB) * RN * 128 + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+        if constexpr (E == 4) {
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(neg[0], neg[1]);
+          *reinterpret_cast<uint2 *>(dst + (KB / 2) * RN * 128) = make_uint2(pos[0], pos[1]);
+        } else {
+          *reinterpret_cast<uint32_t *>(dst) = neg[0];
+          *reinterpret_cast<uint32_t *>(dst + (KB / 2) * RN * 128) = pos[0];
+        }
+        if (lane == 0) s_unit[r] = two_to(e);
       }
-      // 128-byte rows of 64 elements, 16-byte pieces swizzled by the row; blocks of K RN rows apart
-      constexpr int LB = 64 / E;              // lanes per block
-      const int byte = (lane % LB) * E * 2;
-      unsigned char *dst = sm + (lane / LB) * RN * 128 + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-      if constexpr (E == 4) {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(neg[0], neg[1]);
-        *reinterpret_cast<uint2 *>(dst + (KB / 2) * RN * 128) = make_uint2(pos[0], pos[1]);
-      } else {
-        *reinterpret_cast<uint32_t *>(dst) = neg[0];
-        *reinterpret_cast<uint32_t *>(dst + (KB / 2) * RN * 128) = pos[0];
-      }
-      if (lane == 0) s_unit[r] = two_to(e);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);   // this warp's TMEM lanes
 
     if (warp < kManyEpi) {
-      // ---- epilogue: page (lane) x half of the columns
-      const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+      // ---- epilogue: page (lane) x a quarter of the columns at a time
+      const int part = warp >> 2, row = (warp & 3) * 32 + lane;
       auto exp_of = [&](int tile) -> float {   // 2^e of this thread's page (0: no page)
         const int i = tile * kTilePages + row;
         if (i >= nl) return 0.f;
@@ -700,99 +819,123 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
         return page >= 0 && page < a.n_pages ? two_to(a.exp[static_cast<size_t>(page) * a.H_kv + g]) : 0.f;
       };
       float e_next = exp_of(0);
-      for (int tile = 0; ok && tile < tiles; ++tile, buf.step()) {
+      for (int tile = 0; ok && tile < tiles; ++tile, d_phase ^= 1u) {
         const float e = e_next;
         e_next = exp_of(tile + 1);
-        if (!(ok = warp_wait(&d_full[buf.slot], buf.phase, abort, a.wait_ns))) break;
-        tc_fence_after();
-        const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf.slot * (cols / 2) + half * (rn / 2);
-        const float4 *unit = reinterpret_cast<const float4 *>(s_unit + half * (rn / 2));
         float b0 = -INFINITY, b1 = -INFINITY;
-        for (int c = 0; c < rn / 2; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(src + c, s);
-          tmem_wait_ld();
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = warp_wait(&d_full[h], d_phase, abort, a.wait_ns))) break;
+          tc_fence_after();
+          const int c0 = h * (rn / 2) + part * (rn / 4);
+          const float4 *unit = reinterpret_cast<const float4 *>(s_unit + c0);
+          for (int c = 0; c < rn / 4; c += 16) {
+            uint32_t s[16];
+            tmem_ld16(t_lane + c0 + c, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 u = unit[(c + x) / 4];
-            const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
-            const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
-            b0 = fmax3(b0, y.x, y.y);
-            b1 = fmax3(b1, z.x, z.y);
+            for (int x = 0; x < 16; x += 4) {
+              const float4 u = unit[(c + x) / 4];
+              const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
+              const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
+              b0 = fmax3(b0, y.x, y.y);
+              b1 = fmax3(b1, z.x, z.y);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_empty[h]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[buf.slot]);
-        if (e > 0.f) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * e));
+        if (ok && e > 0.f) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * e));
       }
-    } else if (warp == kManyEpi) {
+    } else if (warp == kManyEpi + kManyConv) {
       // ---- MMA issuer
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      const uint32_t id = idesc_f16_f32(kTilePages, rn);
-      const uint64_t da = sdesc_sw128(smem_u32(sm + L.oSlots), 16, 1024), db = sdesc_sw128(smem_u32(sm), 16, 1024);
-      for (int tile = 0; ok && tile < tiles; ++tile, buf.step()) {
-        if (!(ok = warp_wait(&d_empty[buf.slot], buf.phase ^ 1u, abort, a.wait_ns))) break;
-        tc_fence_after();
-        for (int b = 0; b < KB; ++b, ring.step()) {
-          if (!(ok = warp_wait(&full[ring.slot], ring.phase, abort, a.wait_ns))) break;
+      const uint32_t id = idesc_f16_f32(kTilePages, rn / 2);
+      const uint64_t db = sdesc_sw128(smem_u32(sm), 16, 1024);
+      for (int tile = 0; ok && tile < tiles; ++tile, buf.step(), d_phase ^= 1u) {
+        if (!(ok = warp_wait(&a_full[buf.slot], buf.phase, abort, a.wait_ns))) break;
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = warp_wait(&d_empty[h], d_phase ^ 1u, abort, a.wait_ns))) break;
           tc_fence_after();
 #pragma unroll
-          for (int s = 0; s < 4; ++s)         // (descriptors count 16 bytes)
-            mma_ss(leader, tmem + buf.slot * (cols / 2), da + ring.slot * (kSlotBytes >> 4) + 2 * s,
-                   db + static_cast<uint64_t>(b * RN * 8 + 2 * s), id, b + s > 0);
-          commit_if(leader, &empty[ring.slot]);
+          for (int s = 0; s < 4 * KB; ++s)    // 16 elements of K: 8 columns of A, 32 bytes of B's rows
+            mma_ts(leader, tmem + h * (rn / 2), tmem + RN + buf.slot * A + 8 * s,
+                   db + static_cast<uint64_t>(((s >> 2) * RN + h * (rn / 2)) * 8 + 2 * (s & 3)), id, s > 0);
+          commit_if(leader, &d_full[h]);
         }
-        if (ok) commit_if(leader, &d_full[buf.slot]);
+        if (ok) commit_if(leader, &a_empty[buf.slot]);
       }
     } else {
-      // ---- converters: a thread brings alternate 16-byte pieces of one page's digest row
-      const int ct = tid - (kManyEpi + 1) * 32, row = ct >> 1, hf = ct & 1;
-      auto page_of = [&](int tile) -> int {
-        const int i = tile * kTilePages + row;
-        return i < nl ? table[i] : -1;
-      };
-      uint4 dig[KB][2];
-      auto fetch = [&](int b, int page) {
+      // ---- converters: 16-byte pieces of the digests into a raw tile (PP threads a row), then a thread
+      // per page and half of its row widens them
+      const int ct = tid - kManyEpi * 32, piece = ct % PP, half = ct >> 7, row = ct & 127;
+      constexpr int RPP = kManyConv * 32 / PP, N = kTilePages / RPP;   // rows per pass, passes
+      int ids[N];
+      auto ids_of = [&](int tile) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          dig[b][v] = make_uint4(0, 0, 0, 0);
-          if (page >= 0 && page < a.n_pages)
-            dig[b][v] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + (static_cast<size_t>(page) * a.H_kv + g) * 2 * D +
-                                                              b * 64 + v * 32 + hf * 16));
+        for (int i = 0; i < N; ++i) {
+          const int x = tile * kTilePages + ct / PP + i * RPP;
+          ids[i] = x < nl ? table[x] : -1;
         }
       };
-      const int page0 = page_of(0);
-      int page = page_of(1);
+      auto fetch = [&](int tile) {            // the tile of `ids`
+        unsigned char *raw = sm + L.oRaw + (tile & 1) * kTilePages * 2 * D;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) fetch(b, page0);
-      for (int tile = 0; ok && tile < tiles; ++tile) {
-        const int page_next = page_of(tile + 2);
+        for (int i = 0; i < N; ++i) {
+          const int r = ct / PP + i * RPP;
+          const bool good = ids[i] >= 0 && ids[i] < a.n_pages;
+          cp_async_16_or_0(raw + r * 2 * D + ((piece ^ (r & (PP - 1))) << 4),
+                           a.bounds + (static_cast<size_t>(good ? ids[i] : 0) * a.H_kv + g) * 2 * D + piece * 16, good);
+        }
+        cp_async_commit();
+      };
+      if (tiles > 0) {
+        ids_of(0);
+        fetch(0);
+        ids_of(1);
+      }
+      for (int tile = 0; tile < tiles; ++tile, buf.step()) {
+        if (tile + 1 < tiles) {
+          fetch(tile + 1);
+          ids_of(tile + 2);
+          cp_async_wait<1>();
+        } else {
+          cp_async_wait<0>();
+        }
+        named_bar_sync(1, kManyConv * 32);    // the tile is there for all (every converter comes here, ok or not)
+        if (ok) ok = warp_wait(&a_empty[buf.slot], buf.phase ^ 1u, abort, a.wait_ns);
+        if (ok) {
+          tc_fence_after();
+          const unsigned char *raw = sm + L.oRaw + (tile & 1) * kTilePages * 2 * D + row * 2 * D;
+          // half a row: PP / 2 pieces, 8 columns each
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          if (!ok || !(ok = warp_wait(&empty[ring.slot], ring.phase ^ 1u, abort, a.wait_ns))) break;
-          unsigned char *dst = sm + L.oSlots + ring.slot * kSlotBytes + row * 128;
+          for (int p = 0; p < PP / 2; p += 2) {
+            uint32_t h[16];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint2 x = widen_s8(dig[b][v].x), y = widen_s8(dig[b][v].y), z = widen_s8(dig[b][v].z),
-                        w = widen_s8(dig[b][v].w);
-            const int c = v * 4 + hf * 2;
-            *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-            *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, w.x, w.y);
+            for (int q = 0; q < 2; ++q) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(raw + (((half * (PP / 2) + p + q) ^ (row & (PP - 1))) << 4));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint2 y = widen_s8(w[x]);
+                h[8 * q + 2 * x] = y.x;
+                h[8 * q + 2 * x + 1] = y.y;
+              }
+            }
+            tmem_st16(t_lane + RN + buf.slot * A + half * (A / 2) + 8 * p, h);
           }
-          if (tile + 1 < tiles) fetch(b, page);
-          fence_proxy_async_smem();
+          tmem_wait_st();
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[ring.slot]);
-          ring.step();
+          if (lane == 0) mbar_arrive(&a_full[buf.slot]);
         }
-        page = page_next;
+        named_bar_sync(1, kManyConv * 32);    // the raw tile is read
       }
     }
     ok = __syncthreads_and(ok);               // (also: every score of these rows is in)
     if (!ok) break;
   }
-  if (warp == kManyEpi) {
+  if (warp == kManyEpi + kManyConv) {
     // the tensor core is idle before its memory goes, also where a wait ran out
     commit_if(lane == 0, drained);
     const uint64_t t0 = global_ns();
@@ -801,12 +944,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     tmem_dealloc(*tmem_slot, cols);
     if (lane == 0 && !ok) atomicOr(&g_select_error, 1);
   }
+  if (rank == 0 && warp == 0) put_fixed(a, j, g, k);
   __syncthreads();
   pick<kManyThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
 }
 
 constexpr size_t kManyBytes = 227 * 1024;   // dynamic shared memory, at most
-static_assert(128 * 4 * 128 + kSlots * kSlotBytes + 128 * 4 + 256 + sizeof(SelectShared) + 16 + kSelectMaxPages / 16 * 4 <= kManyBytes, "widest table");
+static_assert(many_layout(128, 128).oKey + kSelectMaxPages / 16 * 4 <= kManyBytes, "widest table");
 
 template <typename Kern>
 cudaError_t launch_cluster(Kern kern, int items, int C, int threads, size_t smem, cudaStream_t s, const PageSelectArgs &a) {
@@ -834,8 +978,8 @@ template <int D>
 cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   const int items = a.n_blocks * a.H_kv, rows = a.cfg.q_block * (a.H_q / a.H_kv);
   const bool few = rows <= kFewRows;
-  // CTAs of an item: until the launch has one per SM, or a CTA a page per thread (a tile)
-  const int least = few ? kFewThreads : kTilePages;
+  // CTAs of an item: until the launch has one per SM, or a CTA a tile (16 pages a warp)
+  const int least = kTilePages;
   int C = 1;
   while (C < 16 && items * C < 152 && a.max_pages > C * least) C *= 2;
   a.slice = (a.max_pages + C - 1) / C;
@@ -844,7 +988,8 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
     a.slice = (a.max_pages + C - 1) / C;
   }
   const size_t keys = static_cast<size_t>(a.slice) * 4;
-  if (few) return launch_cluster(select_few_kernel<D>, items, C, kFewThreads, keys, s, a);
+  if (rows <= 8) return launch_cluster(select_few_kernel<D, 1>, items, C, kFewThreads, keys, s, a);
+  if (few) return launch_cluster(select_few_kernel<D, 2>, items, C, kFewThreads, keys, s, a);
   // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
   a.rows = std::min((rows + 63) & ~63, 256);
   if (many_layout(D, a.rows).oKey + keys > kManyBytes) a.rows = 128;

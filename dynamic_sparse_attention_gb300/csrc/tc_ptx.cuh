@@ -156,6 +156,14 @@ __device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, 
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
 // arrive on `bar` when every tensor-core instruction issued so far has completed
 __device__ __forceinline__ void commit_if(uint32_t pred, uint64_t *bar) {
   asm volatile(
