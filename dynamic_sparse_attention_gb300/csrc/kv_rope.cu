@@ -53,14 +53,15 @@ __device__ __forceinline__ uint4 pack8(const float *y) {
 // (2 i, 2 i + 1) lie inside a piece), the lanes behind those two neighbours of the rest.  A lane
 // then turns 8 pairs by the same 8 angles in every row of the token.
 template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(kThreads) kv_rope_kernel(const RopeWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kv_rope_kernel(const RopeWriteArgs a) {
   constexpr int LPR = D / 16;                 // lanes per row
   constexpr int RPW = 32 / LPR;               // rows per warp at a time
   constexpr int APL = 8 / RPW;                // angles that a lane computes (its row group's share of 8)
   __shared__ long long s_slot[kMaxTok];       // page * page_size + offset; -1: no page; -2: no chunk
   __shared__ int s_pos[kMaxTok];
   __shared__ unsigned long long s_freq[D / 2];
-  __shared__ float s_w[2][D];
+  __shared__ __align__(16) float s_w[2][D];
+  __shared__ __align__(16) float s_turn[kWarps][2][LPR][8];   // cosine, sine of the warp's token
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n0 = blockIdx.x * a.tpc, n1 = min(a.n_tok, n0 + a.tpc);
   grid_dep_wait();
@@ -112,45 +113,53 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const RopeWriteArgs a
     const long long slot = s_slot[i];
     if (slot == -2) continue;                 // the whole warp
     const size_t n = static_cast<size_t>(n0) + i;
-    // the token's 8 angles of this lane, computed once by the row groups together
-    float cs[8], sn[8];
-    {
-      float c[APL], s[APL];
-      const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(s_pos[i]));
-#pragma unroll
-      for (int x = 0; x < APL; ++x) {
-        const int t = rg * APL + x;           // which of the 8
-        const int f = INTER ? (t < 4 ? 4 * p0 + t : 4 * p1 + t - 4) : 8 * l + t;
-        c[x] = 1.f;
-        s[x] = 0.f;
-        if (turns) {
-          const int frac = static_cast<int>((s_freq[f] * pos) >> 32);   // of a turn, times 2^32
-          sincospif(static_cast<float>(frac) * 0x1p-31f, &s[x], &c[x]);
-          c[x] *= a.cfg.rope_scale;
-          s[x] *= a.cfg.rope_scale;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        cs[t] = __shfl_sync(kFull, c[t % APL], t / APL * LPR + l);
-        sn[t] = __shfl_sync(kFull, s[t % APL], t / APL * LPR + l);
-      }
-    }
-    for (int r0 = (warp % a.wpt) * RPW; r0 < rows; r0 += a.wpt * RPW) {
+    // row group r0 of the token (the lane's row of it)
+    auto fetch = [&](int r0, uint4 &u0, uint4 &u1) {
       const int r = r0 + rg;
       const bool is_q = r < a.H_q, is_k = !is_q && r < a.H_q + a.H_kv;
       const int h = is_q ? r : is_k ? r - a.H_q : r - a.H_q - a.H_kv;
-      const bool live = r < rows && (is_q || slot >= 0);
-      uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-      if (live) {
+      u0 = u1 = make_uint4(0, 0, 0, 0);
+      if (r < rows && (is_q || slot >= 0)) {
         const uint16_t *src = (is_q ? a.q + n * a.q_stride : is_k ? a.k_new + n * a.k_stride : a.v_new + n * a.v_stride) +
                               static_cast<size_t>(h) * D;
         u0 = __ldcs(reinterpret_cast<const uint4 *>(src) + p0);
         u1 = __ldcs(reinterpret_cast<const uint4 *>(src) + p1);
       }
+    };
+    // two groups at a time, the next two requested meanwhile (the angles wait in shared memory: their 16
+    // registers are what lets a third CTA run)
+    const int step = a.wpt * RPW, first = (warp % a.wpt) * RPW;
+    uint4 u0, u1, v0, v1;
+    fetch(first, u0, u1);
+    fetch(first + step, v0, v1);
+    // the token's 8 angles of this lane, each computed by one row group for all
+    __syncwarp();
+    {
+      const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(s_pos[i]));
+#pragma unroll
+      for (int x = 0; x < APL; ++x) {
+        const int t = rg * APL + x;           // which of the 8
+        const int f = INTER ? (t < 4 ? 4 * p0 + t : 4 * p1 + t - 4) : 8 * l + t;
+        if (turns) {
+          const int frac = static_cast<int>((s_freq[f] * pos) >> 32);   // of a turn, times 2^32
+          float c, s;
+          sincospif(static_cast<float>(frac) * 0x1p-31f, &s, &c);
+          s_turn[warp][0][l][t] = c * a.cfg.rope_scale;
+          s_turn[warp][1][l][t] = s * a.cfg.rope_scale;
+        }
+      }
+    }
+    __syncwarp();
+    auto cs = [&](int e) -> float { return s_turn[warp][0][l][e]; };
+    auto sn = [&](int e) -> float { return s_turn[warp][1][l][e]; };
+    auto process = [&](int r0, const uint4 &w0, const uint4 &w1) {
+      const int r = r0 + rg;
+      const bool is_q = r < a.H_q, is_k = !is_q && r < a.H_q + a.H_kv;
+      const int h = is_q ? r : is_k ? r - a.H_q : r - a.H_q - a.H_kv;
+      const bool live = r < rows && (is_q || slot >= 0);
       float y0[8], y1[8];
-      unpack16(u0, y0, uint16_t());
-      unpack16(u1, y1, uint16_t());
+      unpack16(w0, y0, uint16_t());
+      unpack16(w1, y1, uint16_t());
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(y0[e], y0[e], fmaf(y1[e], y1[e], ss));
@@ -171,17 +180,17 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const RopeWriteArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = y0[2 * e], z = y0[2 * e + 1], v = y1[2 * e], w = y1[2 * e + 1];
-              y0[2 * e] = x * cs[e] - z * sn[e];
-              y0[2 * e + 1] = z * cs[e] + x * sn[e];
-              y1[2 * e] = v * cs[4 + e] - w * sn[4 + e];
-              y1[2 * e + 1] = w * cs[4 + e] + v * sn[4 + e];
+              y0[2 * e] = x * cs(e) - z * sn(e);
+              y0[2 * e + 1] = z * cs(e) + x * sn(e);
+              y1[2 * e] = v * cs(4 + e) - w * sn(4 + e);
+              y1[2 * e + 1] = w * cs(4 + e) + v * sn(4 + e);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float x = y0[e], z = y1[e];
-              y0[e] = x * cs[e] - z * sn[e];
-              y1[e] = z * cs[e] + x * sn[e];
+              y0[e] = x * cs(e) - z * sn(e);
+              y1[e] = z * cs(e) + x * sn(e);
             }
           }
         }
@@ -221,9 +230,16 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const RopeWriteArgs a
                              : static_cast<uint16_t *>(is_k ? a.k_pages : a.v_pages) +
                                    (static_cast<size_t>(slot) * a.H_kv + h) * D;
         const bool same = !is_q && !is_k;     // values pass as they are
-        reinterpret_cast<uint4 *>(dst)[p0] = same ? u0 : pack8(y0);
-        reinterpret_cast<uint4 *>(dst)[p1] = same ? u1 : pack8(y1);
+        reinterpret_cast<uint4 *>(dst)[p0] = same ? w0 : pack8(y0);
+        reinterpret_cast<uint4 *>(dst)[p1] = same ? w1 : pack8(y1);
       }
+    };
+    for (int r0 = first; r0 < rows; r0 += 2 * step) {
+      const uint4 w0 = u0, w1 = u1, x0 = v0, x1 = v1;
+      fetch(r0 + 2 * step, u0, u1);
+      fetch(r0 + 3 * step, v0, v1);
+      process(r0, w0, w1);
+      if (r0 + step < rows) process(r0 + step, x0, x1);
     }
   }
 }

@@ -39,7 +39,7 @@ std::atomic<unsigned long long> g_wait_limit_ns{500000000ull};   // of later lau
 // ------------------------------------------------------------------ digests
 
 constexpr int kDigestThreads = 256, kDigestWarps = kDigestThreads / 32;
-constexpr int kMaxWindow = 64;
+constexpr int kMaxWindow = 128;
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN loses
   uint32_t r;
@@ -766,39 +766,59 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     __syncthreads();                          // the rows before are read (and the barriers are there)
     const int rows = min(RN, R - r0);
     const int rn = (rows + 63) & ~63;         // columns in use; those behind the last row repeat it
-    constexpr int U = 8, W = kManyThreads / 32;   // rows a warp asks for at once
-    for (int r1 = warp; r1 < rn; r1 += U * W) {
-      constexpr int E = D / 32;
-      uint32_t w[U][E / 2];
+    // D / 8 lanes hold 8 elements of a row each; a warp asks for U steps of its rows at once
+    constexpr int LPR = D / 8, RPW = 32 / LPR, U = 8, W = kManyThreads / 32 * RPW;
+    const int G = a.H_q / a.H_kv, piece = lane % LPR;
+    for (int r1 = warp * RPW + lane / LPR; r1 - lane / LPR < rn; r1 += U * W) {
+      uint4 w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r1 + u * W < rn) load_row<D>(a, k, g, r0 + min(r1 + u * W, rows - 1), w[u]);
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + min(r1 + u * W, rows - 1);
+        w[u] = __ldg(reinterpret_cast<const uint4 *>(a.q + static_cast<size_t>(k.lo + r / G) * a.q_stride +
+                                                     static_cast<size_t>(g * G + r % G) * D) + piece);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = r1 + u * W;
-        if (r >= rn) break;
-        float x[E];
-        const int e = row_of<D>(w[u], x);
-        const float inv = two_to(-e);
-        uint32_t neg[E / 2], pos[E / 2];
+        if (r - lane / LPR >= rn) break;      // (the whole warp)
+        const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        uint32_t m2 = __vmaxu2(__vmaxu2(x[0] & kAbs, x[1] & kAbs), __vmaxu2(x[2] & kAbs, x[3] & kAbs));
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        const bool odd = __any_sync(kFull, m >= 0x7f80u);   // infinities or NaN among them: rare
+        if (odd) {
+          m = 0;
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const int v = whole(x[i] * inv), y = whole(x[i + 1] * inv);
-          neg[i / 2] = pack_f16x2(static_cast<float>(min(v, 0)), static_cast<float>(min(y, 0)));
-          pos[i / 2] = pack_f16x2(static_cast<float>(max(v, 0)), static_cast<float>(max(y, 0)));
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t v = (x[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+            m = max(m, v < 0x7f80u ? v : 0u);
+          }
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        const int e = exponent127(m << 16);
+        const float inv = two_to(-e);
+        uint32_t neg[4], pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // nearest whole number, ties to even: the sum's last place is 1 (conversions to integers and
+          // back have a quarter of the rate)
+          constexpr float kMagic = 12582912.f;
+          float v = fmaf(bf16_lo(x[i]), inv, kMagic) - kMagic, y = fmaf(bf16_hi(x[i]), inv, kMagic) - kMagic;
+          if (odd) {
+            v = v == v ? v : 0.f;
+            y = y == y ? y : 0.f;
+          }
+          neg[i] = pack_f16x2(fmaxf(fminf(v, 0.f), -127.f), fmaxf(fminf(y, 0.f), -127.f));
+          pos[i] = pack_f16x2(fminf(fmaxf(v, 0.f), 127.f), fminf(fmaxf(y, 0.f), 127.f));
         }
         // 128-byte rows of 64 elements, 16-byte pieces swizzled by the row; blocks of K RN rows apart
-        constexpr int LB = 64 / E;            // lanes per block
-        const int byte = (lane % LB) * E * 2;
-        unsigned char *dst = sm + (lane / LB) * RN * 128 + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-        if constexpr (E == 4) {
-          *reinterpret_cast<uint2 *>(dst) = make_uint2(neg[0], neg[1]);
-          *reinterpret_cast<uint2 *>(dst + (KB / 2) * RN * 128) = make_uint2(pos[0], pos[1]);
-        } else {
-          *reinterpret_cast<uint32_t *>(dst) = neg[0];
-          *reinterpret_cast<uint32_t *>(dst + (KB / 2) * RN * 128) = pos[0];
+        if (r < rn) {
+          unsigned char *dst = sm + (piece >> 3) * RN * 128 + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+          *reinterpret_cast<uint4 *>(dst + (KB / 2) * RN * 128) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+          if (piece == 0) s_unit[r] = two_to(e);
         }
-        if (lane == 0) s_unit[r] = two_to(e);
       }
     }
     fence_proxy_async_smem();
@@ -850,7 +870,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     } else if (warp == kManyEpi + kManyConv) {
       // ---- MMA issuer
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      const uint32_t id = idesc_f16_f32(kTilePages, rn / 2);
+      // (operands the same for the whole warp, as the compiler can see: see tc_ptx.cuh)
+      const uint32_t half = __shfl_sync(kFull, rn / 2, 0), tm = __shfl_sync(kFull, tmem, 0);
+      const uint32_t id = idesc_f16_f32(kTilePages, static_cast<int>(half));
       const uint64_t db = sdesc_sw128(smem_u32(sm), 16, 1024);
       for (int tile = 0; ok && tile < tiles; ++tile, buf.step(), d_phase ^= 1u) {
         if (!(ok = warp_wait(&a_full[buf.slot], buf.phase, abort, a.wait_ns))) break;
@@ -859,8 +881,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < 4 * KB; ++s)    // 16 elements of K: 8 columns of A, 32 bytes of B's rows
-            mma_ts(leader, tmem + h * (rn / 2), tmem + RN + buf.slot * A + 8 * s,
-                   db + static_cast<uint64_t>(((s >> 2) * RN + h * (rn / 2)) * 8 + 2 * (s & 3)), id, s > 0);
+            mma_ts(leader, tm + h * half, tm + RN + buf.slot * A + 8 * s,
+                   db + static_cast<uint64_t>(((s >> 2) * RN + h * half) * 8 + 2 * (s & 3)), id, s > 0);
           commit_if(leader, &d_full[h]);
         }
         if (ok) commit_if(leader, &a_empty[buf.slot]);
@@ -1002,10 +1024,9 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
 cudaError_t launch_page_digest(const DigestArgs &a0, cudaStream_t s) {
   DigestArgs a = a0;
   while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
-  // token rows per CTA: a page's worth in a long chunk, fewer where each row may be a page of its
-  // own and the launch would not fill the GPU
+  // token rows per CTA: as many as leave four CTAs an SM, one where each row may be a page of its own
   a.window = 1;
-  while (a.window < kMaxWindow && a.window < a.page_size && a.n_tok / (2 * a.window) >= 152) a.window *= 2;
+  while (a.window < kMaxWindow && a.n_tok / (2 * a.window) >= 4 * 152) a.window *= 2;
   const dim3 grid((a.n_tok + a.window - 1) / a.window, (a.H_kv + kDigestWarps - 1) / kDigestWarps);
   ProfScope ps("page_digest", s);
   if (a.fp8)
