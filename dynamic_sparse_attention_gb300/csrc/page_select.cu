@@ -38,8 +38,8 @@ std::atomic<unsigned long long> g_wait_limit_ns{500000000ull};   // of later lau
 
 // ------------------------------------------------------------------ digests
 
-constexpr int kDigestThreads = 256, kDigestWarps = kDigestThreads / 32;
-constexpr int kMaxWindow = 128;
+constexpr int kDigestThreads = 256, kDigestPairs = kDigestThreads / 64;
+constexpr int kMaxWindow = 1024, kDigestHeads = 2;   // token rows and heads of a CTA
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN loses
   uint32_t r;
@@ -86,16 +86,18 @@ __device__ __forceinline__ bool is_inf(uint32_t w) {
   return (w & 0x7fffu) == 0x7f80u || ((w >> 16) & 0x7fffu) == 0x7f80u;
 }
 
-// A warp digests one page of one head: D / 8 lanes hold 8 channels of a token each, the warp's
-// 256 / D groups of them take the page's tokens in turn, with running bounds in registers.
+// Two warps digest one page of one head: D / 8 lanes hold 8 channels of a token each, the groups of
+// them take the page's tokens in turn with running bounds in registers, and the second warp
+// hands its bounds to the first.
 template <int D, bool FP8>
-__device__ void digest_page(const DigestArgs &a, int page, int head, int keys) {
+__device__ void digest_page(const DigestArgs &a, int page, int head, int keys, uint4 (*s_part)[32] /* [2] */) {
   constexpr int LPT = D / 8, TPW = 32 / LPT, U = 8;   // lanes per token, tokens per step, steps in flight
   const int lane = threadIdx.x & 31, piece = lane % LPT, t0 = lane / LPT;
+  const int second = (threadIdx.x >> 5) & 1, bar = 1 + (threadIdx.x >> 6);
   const size_t row0 = (static_cast<size_t>(page) << a.lg_page) * a.H_kv + head;
   constexpr uint32_t kNan2 = 0x7fff7fffu;
   uint32_t lo[4] = {kNan2, kNan2, kNan2, kNan2}, hi[4] = {kNan2, kNan2, kNan2, kNan2};
-  for (int t = t0; t < keys; t += U * TPW) {
+  for (int t = t0 + second * U * TPW; t < keys; t += 2 * U * TPW) {
     uint4 u[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -111,6 +113,22 @@ __device__ void digest_page(const DigestArgs &a, int page, int head, int keys) {
       }
     }
   }
+  if (second) {
+    s_part[0][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    s_part[1][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+  named_bar_sync(bar, 64);
+  if (!second) {
+    const uint4 l = s_part[0][lane], h = s_part[1][lane];
+    const uint32_t w[4] = {l.x, l.y, l.z, l.w}, x[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      lo[c] = min2(lo[c], w[c]);
+      hi[c] = max2(hi[c], x[c]);
+    }
+  }
+  named_bar_sync(bar, 64);                    // read: the next page's may be written
+  if (second) return;
 #pragma unroll
   for (int o = LPT; o < 32; o <<= 1)
 #pragma unroll
@@ -168,46 +186,63 @@ __device__ void digest_page(const DigestArgs &a, int page, int head, int keys) {
   }
 }
 
-// A CTA takes the pages whose first row of a chunk lies in its `window` token rows, every head of
-// them a warp's work; gridDim.y CTAs share the heads.
+// A CTA takes the pages whose first row of a chunk lies in its `window` token rows, for kDigestHeads
+// heads.  (As many CTAs as fit the GPU four times, however long the chunks: with a CTA for each page
+// and a warp for each of its heads 58 us for a prompt of 128K tokens, the last of four rounds nearly
+// empty.)
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kDigestThreads) digest_kernel(const DigestArgs a) {
+__global__ void __launch_bounds__(kDigestThreads, 4) digest_kernel(const DigestArgs a) {
   __shared__ int s_seq[kMaxWindow];
   __shared__ int s_page[kMaxWindow], s_keys[kMaxWindow];
+  __shared__ uint4 s_part[kDigestPairs][2][32];
   __shared__ int s_n;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int n0 = blockIdx.x * a.window, n1 = min(a.n_tok, n0 + a.window);
+  const int h0 = blockIdx.y * kDigestHeads, nh = min(kDigestHeads, a.H_kv - h0);
   grid_dep_wait();
-  if (tid < kMaxWindow) s_seq[tid] = -1;
+  for (int i = tid; i < a.window; i += kDigestThreads) s_seq[i] = -1;
   if (tid == 0) s_n = 0;
   __syncthreads();
-  for (int b = tid; b < a.B; b += kDigestThreads) {
-    const int qs = a.q_start[b], qe = a.q_start[b + 1];
-    DSA_CHECK(qs >= 0 && qe <= a.n_tok);
-    for (int n = max(qs, n0); n < min(qe, n1); ++n) s_seq[n - n0] = b;
+  for (int b0 = tid & ~31; b0 < a.B; b0 += kDigestThreads) {
+    // the rows of a warp's sequences, marked by all of its lanes
+    int lo = 0, hi = 0;
+    if (b0 + lane < a.B) {
+      const int qs = a.q_start[b0 + lane], qe = a.q_start[b0 + lane + 1];
+      DSA_CHECK(qs >= 0 && qe <= a.n_tok);
+      lo = max(qs, n0);
+      hi = min(qe, n1);
+    }
+    uint32_t some = __ballot_sync(kFull, lo < hi);
+    while (some) {
+      const int src = __ffs(some) - 1;
+      some &= some - 1;
+      const int x = __shfl_sync(kFull, lo, src), y = __shfl_sync(kFull, hi, src);
+      for (int n = x + lane; n < y; n += 32) s_seq[n - n0] = b0 + src;
+    }
   }
   __syncthreads();
-  if (tid < n1 - n0 && s_seq[tid] >= 0) {
-    const int b = s_seq[tid], n = n0 + tid;
+  for (int i = tid; i < n1 - n0; i += kDigestThreads) {
+    const int b = s_seq[i], n = n0 + i;
+    if (b < 0) continue;
     const int qs = a.q_start[b], qe = a.q_start[b + 1], cap = a.max_pages << a.lg_page;
     const int kv = min(max(a.kv_len[b], 0), cap);
     DSA_CHECK(kv == a.kv_len[b]);
     const long long pos = kv - (static_cast<long long>(qe) - n);
     if (pos >= 0 && ((pos & (a.page_size - 1)) == 0 || n == qs)) {
-      const int i = static_cast<int>(pos >> a.lg_page);
-      const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + i];
+      const int p = static_cast<int>(pos >> a.lg_page);
+      const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + p];
       DSA_CHECK(page >= 0 && page < a.n_pages);
       if (page >= 0 && page < a.n_pages) {
         const int at = atomicAdd(&s_n, 1);   // (any order: each page is its own work)
         s_page[at] = page;
-        s_keys[at] = min(a.page_size, kv - (i << a.lg_page));
+        s_keys[at] = min(a.page_size, kv - (p << a.lg_page));
       }
     }
   }
   __syncthreads();
-  const int work = s_n * a.H_kv;
-  for (int i = blockIdx.y * kDigestWarps + warp; i < work; i += gridDim.y * kDigestWarps)
-    digest_page<D, FP8>(a, s_page[i / a.H_kv], i % a.H_kv, s_keys[i / a.H_kv]);
+  const int work = s_n * nh, pair = tid >> 6;
+  for (int i = pair; i < work; i += kDigestPairs)
+    digest_page<D, FP8>(a, s_page[i / nh], h0 + i % nh, s_keys[i / nh], s_part[pair]);
 }
 
 // ------------------------------------------------------------------ selection
@@ -765,7 +800,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   for (int r0 = 0; r0 < R; r0 += RN) {
     __syncthreads();                          // the rows before are read (and the barriers are there)
     const int rows = min(RN, R - r0);
-    const int rn = (rows + 63) & ~63;         // columns in use; those behind the last row repeat it
+    const int rn = RN;                        // columns (those behind the last row repeat it)
     // D / 8 lanes hold 8 elements of a row each; a warp asks for U steps of its rows at once
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = 8, W = kManyThreads / 32 * RPW;
     const int G = a.H_q / a.H_kv, piece = lane % LPR;
@@ -870,8 +905,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     } else if (warp == kManyEpi + kManyConv) {
       // ---- MMA issuer
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      // (operands the same for the whole warp, as the compiler can see: see tc_ptx.cuh)
-      const uint32_t half = __shfl_sync(kFull, rn / 2, 0), tm = __shfl_sync(kFull, tmem, 0);
+      const uint32_t half = static_cast<uint32_t>(RN) / 2, tm = __shfl_sync(kFull, tmem, 0);
       const uint32_t id = idesc_f16_f32(kTilePages, static_cast<int>(half));
       const uint64_t db = sdesc_sw128(smem_u32(sm), 16, 1024);
       for (int tile = 0; ok && tile < tiles; ++tile, buf.step(), d_phase ^= 1u) {
@@ -1024,10 +1058,12 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
 cudaError_t launch_page_digest(const DigestArgs &a0, cudaStream_t s) {
   DigestArgs a = a0;
   while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
-  // token rows per CTA: as many as leave four CTAs an SM, one where each row may be a page of its own
-  a.window = 1;
-  while (a.window < kMaxWindow && a.n_tok / (2 * a.window) >= 4 * 152) a.window *= 2;
-  const dim3 grid((a.n_tok + a.window - 1) / a.window, (a.H_kv + kDigestWarps - 1) / kDigestWarps);
+  // token rows per CTA: an equal share of a launch that fills the GPU once with four CTAs an SM; a few
+  // at least, unless each may be a page of its own
+  const int heads = (a.H_kv + kDigestHeads - 1) / kDigestHeads;
+  const int ctas = std::max(1, 4 * 152 / heads);
+  a.window = std::min(std::max((a.n_tok + ctas - 1) / ctas, 1), kMaxWindow);
+  const dim3 grid((a.n_tok + a.window - 1) / a.window, heads);
   ProfScope ps("page_digest", s);
   if (a.fp8)
     return a.D == 128 ? launch_pdl(digest_kernel<128, true>, grid, dim3(kDigestThreads), 0, s, a)
