@@ -307,9 +307,9 @@ struct PageSelectArgs {
   dsa_page_select_cfg cfg;
   int n_blocks, max_list;
   int32_t *sel_q_start, *sel_kv_len, *sel_table, *sel_index;
-  // (launcher) log2 of page_size, scores a CTA has room for, rows it holds at a time, limit of a wait
-  int lg_page, slice, rows;
-  unsigned long long wait_ns;
+  // (launcher) log2 of page_size, scores a CTA has room for, limit of a wait
+  int lg_page, slice;
+  uint32_t wait_clocks;
 };
 constexpr int kSelectMaxPages = 262144;
 cudaError_t launch_page_select(const PageSelectArgs &a, cudaStream_t s);

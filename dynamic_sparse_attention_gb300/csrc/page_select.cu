@@ -590,13 +590,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
   const int p_first = k.s0 + min(n, rank * per), nl = min(k.first, p_first + per) - p_first;
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
   const int tasks = (nl + 15) / 16;
-  // digests (and 2^e of the page that the lane writes the key of) of a task, requested ahead
+  // digests (and the exponent of the page that the lane writes the key of) of a task, requested ahead
   auto ids_of = [&](int task) -> int {
-    const int i = task * 16 + (lane & 15);
-    return i < nl ? table[i] : -1;
+    const int i = task * 16 + (lane & 15), id = i < nl ? table[i] : -1;
+    DSA_CHECK(i >= nl || (id >= 0 && id < a.n_pages));
+    return id;
   };
   uint4 ra[P], rb[P];
-  float e_next = 0.f;
+  constexpr int kNone = 128;                  // (no exponent)
+  int e_next = kNone;
   auto fetch = [&](int ids) {
     const int pa = __shfl_sync(kFull, ids, gr), pb = __shfl_sync(kFull, ids, gr + 8);
     const bool oka = pa >= 0 && pa < a.n_pages, okb = pb >= 0 && pb < a.n_pages;
@@ -606,8 +608,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
       ra[i] = oka ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + rowa * 2 * D) + i * 4 + t) : make_uint4(0, 0, 0, 0);
       rb[i] = okb ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + rowb * 2 * D) + i * 4 + t) : make_uint4(0, 0, 0, 0);
     }
-    e_next = 0.f;
-    if (t < 2 && (t ? okb : oka)) e_next = two_to(a.exp[t ? rowb : rowa]);
+    e_next = t < 2 && (t ? okb : oka) ? a.exp[t ? rowb : rowa] : kNone;   // (looked at a task later)
   };
   const int ids0 = ids_of(warp);
   int ids = ids_of(warp + kFewThreads / 32);
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
         for (int c = 0; c < NT8; ++c) mma_16816_f16(acc[c][x & 1], af, bq[c][i][2 * x], bq[c][i][2 * x + 1]);
       }
     }
-    const float e = e_next;
+    const int e = e_next;
     const int next = ids;
     ids = ids_of(task + 2 * (kFewThreads / 32));
     fetch(next);                              // (all -1 behind the last task: nothing is read)
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
       sb = fmaxf(sb, __shfl_xor_sync(kFull, sb, o));
     }
     const int i = task * 16 + gr + 8 * t;
-    if (t < 2 && i < nl) s_key[i] = e > 0.f ? ordered_key((t ? sb : sa) * e) : 0u;   // no page: below every score
+    if (t < 2 && i < nl) s_key[i] = e != kNone ? ordered_key((t ? sb : sa) * two_to(e)) : 0u;   // no page: below every score
   }
   if (rank == 0 && warp == kFewThreads / 32 - 1) put_fixed(a, j, g, k);
   __syncthreads();
@@ -710,12 +711,12 @@ constexpr int kManyEpi = 8, kManyConv = 8;                       // warps: epilo
 constexpr int kManyThreads = (kManyEpi + kManyConv + 1) * 32;
 constexpr int kTilePages = 128;
 
-// The whole warp waits, at most `limit` ns; the outcome is warp-uniform.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit) {
-  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-  const uint64_t t0 = global_ns();
+// The whole warp waits, at most `limit` clocks; the outcome is warp-uniform.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t limit) {
+  if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
   do {
-    if (__any_sync(kFull, *abort || global_ns() - t0 > limit)) {
+    if (__any_sync(kFull, *abort || static_cast<uint32_t>(clock()) - t0 > limit)) {
       *abort = 1;
       return false;
     }
@@ -742,14 +743,13 @@ __device__ __forceinline__ void cp_async_16_or_0(void *dst, const void *src, boo
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 16 : 0));
 }
 
-template <int D>
+template <int D, int RN>                      // RN: rows held at a time, 64, 128 or 256
 __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const PageSelectArgs a) {
   constexpr int KB = 2 * D / 64;              // 64-element blocks of K
   constexpr int A = D;                        // TMEM columns of a tile's digests (2 D fp16)
   constexpr int PP = 2 * D / 16;              // 16-byte pieces of a digest row
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int RN = a.rows;                      // rows held at a time
-  const ManyLayout L = many_layout(D, RN);
+  constexpr ManyLayout L = many_layout(D, RN);
   SelectShared &sh = *reinterpret_cast<SelectShared *>(sm + L.oShared);
   float *s_unit = reinterpret_cast<float *>(sm + L.oUnit);
   uint64_t *a_full = reinterpret_cast<uint64_t *>(sm + L.oBar), *a_empty = a_full + 2, *d_full = a_empty + 2,
@@ -776,13 +776,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   const int R = k.n * (a.H_q / a.H_kv);
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
   const int tiles = (nl + kTilePages - 1) / kTilePages;
-  const uint32_t cols = RN + 2 * A <= 256 ? 256u : 512u;          // TMEM: scores of RN rows, two tiles
+  constexpr uint32_t cols = RN + 2 * A <= 256 ? 256u : 512u;          // TMEM: scores of RN rows, two tiles
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&a_full[s], kManyConv);
       mbar_init(&a_empty[s], 1);
       mbar_init(&d_full[s], 1);
-      mbar_init(&d_empty[s], kManyEpi);
+      mbar_init(&d_empty[s], kManyEpi / 2);
     }
     mbar_init(drained, 1);
     *abort = 0;
@@ -864,62 +864,72 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);   // this warp's TMEM lanes
 
     if (warp < kManyEpi) {
-      // ---- epilogue: page (lane) x a quarter of the columns at a time
-      const int part = warp >> 2, row = (warp & 3) * 32 + lane;
-      auto exp_of = [&](int tile) -> float {   // 2^e of this thread's page (0: no page)
-        const int i = tile * kTilePages + row;
-        if (i >= nl) return 0.f;
-        const int page = table[i];
-        DSA_CHECK(page >= 0 && page < a.n_pages);
-        return page >= 0 && page < a.n_pages ? two_to(a.exp[static_cast<size_t>(page) * a.H_kv + g]) : 0.f;
+      // ---- epilogue: page (lane) x columns; four warps read one half's scores while the others read the
+      // other's
+      const int h = warp >> 2, row = (warp & 3) * 32 + lane;
+      // this thread's page two tiles ahead and its exponent one ahead (looked at when used, so that
+      // neither load is waited for: 1.9 us a tile otherwise)
+      auto page_of = [&](int tile) -> int {
+        const int i = tile * kTilePages + row, page = i < nl ? table[i] : -1;
+        DSA_CHECK(i >= nl || (page >= 0 && page < a.n_pages));
+        return page;
       };
-      float e_next = exp_of(0);
+      constexpr int kNone = 128;               // (no exponent)
+      auto exp_of = [&](int page) -> int {
+        return page >= 0 && page < a.n_pages ? a.exp[static_cast<size_t>(page) * a.H_kv + g] : kNone;
+      };
+      const float4 *unit = reinterpret_cast<const float4 *>(s_unit + h * (RN / 2));
+      const int page0 = page_of(0);
+      int page_next = page_of(1), e_next = exp_of(page0);
       for (int tile = 0; ok && tile < tiles; ++tile, d_phase ^= 1u) {
-        const float e = e_next;
-        e_next = exp_of(tile + 1);
+        const int e = e_next;
+        e_next = exp_of(page_next);
+        page_next = page_of(tile + 2);
+        if (!(ok = warp_wait(&d_full[h], d_phase, abort, a.wait_clocks))) break;
+        tc_fence_after();
         float b0 = -INFINITY, b1 = -INFINITY;
-        for (int h = 0; h < 2; ++h) {
-          if (!(ok = warp_wait(&d_full[h], d_phase, abort, a.wait_ns))) break;
-          tc_fence_after();
-          const int c0 = h * (rn / 2) + part * (rn / 4);
-          const float4 *unit = reinterpret_cast<const float4 *>(s_unit + c0);
-          for (int c = 0; c < rn / 4; c += 16) {
-            uint32_t s[16];
-            tmem_ld16(t_lane + c0 + c, s);
-            tmem_wait_ld();
+        for (int c = 0; c < RN / 2; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(t_lane + h * (RN / 2) + c, s);
+          tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) {
-              const float4 u = unit[(c + x) / 4];
-              const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
-              const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
-              b0 = fmax3(b0, y.x, y.y);
-              b1 = fmax3(b1, z.x, z.y);
-            }
+          for (int x = 0; x < 32; x += 4) {
+            const float4 u = unit[(c + x) / 4];
+            const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
+            const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
+            b0 = fmax3(b0, y.x, y.y);
+            b1 = fmax3(b1, z.x, z.y);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&d_empty[h]);
         }
-        if (ok && e > 0.f) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * e));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[h]);
+        if (e != kNone) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * two_to(e)));
       }
     } else if (warp == kManyEpi + kManyConv) {
       // ---- MMA issuer
+      // (operands that the compiler can tell to be the same for the whole warp, see tc_ptx.cuh: with the
+      // rows a variable a tile's 32 instructions took 3,600 clocks to issue, whatever their N)
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      const uint32_t half = static_cast<uint32_t>(RN) / 2, tm = __shfl_sync(kFull, tmem, 0);
-      const uint32_t id = idesc_f16_f32(kTilePages, static_cast<int>(half));
+      constexpr uint32_t id = idesc_f16_f32(kTilePages, RN / 2);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       const uint64_t db = sdesc_sw128(smem_u32(sm), 16, 1024);
+#pragma unroll 1
       for (int tile = 0; ok && tile < tiles; ++tile, buf.step(), d_phase ^= 1u) {
-        if (!(ok = warp_wait(&a_full[buf.slot], buf.phase, abort, a.wait_ns))) break;
+        const int slot = __shfl_sync(kFull, buf.slot, 0);
+        if (!(ok = warp_wait(&a_full[slot], buf.phase, abort, a.wait_clocks))) break;
+        const uint32_t at = tm + RN + slot * A;
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!(ok = warp_wait(&d_empty[h], d_phase ^ 1u, abort, a.wait_ns))) break;
+          if (!ok || !(ok = warp_wait(&d_empty[h], d_phase ^ 1u, abort, a.wait_clocks))) break;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < 4 * KB; ++s)    // 16 elements of K: 8 columns of A, 32 bytes of B's rows
-            mma_ts(leader, tm + h * half, tm + RN + buf.slot * A + 8 * s,
-                   db + static_cast<uint64_t>(((s >> 2) * RN + h * half) * 8 + 2 * (s & 3)), id, s > 0);
+            mma_ts(leader, tm + h * (RN / 2), at + 8 * s, db + ((s >> 2) * RN + h * (RN / 2)) * 8 + 2 * (s & 3), id,
+                   s > 0 ? 1u : 0u);
           commit_if(leader, &d_full[h]);
         }
-        if (ok) commit_if(leader, &a_empty[buf.slot]);
+        if (ok) commit_if(leader, &a_empty[slot]);
       }
     } else {
       // ---- converters: 16-byte pieces of the digests into a raw tile (PP threads a row), then a thread
@@ -943,23 +953,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
           cp_async_16_or_0(raw + r * 2 * D + ((piece ^ (r & (PP - 1))) << 4),
                            a.bounds + (static_cast<size_t>(good ? ids[i] : 0) * a.H_kv + g) * 2 * D + piece * 16, good);
         }
-        cp_async_commit();
       };
-      if (tiles > 0) {
-        ids_of(0);
-        fetch(0);
-        ids_of(1);
+      // two tiles in flight, the third's pages known (a group of copies is closed for every tile, so
+      // that they can be counted)
+      for (int tile = 0; tile < 2; ++tile) {
+        ids_of(tile);
+        if (tile < tiles) fetch(tile);
+        cp_async_commit();
       }
+      ids_of(2);
       for (int tile = 0; tile < tiles; ++tile, buf.step()) {
-        if (tile + 1 < tiles) {
-          fetch(tile + 1);
-          ids_of(tile + 2);
-          cp_async_wait<1>();
-        } else {
-          cp_async_wait<0>();
-        }
+        cp_async_wait<1>();
         named_bar_sync(1, kManyConv * 32);    // the tile is there for all (every converter comes here, ok or not)
-        if (ok) ok = warp_wait(&a_empty[buf.slot], buf.phase ^ 1u, abort, a.wait_ns);
+        if (ok) ok = warp_wait(&a_empty[buf.slot], buf.phase ^ 1u, abort, a.wait_clocks);
         if (ok) {
           tc_fence_after();
           const unsigned char *raw = sm + L.oRaw + (tile & 1) * kTilePages * 2 * D + row * 2 * D;
@@ -986,7 +992,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
           if (lane == 0) mbar_arrive(&a_full[buf.slot]);
         }
         named_bar_sync(1, kManyConv * 32);    // the raw tile is read
+        if (tile + 2 < tiles) fetch(tile + 2);
+        cp_async_commit();
+        ids_of(tile + 3);
       }
+      cp_async_wait<0>();
     }
     ok = __syncthreads_and(ok);               // (also: every score of these rows is in)
     if (!ok) break;
@@ -1034,23 +1044,31 @@ template <int D>
 cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   const int items = a.n_blocks * a.H_kv, rows = a.cfg.q_block * (a.H_q / a.H_kv);
   const bool few = rows <= kFewRows;
-  // CTAs of an item: until the launch has one per SM, or a CTA a tile (16 pages a warp)
-  const int least = kTilePages;
+  // CTAs of an item, while the launch does not fill the GPU with them.  Few rows: 16 tokens of 8 heads
+  // over 512 pages take 11.0 us with one, 12.3 with two, 19.9 with four; over 2,048 pages 28.4, 24.8,
+  // 34.9; a token over 16,384 42.7, 27.4 and 24.3 us with 4, 8 and 16.  Many rows: a block of 64
+  // tokens of 8 heads over 2,048 pages 24.6, 21.9 and 42.4 us with 4, 8 and 16 (16 CTAs of a whole SM
+  // find no room in a cluster's SMs at once).
+  const int most = few ? 16 : 8;
   int C = 1;
-  while (C < 16 && items * C < 152 && a.max_pages > C * least) C *= 2;
+  while (C < most && a.max_pages > C * kTilePages && items * C * (a.max_pages > C * 1024 && few ? 1 : 2) <= 152) C *= 2;
   a.slice = (a.max_pages + C - 1) / C;
   while (C < 16 && a.slice > kSelectMaxPages / 16) {
     C *= 2;
     a.slice = (a.max_pages + C - 1) / C;
   }
   const size_t keys = static_cast<size_t>(a.slice) * 4;
+  // (16 rows by tcgen05 instead: 2,048 tokens in blocks of 4 over 2,048 pages 1,053 us in place of 447)
   if (rows <= 8) return launch_cluster(select_few_kernel<D, 1>, items, C, kFewThreads, keys, s, a);
   if (few) return launch_cluster(select_few_kernel<D, 2>, items, C, kFewThreads, keys, s, a);
   // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
-  a.rows = std::min((rows + 63) & ~63, 256);
-  if (many_layout(D, a.rows).oKey + keys > kManyBytes) a.rows = 128;
-  a.wait_ns = g_wait_limit_ns;
-  return launch_cluster(select_many_kernel<D>, items, C, kManyThreads, many_layout(D, a.rows).oKey + keys, s, a);
+  // about two clocks a nanosecond; at most 2^31 of them, a second
+  a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
+  const size_t smem = many_layout(D, rows <= 64 ? 64 : 128).oKey + keys, smem256 = many_layout(D, 256).oKey + keys;
+  if (rows <= 64) return launch_cluster(select_many_kernel<D, 64>, items, C, kManyThreads, smem, s, a);
+  if (rows <= 128 || smem256 > kManyBytes)
+    return launch_cluster(select_many_kernel<D, 128>, items, C, kManyThreads, smem, s, a);
+  return launch_cluster(select_many_kernel<D, 256>, items, C, kManyThreads, smem256, s, a);
 }
 
 }  // namespace

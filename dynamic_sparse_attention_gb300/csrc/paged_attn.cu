@@ -382,17 +382,6 @@ __device__ __forceinline__ uint32_t clock_lo() {
   return t;
 }
 
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // The whole warp waits; the outcome is warp-uniform.  Every lane asks, without a time hint: the
 // hardware then holds the warp until the phase completes (or a limit of its own passes).  One
 // lane polling, or hints, cost the other roles issue slots and woke late: 128K chunk 3.57 ->

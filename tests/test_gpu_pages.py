@@ -641,3 +641,26 @@ def test_repeats_bit_by_bit_and_on_another_stream():
         runs.append((sel.page_table, o, z))
     for r in runs[1:]:
         assert all(torch.equal(x, y) for x, y in zip(r, runs[0]))
+
+
+def test_waits_that_run_out():
+    """With a limit of a nanosecond the selection of many rows gives up: the error bit is set, every entry is
+    a page of its sequence or -1, and the next call is whole."""
+    b = Batch([(100, 8000), (70, 5000)], 8, 2, 128, 16, False, seed=6).fill().digest_all()
+    q = b.rows(b.N, 8)
+    call = lambda: dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=30, q_block=64, want_index=True)
+    torch.cuda.synchronize()
+    assert dsa.device_error() == 0
+    dsa.set_wait_limit(1)
+    try:
+        sel = call()
+        torch.cuda.synchronize()
+    finally:
+        dsa.set_wait_limit(0)
+    assert dsa.device_error() == 16
+    owner = torch.tensor([0, 0, 1, 1], device="cuda")
+    for j, s in enumerate(owner.tolist()):
+        i = sel.index[j]
+        assert ((i >= -1) & (i < -(-b.seqs[s][1] // 16))).all()
+        assert (sel.page_table[j] == torch.where(i < 0, -1, b.table[s][i.clamp(min=0).long()])).all()
+    check_select(b, q, 30, 1, 1, 64, call())
