@@ -700,13 +700,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
 }
 
 // Many rows (a chunk's blocks): the products on tcgen05, the integers as fp16.  Pages lie on the
-// TMEM lanes (M = 128) and the block's rows on its columns (N = up to 256, in two halves), so a thread
-// owns a page and takes the largest score of its row of columns without talking to another.  The
+// TMEM lanes (M = 128) and the block's rows on its columns (N = 64 or 128; 256 rows as two products),
+// so a thread owns a page and takes the largest score of its columns without talking to another.  The
 // rows' integers stay in shared memory, those below zero against lo and those above against hi (K =
 // 2 D).  Digests come in tiles of 128 pages by cp.async and go, widened to fp16, to TMEM as the A
-// operand: with A in shared memory as well, reading both and writing A took its whole bandwidth (96 + 32
-// of 128 bytes a clock; a tile 4,000 clocks where the products need 2,048).  While one half's scores
-// are read, the other half is computed.
+// operand.  While one product's scores are read, the next is computed.  The same with mma.sync took 355 us
+// for 2,048 tokens in blocks of 64 over 2,048 pages of 8 heads.
 constexpr int kManyEpi = 8, kManyConv = 8;                       // warps: epilogue, converters, MMA issuer
 constexpr int kManyThreads = (kManyEpi + kManyConv + 1) * 32;
 constexpr int kTilePages = 128;
@@ -747,6 +746,7 @@ template <int D, int RN>                      // RN: rows held at a time, 64, 12
 __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const PageSelectArgs a) {
   constexpr int KB = 2 * D / 64;              // 64-element blocks of K
   constexpr int A = D;                        // TMEM columns of a tile's digests (2 D fp16)
+  constexpr int NH = RN > 128 ? 2 : 1, N = RN / NH;   // products per tile, rows of one: a tile's scores, or halves
   constexpr int PP = 2 * D / 16;              // 16-byte pieces of a digest row
   extern __shared__ __align__(1024) unsigned char sm[];
   constexpr ManyLayout L = many_layout(D, RN);
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   const int R = k.n * (a.H_q / a.H_kv);
   const int32_t *table = a.page_table + static_cast<size_t>(k.b) * a.max_pages + p_first;
   const int tiles = (nl + kTilePages - 1) / kTilePages;
-  constexpr uint32_t cols = RN + 2 * A <= 256 ? 256u : 512u;          // TMEM: scores of RN rows, two tiles
+  constexpr uint32_t cols = 2 * N + 2 * A <= 256 ? 256u : 512u;   // TMEM: scores of two products, two tiles
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&a_full[s], kManyConv);
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   }
   // what a role carries over from one set of rows to the next
   Ring<2> buf;                                // the digests' buffer
-  uint32_t d_phase = 0;
+  uint32_t unit = 0;                          // products so far: they take the scores' buffers in turn
   bool ok = true;
 
   for (int r0 = 0; r0 < R; r0 += RN) {
@@ -864,11 +864,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);   // this warp's TMEM lanes
 
     if (warp < kManyEpi) {
-      // ---- epilogue: page (lane) x columns; four warps read one half's scores while the others read the
+      // ---- epilogue: page (lane) x columns; four warps read one buffer's scores while the others read the
       // other's
-      const int h = warp >> 2, row = (warp & 3) * 32 + lane;
+      const uint32_t mine = warp >> 2;
+      const int row = (warp & 3) * 32 + lane;
       // this thread's page two tiles ahead and its exponent one ahead (looked at when used, so that
-      // neither load is waited for: 1.9 us a tile otherwise)
+      // neither load is waited for)
       auto page_of = [&](int tile) -> int {
         const int i = tile * kTilePages + row, page = i < nl ? table[i] : -1;
         DSA_CHECK(i >= nl || (page >= 0 && page < a.n_pages));
@@ -878,56 +879,60 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
       auto exp_of = [&](int page) -> int {
         return page >= 0 && page < a.n_pages ? a.exp[static_cast<size_t>(page) * a.H_kv + g] : kNone;
       };
-      const float4 *unit = reinterpret_cast<const float4 *>(s_unit + h * (RN / 2));
       const int page0 = page_of(0);
       int page_next = page_of(1), e_next = exp_of(page0);
-      for (int tile = 0; ok && tile < tiles; ++tile, d_phase ^= 1u) {
+      for (int tile = 0; ok && tile < tiles; ++tile) {
         const int e = e_next;
         e_next = exp_of(page_next);
         page_next = page_of(tile + 2);
-        if (!(ok = warp_wait(&d_full[h], d_phase, abort, a.wait_clocks))) break;
-        tc_fence_after();
-        float b0 = -INFINITY, b1 = -INFINITY;
-        for (int c = 0; c < RN / 2; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(t_lane + h * (RN / 2) + c, s);
-          tmem_wait_ld();
+#pragma unroll 1
+        for (int h = 0; h < NH; ++h, ++unit) {
+          if ((unit & 1u) != mine) continue;
+          if (!(ok = warp_wait(&d_full[mine], (unit >> 1) & 1u, abort, a.wait_clocks))) break;
+          tc_fence_after();
+          const float4 *u4 = reinterpret_cast<const float4 *>(s_unit + h * N);
+          float b0 = -INFINITY, b1 = -INFINITY;
+          for (int c = 0; c < N; c += 32) {
+            uint32_t s[32];
+            tmem_ld32(t_lane + mine * N + c, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 u = unit[(c + x) / 4];
-            const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
-            const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
-            b0 = fmax3(b0, y.x, y.y);
-            b1 = fmax3(b1, z.x, z.y);
+            for (int x = 0; x < 32; x += 4) {
+              const float4 u = u4[(c + x) / 4];
+              const float2 y = fmul2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(u.x, u.y));
+              const float2 z = fmul2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(u.z, u.w));
+              b0 = fmax3(b0, y.x, y.y);
+              b1 = fmax3(b1, z.x, z.y);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_empty[mine]);
+          if (e != kNone) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * two_to(e)));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[h]);
-        if (e != kNone) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * two_to(e)));
       }
     } else if (warp == kManyEpi + kManyConv) {
       // ---- MMA issuer
-      // (operands that the compiler can tell to be the same for the whole warp, see tc_ptx.cuh: with the
-      // rows a variable a tile's 32 instructions took 3,600 clocks to issue, whatever their N)
+      // (an instruction takes 71 clocks to issue whatever its N, so a product has as many rows as may be;
+      // the operands are what the compiler can tell to be the same for the whole warp, see tc_ptx.cuh)
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      constexpr uint32_t id = idesc_f16_f32(kTilePages, RN / 2);
+      constexpr uint32_t id = idesc_f16_f32(kTilePages, N);
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       const uint64_t db = sdesc_sw128(smem_u32(sm), 16, 1024);
 #pragma unroll 1
-      for (int tile = 0; ok && tile < tiles; ++tile, buf.step(), d_phase ^= 1u) {
+      for (int tile = 0; ok && tile < tiles; ++tile, buf.step()) {
         const int slot = __shfl_sync(kFull, buf.slot, 0);
         if (!(ok = warp_wait(&a_full[slot], buf.phase, abort, a.wait_clocks))) break;
-        const uint32_t at = tm + RN + slot * A;
+        const uint32_t at = tm + 2 * N + slot * A;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || !(ok = warp_wait(&d_empty[h], d_phase ^ 1u, abort, a.wait_clocks))) break;
+        for (int h = 0; h < NH; ++h, ++unit) {
+          const uint32_t to = __shfl_sync(kFull, unit & 1u, 0);
+          if (!ok || !(ok = warp_wait(&d_empty[to], ((unit >> 1) & 1u) ^ 1u, abort, a.wait_clocks))) break;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < 4 * KB; ++s)    // 16 elements of K: 8 columns of A, 32 bytes of B's rows
-            mma_ts(leader, tm + h * (RN / 2), at + 8 * s, db + ((s >> 2) * RN + h * (RN / 2)) * 8 + 2 * (s & 3), id,
-                   s > 0 ? 1u : 0u);
-          commit_if(leader, &d_full[h]);
+            mma_ts(leader, tm + to * N, at + 8 * s, db + ((s >> 2) * RN + h * N) * 8 + 2 * (s & 3), id, s > 0 ? 1u : 0u);
+          commit_if(leader, &d_full[to]);
         }
         if (ok) commit_if(leader, &a_empty[slot]);
       }
@@ -935,11 +940,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
       // ---- converters: 16-byte pieces of the digests into a raw tile (PP threads a row), then a thread
       // per page and half of its row widens them
       const int ct = tid - kManyEpi * 32, piece = ct % PP, half = ct >> 7, row = ct & 127;
-      constexpr int RPP = kManyConv * 32 / PP, N = kTilePages / RPP;   // rows per pass, passes
-      int ids[N];
+      constexpr int RPP = kManyConv * 32 / PP, NP = kTilePages / RPP;   // rows per pass, passes
+      int ids[NP];
       auto ids_of = [&](int tile) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < NP; ++i) {
           const int x = tile * kTilePages + ct / PP + i * RPP;
           ids[i] = x < nl ? table[x] : -1;
         }
@@ -947,7 +952,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
       auto fetch = [&](int tile) {            // the tile of `ids`
         unsigned char *raw = sm + L.oRaw + (tile & 1) * kTilePages * 2 * D;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < NP; ++i) {
           const int r = ct / PP + i * RPP;
           const bool good = ids[i] >= 0 && ids[i] < a.n_pages;
           cp_async_16_or_0(raw + r * 2 * D + ((piece ^ (r & (PP - 1))) << 4),
@@ -984,7 +989,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
                 h[8 * q + 2 * x + 1] = y.y;
               }
             }
-            tmem_st16(t_lane + RN + buf.slot * A + half * (A / 2) + 8 * p, h);
+            tmem_st16(t_lane + 2 * N + buf.slot * A + half * (A / 2) + 8 * p, h);
           }
           tmem_wait_st();
           tc_fence_before();
