@@ -8,7 +8,9 @@
 // to store and rounded once: to bf16, or for an FP8 cache by the rule of kv_cache.cu applied to
 // the fp32 values (values are bf16 already, so they come out as kv_cache_write stores them).
 //
-// Bound by HBM: every row is read once and written once.
+// Bound by HBM: every row is read once and written once.  Measured (of 6,791 GB/s): 34,700 tokens of 32
+// query and 8 key heads of 128, bf16 (1,193 MB), 196 us, 6,090 GB/s (90 %); a decode step's 16 tokens 4.9
+// us, a launch's latencies.
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
@@ -126,8 +128,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv_rope_kernel(const RopeWriteArg
         u1 = __ldcs(reinterpret_cast<const uint4 *>(src) + p1);
       }
     };
-    // two groups at a time, the next two requested meanwhile (the angles wait in shared memory: their 16
-    // registers are what lets a third CTA run)
+    // two groups at a time, the next two requested meanwhile (34,700 tokens: 244 us without and with
+    // one ahead, 196 so); the angles wait in shared memory, whose 16 registers let a third CTA run
     const int step = a.wpt * RPW, first = (warp % a.wpt) * RPW;
     uint4 u0, u1, v0, v1;
     fetch(first, u0, u1);

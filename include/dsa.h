@@ -578,7 +578,8 @@ int page_select_sizes(const dsa_paged_shape *shape, const dsa_page_select_cfg *c
  *   sel_q_start [n_blocks + 1], sel_kv_len [n_blocks], sel_table [n_blocks, H_kv, max_list]: the
  *          blocks as sequences of their own for paged_attn_lists: their rows, the keys of their
  *          lists up to the last token's, and the lists as page ids (-1 behind their end).  Blocks
- *          behind the last one hold no rows and no keys
+ *          behind the last one hold no rows and no keys (and as all pages tie without a row, those
+ *          of the last sequence's `keep` earliest that are not sinks or local; nothing attends them)
  *   sel_index [n_blocks, H_kv, max_list]  the lists as places in the sequence's table (NULL to
  *          skip), -1 behind their end
  * A page outside [0, n_pages) scores lowest.  q_block in [1, 256], max_pages <= 262144, n_blocks <=

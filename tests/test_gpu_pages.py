@@ -354,9 +354,15 @@ def check_select(b, q, keep, n_sink, n_local, q_block, sel, rows0=0, some=None):
                 assert np.array_equal(table[j, h], np.where(want < 0, -1, b.table_np[s, want])), (s, i, h)
             j += 1
         at += n
-    assert (start[j:] == at).all() and (lens[j:] == 0).all() and (table[j:] == -1).all()
+    # blocks behind the last one: no rows, no keys; all pages tie, so the earliest are picked
+    assert (start[j:] == at).all() and (lens[j:] == 0).all()
+    first = max(0, max(b.seqs[-1][1], 0) // b.page - n_local)
+    s0 = min(n_sink, first)
+    want = np.full(table.shape[2], -1)
+    want[:max(0, min(keep, first) - s0)] = np.arange(s0, max(s0, min(keep, first)))
+    assert (table[j:] == np.where(want < 0, -1, b.table_np[-1, want])).all()
     if index is not None:
-        assert (index[j:] == -1).all()
+        assert (index[j:] == want).all()
 
 
 SELECT = [
