@@ -1184,9 +1184,6 @@ def page_select(q, digest: PageDigest, q_start, kv_len, page_table, *, keep: int
     if out is None:
         def new(*size):
             return torch.empty(size, dtype=torch.int32, device=q.device)
-        if n_tok == 0:                                  # (nothing is launched)
-            return PageSelection(torch.zeros(1, dtype=torch.int32, device=q.device), new(0), new(*dims),
-                                 new(*dims) if want_index else None)
         out = PageSelection(new(n_blocks + 1), new(n_blocks), new(*dims), new(*dims) if want_index else None)
     else:
         for name, t, size in (("q_start", out.q_start, (n_blocks + 1,)), ("kv_len", out.kv_len, (n_blocks,)),
@@ -1195,6 +1192,13 @@ def page_select(q, digest: PageDigest, q_start, kv_len, page_table, *, keep: int
                 continue
             if _index(t, "out." + name, len(size), dev) and tuple(t.shape) != size:
                 raise ValueError(f"out.{name} must be {list(size)}")
+    if n_tok == 0:                                      # nothing is launched: blocks without rows
+        out.q_start.zero_()
+        out.kv_len.zero_()
+        out.page_table.fill_(-1)
+        if out.index is not None:
+            out.index.fill_(-1)
+        return out
     status = lib.page_select(q.data_ptr(), q_stride, bounds, exp, start, lens, table, shape, cfg,
                              out.q_start.data_ptr(), out.kv_len.data_ptr(), out.page_table.data_ptr(),
                              None if out.index is None else out.index.data_ptr(), st)

@@ -670,3 +670,16 @@ def test_waits_that_run_out():
         assert ((i >= -1) & (i < -(-b.seqs[s][1] // 16))).all()
         assert (sel.page_table[j] == torch.where(i < 0, -1, b.table[s][i.clamp(min=0).long()])).all()
     check_select(b, q, 30, 1, 1, 64, call())
+
+
+def test_no_tokens():
+    """A call without rows: blocks without rows, which attend nothing."""
+    b = Batch([(1, 100), (1, 40)], 4, 2, 64, 16, False).fill().digest_all()
+    q, zero = b.rows(1, 4)[:0], ints([0, 0, 0])
+    sel = dsa.page_select(q, b.digest, zero, b.kv_len, b.table, keep=3, q_block=16, want_index=True)
+    assert not sel.q_start.any() and not sel.kv_len.any() and (sel.page_table == -1).all() and (sel.index == -1).all()
+    out, lse = dsa.paged_attn(q, b.cache, sel.q_start, sel.kv_len, sel.page_table)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    dsa.page_digest_update(b.cache, b.digest, 0, zero, b.kv_len, b.table)
+    dsa.kv_cache_write_rope(b.cache, q, q[:, :2], q[:, :2], zero, b.kv_len, b.table, None)
+    dsa.kv_pages_copy(b.cache, zero[:0], zero[:0], digest=b.digest)
