@@ -62,6 +62,12 @@ __device__ __forceinline__ int exponent127(uint32_t u) {
   return min(max(e, -50), 50);
 }
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// A digest's exponent as the caller's array has it: outside the digests' range it is no power of two
+// that keeps a score finite, and counts as the nearest one inside.
+__device__ __forceinline__ float two_to_stored(int e) {
+  DSA_CHECK(e >= -50 && e <= 50);
+  return two_to(min(max(e, -50), 50));
+}
 
 // The 8 keys' channels of lane's 16-byte piece (bf16) or 8-byte piece (E4M3 with the row's scale
 // byte, as the bf16 values that they stand for).
@@ -503,7 +509,7 @@ __device__ void pick(const PageSelectArgs &a, cg::cluster_group &cluster, Select
     left -= __shfl_sync(kFull, run, who);
     lo += __shfl_sync(kFull, bin, who) << shift;
     in = __shfl_sync(kFull, in, who);
-    hi = min(hi, lo + ((1u << shift) - 1u));
+    hi = lo + min(hi - lo, (1u << shift) - 1u);   // (the bin's end may lie past 2^32)
     if (shift == 0 || in == left) break;      // (the same for every warp of the cluster)
   }
   // keys above `hi` are in, and the first `left` of those from `lo` on
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const PageSe
       sb = fmaxf(sb, __shfl_xor_sync(kFull, sb, o));
     }
     const int i = task * 16 + gr + 8 * t;
-    if (t < 2 && i < nl) s_key[i] = e != kNone ? ordered_key((t ? sb : sa) * two_to(e)) : 0u;   // no page: below every score
+    if (t < 2 && i < nl) s_key[i] = e != kNone ? ordered_key((t ? sb : sa) * two_to_stored(e)) : 0u;   // no page: below every score
   }
   if (rank == 0 && warp == kFewThreads / 32 - 1) put_fixed(a, j, g, k);
   __syncthreads();
@@ -938,7 +944,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&d_empty[mine]);
-          if (e != kNone) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * two_to(e)));
+          if (e != kNone) atomicMax(&s_key[tile * kTilePages + row], ordered_key(fmaxf(b0, b1) * two_to_stored(e)));
         }
       }
     } else if (warp == kManyEpi + kManyConv) {

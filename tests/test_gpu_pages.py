@@ -417,6 +417,34 @@ def test_select_ties_and_odd_numbers(q_block):
         check_select(b, q, keep, 1, 0, q_block, sel)
 
 
+@pytest.mark.parametrize("q_block", [1, 4, 32])
+def test_select_with_exponents_out_of_range(q_block):
+    """Whatever 8 bits a digest holds (arrays that nothing has written yet), every list has its length
+    and nothing is written beside the lists; exponents count as the nearest in [-50, 50]."""
+    b = Batch([(40, 3000), (7, 90)], 8, 2, 128, 16, False, seed=q_block)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q, wide = b.rows(b.N, 8) * 2.0 ** 60, 3
+    dims = ((b.N + 2 * (q_block - 1)) // q_block, 2)
+    for keep in (1, 20, 100):
+        b.digest.bounds.random_(-128, 128, generator=g)
+        b.digest.exp.random_(-128, 128, generator=g)
+        b.digest.exp[::3] = -128
+        b.digest.exp[1::3] = 127
+        most = 1 + keep + 1 + (q_block + 14) // 16 + 1
+        held = torch.full((dims[0] + 2 * wide, 2, most), 77, dtype=torch.int32, device="cuda")
+        index = held.clone()
+        out = dsa.PageSelection(torch.empty(dims[0] + 1, dtype=torch.int32, device="cuda"),
+                                torch.empty(dims[0], dtype=torch.int32, device="cuda"), held[wide:-wide], index[wide:-wide])
+        sel = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=keep, q_block=q_block, out=out)
+        torch.cuda.synchronize()
+        for x in (held, index):
+            assert (x[:wide] == 77).all() and (x[-wide:] == 77).all()
+        raw = b.digest.exp.clone()
+        b.digest.exp.clamp_(-50, 50)
+        check_select(b, q, keep, 1, 1, q_block, sel)
+        b.digest.exp.copy_(raw)
+
+
 def test_select_of_short_sequences_and_loose_rows():
     """Chunks longer than their sequence (rows at negative positions), rows of no chunk, a sequence
     without keys; a table much wider than the sequences."""
