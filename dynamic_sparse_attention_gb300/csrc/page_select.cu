@@ -1058,13 +1058,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) select_many_kernel(const Page
   pick<kManyThreads>(a, cluster, sh, s_key, nl, p_first, j, g, k);
 }
 
-constexpr size_t kManyBytes = 227 * 1024;   // dynamic shared memory, at most
+// dynamic shared memory of a launch, at most
+constexpr size_t kFewBytes = kSelectMaxPages / 16 * 4, kManyBytes = 227 * 1024;
 static_assert(many_layout(128, 128).oKey + kSelectMaxPages / 16 * 4 <= kManyBytes, "widest table");
 
-template <typename Kern>
-cudaError_t launch_cluster(Kern kern, int items, int C, int threads, size_t smem, cudaStream_t s, const PageSelectArgs &a) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+// What a launch needs of the current device: the kernel's shared memory and clusters allowed there.  Set
+// once per device, and to the most that any call asks for: the limit belongs to the kernel, not to the call,
+// and one that each call set to its own size refused the wider call of another host thread.
+template <auto kKernel>
+cudaError_t prepare(size_t most, bool again = false) {
+  static std::atomic<bool> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && !again && known[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && keep) known[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <auto kKernel>
+cudaError_t launch_cluster(int items, int C, int threads, size_t smem, size_t most, cudaStream_t s,
+                           const PageSelectArgs &a) {
+  cudaError_t e = prepare<kKernel>(most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items) * C);
@@ -1079,8 +1097,15 @@ cudaError_t launch_cluster(Kern kern, int items, int C, int threads, size_t smem
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  ProfScope ps("page_select", s);
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  for (int turn = 0; turn < 2; ++turn) {
+    ProfScope ps("page_select", s);
+    e = cudaLaunchKernelEx(&cfg, kKernel, a);
+    if ((e != cudaErrorInvalidValue && e != cudaErrorInvalidClusterSize) || turn) break;
+    // a context that was torn down and made again has forgotten what was allowed
+    cudaGetLastError();
+    if ((e = prepare<kKernel>(most, true)) != cudaSuccess) break;
+  }
+  return e;
 }
 
 template <int D>
@@ -1102,16 +1127,16 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   }
   const size_t keys = static_cast<size_t>(a.slice) * 4;
   // (16 rows by tcgen05 instead: 2,048 tokens in blocks of 4 over 2,048 pages 1,053 us in place of 447)
-  if (rows <= 8) return launch_cluster(select_few_kernel<D, 1>, items, C, kFewThreads, keys, s, a);
-  if (few) return launch_cluster(select_few_kernel<D, 2>, items, C, kFewThreads, keys, s, a);
+  if (rows <= 8) return launch_cluster<select_few_kernel<D, 1>>(items, C, kFewThreads, keys, kFewBytes, s, a);
+  if (few) return launch_cluster<select_few_kernel<D, 2>>(items, C, kFewThreads, keys, kFewBytes, s, a);
   // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
   // about two clocks a nanosecond; at most 2^31 of them, a second
   a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
   const size_t smem = many_layout(D, rows <= 64 ? 64 : 128).oKey + keys, smem256 = many_layout(D, 256).oKey + keys;
-  if (rows <= 64) return launch_cluster(select_many_kernel<D, 64>, items, C, kManyThreads, smem, s, a);
+  if (rows <= 64) return launch_cluster<select_many_kernel<D, 64>>(items, C, kManyThreads, smem, kManyBytes, s, a);
   if (rows <= 128 || smem256 > kManyBytes)
-    return launch_cluster(select_many_kernel<D, 128>, items, C, kManyThreads, smem, s, a);
-  return launch_cluster(select_many_kernel<D, 256>, items, C, kManyThreads, smem256, s, a);
+    return launch_cluster<select_many_kernel<D, 128>>(items, C, kManyThreads, smem, kManyBytes, s, a);
+  return launch_cluster<select_many_kernel<D, 256>>(items, C, kManyThreads, smem256, kManyBytes, s, a);
 }
 
 }  // namespace

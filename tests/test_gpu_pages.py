@@ -677,6 +677,46 @@ def test_repeats_bit_by_bit_and_on_another_stream():
         assert all(torch.equal(x, y) for x, y in zip(r, runs[0]))
 
 
+@pytest.mark.parametrize("q_block", [1, 32])
+def test_calls_from_threads(q_block):
+    """Host threads, each on a stream of its own, over tables of very different width: every call is
+    taken and gets the lists that it gets alone.  (The C entry itself: what Python does between two calls
+    keeps the threads apart.)"""
+    import ctypes
+    import threading
+    lib, jobs, n = dsa.load(), [], 20 if q_block == 1 else 70
+    for width in (24, 32768, 24, 32768):
+        b = Batch([(n, 350), (n, 300)], 8, 2, 128, 16, False, seed=width, max_pages=width).fill().digest_all()
+        q = b.rows(b.N, 8)
+        want = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=6, q_block=q_block)
+        got, stream = [torch.zeros_like(t) for t in (want.q_start, want.kv_len, want.page_table)], torch.cuda.Stream()
+        shape = dsa.binding.PagedShape(2, b.N, width, b.n_pages, 16, 8, 2, 128, dsa.binding.BF16)
+        cfg = dsa.binding.PageSelectCfg(6, 1, 1, q_block)
+        args = (q.data_ptr(), 8 * 128, b.digest.bounds.data_ptr(), b.digest.exp.data_ptr(), b.q_start.data_ptr(),
+                b.kv_len.data_ptr(), b.table.data_ptr(), ctypes.byref(shape), ctypes.byref(cfg),
+                *(t.data_ptr() for t in got), None, stream.cuda_stream)
+        jobs.append((b, q, want, got, stream, args, shape, cfg))
+    torch.cuda.synchronize()
+    refused, go = [0] * len(jobs), threading.Barrier(len(jobs))
+
+    def work(i):
+        stream, args = jobs[i][4], jobs[i][5]
+        go.wait(timeout=60)
+        for k in range(3000):
+            refused[i] += lib.page_select(*args) != 0
+            if k % 250 == 249:                              # (not too far ahead of the GPU)
+                stream.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=300)
+    torch.cuda.synchronize()
+    assert not any(t.is_alive() for t in threads) and refused == [0] * len(jobs), refused
+    for _, _, want, got, *_ in jobs:
+        assert all(torch.equal(x, y) for x, y in zip(got, (want.q_start, want.kv_len, want.page_table)))
+
+
 def test_waits_that_run_out():
     """With a limit of a nanosecond the selection of many rows gives up: the error bit is set, every entry is
     a page of its sequence or -1, and the next call is whole."""
