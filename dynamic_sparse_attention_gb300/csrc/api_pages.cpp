@@ -1,5 +1,6 @@
 // C-ABI entry points around the paged cache's sparse path: kv_cache_write_rope,
 // page_digest_update, page_select, kv_pages_copy.  Host-side validation and launches.
+#include <algorithm>
 #include <cmath>
 
 #include "api_paged.h"
@@ -62,7 +63,9 @@ int select_sizes(const dsa_paged_shape *s, const dsa_page_select_cfg *c, int *n_
     return fail(DSA_ERR_UNSUPPORTED, "q_block=%d outside [1, %d]", c->q_block, kMaxQueryBlock);
   if (s->max_pages > kSelectMaxPages)
     return fail(DSA_ERR_UNSUPPORTED, "max_pages=%d > %d", s->max_pages, kSelectMaxPages);
-  const long long blocks = (s->n_tok + static_cast<long long>(s->B) * (c->q_block - 1)) / c->q_block;
+  // (a call without tokens has a block too: the attention over the lists takes one sequence at least)
+  const long long blocks =
+      std::max(1ll, (s->n_tok + static_cast<long long>(s->B) * (c->q_block - 1)) / c->q_block);
   if (blocks > kMaxBlocks)
     return fail(DSA_ERR_UNSUPPORTED, "%lld blocks of q_block=%d queries > %d", blocks, c->q_block, kMaxBlocks);
   const long long list = static_cast<long long>(c->n_sink) + c->keep + c->n_local +

@@ -556,7 +556,7 @@ typedef struct {
 } dsa_page_select_cfg;
 
 /* Blocks of queries (n_blocks = (n_tok + B (q_block - 1)) / q_block, at least as many as there
- * are) and entries of a list (max_list = n_sink + keep + n_local + the most pages that a block's
+ * are and at least one) and entries of a list (max_list = n_sink + keep + n_local + the most pages that a block's
  * own tokens lie in) of a page_select call; host only. */
 int page_select_sizes(const dsa_paged_shape *shape, const dsa_page_select_cfg *cfg, int *n_blocks,
                       int *max_list);

@@ -740,6 +740,22 @@ def test_waits_that_run_out():
     check_select(b, q, 30, 1, 1, 64, call())
 
 
+@pytest.mark.parametrize("B", [1, 3])
+@pytest.mark.parametrize("kw", [dict(), dict(q_block=1), dict(q_block=64)])
+def test_a_step_without_tokens(B, kw):
+    """The documented step of a batch that brings nothing, whatever the blocks."""
+    b = Batch([(1, 100)] * B, 4, 2, 64, 16, False).fill().digest_all()
+    q, start = b.rows(1, 4)[:0], ints([0] * (B + 1))
+    old = [t.clone() for t in (b.cache.k, b.cache.v, b.digest.bounds, b.digest.exp)]
+    qr = dsa.kv_cache_write_rope(b.cache, q, q[:, :2], q[:, :2], start, b.kv_len, b.table, None)
+    dsa.page_digest_update(b.cache, b.digest, 0, start, b.kv_len, b.table)
+    sel = dsa.page_select(qr, b.digest, start, b.kv_len, b.table, keep=3, want_index=True, **kw)
+    out, lse = dsa.paged_attn(qr, b.cache, sel.q_start, sel.kv_len, sel.page_table)
+    assert qr.shape == out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert not sel.q_start.any() and not sel.kv_len.any() and (sel.page_table == -1).all() and (sel.index == -1).all()
+    assert all(torch.equal(x, y) for x, y in zip(old, (b.cache.k, b.cache.v, b.digest.bounds, b.digest.exp)))
+
+
 def test_no_tokens():
     """A call without rows: blocks without rows, which attend nothing."""
     b = Batch([(1, 100), (1, 40)], 4, 2, 64, 16, False).fill().digest_all()

@@ -167,6 +167,17 @@ def test_select_arguments_and_sizes(lib):
         assert s0 + 4 + own1 + 1 - first <= width
 
 
+@pytest.mark.parametrize("B,q_block", [(1, 1), (3, 1), (1, 64), (3, 64), (4096, 1)])
+def test_a_call_without_tokens_has_a_block(lib, B, q_block):
+    """So that the attention over its lists, a sequence a block, is a call that is taken."""
+    n, m = ctypes.c_int(), ctypes.c_int()
+    s = _shape(n_tok=0, B=B)
+    cfg = binding.PageSelectCfg(keep=4, n_sink=1, n_local=2, q_block=q_block)
+    assert lib.page_select_sizes(ctypes.byref(s), ctypes.byref(cfg), ctypes.byref(n), ctypes.byref(m)) == 0
+    assert n.value >= 1 and m.value >= 8
+    assert _lists(lib, _shape(n_tok=0, B=n.value, max_pages=m.value), q=None) == 0
+
+
 def test_lists_arguments(lib):
     s = _shape()
     assert _lists(lib, s, table=None) == -4 and _lists(lib, s, q=None) == -4 and _lists(lib, s, scale=0.0) == -1
