@@ -1192,13 +1192,6 @@ def page_select(q, digest: PageDigest, q_start, kv_len, page_table, *, keep: int
                 continue
             if _index(t, "out." + name, len(size), dev) and tuple(t.shape) != size:
                 raise ValueError(f"out.{name} must be {list(size)}")
-    if n_tok == 0:                                      # nothing is launched: blocks without rows
-        out.q_start.zero_()
-        out.kv_len.zero_()
-        out.page_table.fill_(-1)
-        if out.index is not None:
-            out.index.fill_(-1)
-        return out
     status = lib.page_select(q.data_ptr(), q_stride, bounds, exp, start, lens, table, shape, cfg,
                              out.q_start.data_ptr(), out.kv_len.data_ptr(), out.page_table.data_ptr(),
                              None if out.index is None else out.index.data_ptr(), st)

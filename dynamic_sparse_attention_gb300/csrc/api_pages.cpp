@@ -216,9 +216,10 @@ int page_select(const void *q, long long q_stride, const int8_t *bounds, const i
   if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4))
     return fail(DSA_ERR_ALIGNMENT, "q_start, kv_len and page_table must be non-NULL and 4-byte aligned");
   if ((st = check_stride("q_stride", q_stride, shape->H_q, shape->D))) return st;
-  if (shape->n_tok == 0) return DSA_OK;
-  if (!aligned(q, 16)) return fail(DSA_ERR_ALIGNMENT, "q must be non-NULL and 16-byte aligned");
-  if (!aligned(sel_q_start, 4) || !aligned(sel_kv_len, 4) || !aligned(sel_table, 4) || (sel_index && !aligned(sel_index, 4)))
+  const bool none = shape->n_tok == 0;   // (outputs that are NULL are then skipped)
+  if (!none && !aligned(q, 16)) return fail(DSA_ERR_ALIGNMENT, "q must be non-NULL and 16-byte aligned");
+  auto bad = [](const void *p, bool may_be_null) { return p ? !aligned(p, 4) : !may_be_null; };
+  if (bad(sel_q_start, none) || bad(sel_kv_len, none) || bad(sel_table, none) || bad(sel_index, true))
     return fail(DSA_ERR_ALIGNMENT, "sel_q_start, sel_kv_len and sel_table must be non-NULL, all outputs 4-byte aligned");
   const long long lists = static_cast<long long>(a.n_blocks) * shape->H_kv * a.max_list * 4;
   const Span outs[] = {{"sel_q_start", sel_q_start, 4ll * (a.n_blocks + 1)},
@@ -232,6 +233,17 @@ int page_select(const void *q, long long q_stride, const int8_t *bounds, const i
                       {"kv_len", kv_len, 4ll * shape->B},
                       {"page_table", page_table, table_bytes(shape)}};
   if ((st = check_apart(outs, ins))) return st;
+  if (none) {
+    // blocks without rows, keys and pages
+    for (const Span &o : outs) {
+      const int byte = o.p == sel_q_start || o.p == sel_kv_len ? 0 : 0xff;
+      const cudaError_t e = !o.p ? cudaSuccess
+                                 : cudaMemsetAsync(const_cast<void *>(o.p), byte, static_cast<size_t>(o.n),
+                                                   static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e, "page selection without tokens");
+    }
+    return DSA_OK;
+  }
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
   a.bounds = bounds;

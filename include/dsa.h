@@ -582,6 +582,8 @@ int page_select_sizes(const dsa_paged_shape *shape, const dsa_page_select_cfg *c
  *          of the last sequence's `keep` earliest that are not sinks or local; nothing attends them)
  *   sel_index [n_blocks, H_kv, max_list]  the lists as places in the sequence's table (NULL to
  *          skip), -1 behind their end
+ * A call without tokens (n_tok = 0) lists nothing: q_start and kv_len 0, -1 throughout; outputs that are
+ * NULL are then skipped.
  * A page outside [0, n_pages) scores lowest; an exponent outside [-50, 50] counts as the nearest of the
  * two.  q_block in [1, 256], max_pages <= 262144, n_blocks <=
  * 4096, else UNSUPPORTED.  shape->dtype is not used but checked.  Where a CTA's bounded waits ran

@@ -756,6 +756,39 @@ def test_a_step_without_tokens(B, kw):
     assert all(torch.equal(x, y) for x, y in zip(old, (b.cache.k, b.cache.v, b.digest.bounds, b.digest.exp)))
 
 
+@pytest.mark.parametrize("q_block", [1, 16])
+def test_no_tokens_at_the_c_entry(q_block):
+    """The C entry itself writes the lists of a call without tokens, and nothing beside them."""
+    import ctypes
+    lib, B = dsa.load(), 2
+    b = Batch([(1, 100)] * B, 4, 2, 64, 16, False).fill().digest_all()
+    shape = dsa.binding.PagedShape(B, 0, b.table.shape[1], b.n_pages, 16, 4, 2, 64, dsa.binding.BF16)
+    cfg, n, m = dsa.binding.PageSelectCfg(3, 1, 1, q_block), ctypes.c_int(), ctypes.c_int()
+    assert lib.page_select_sizes(ctypes.byref(shape), ctypes.byref(cfg), ctypes.byref(n), ctypes.byref(m)) == 0
+    sizes = [n.value + 1, n.value, n.value * 2 * m.value, n.value * 2 * m.value]
+    call = lambda ptrs: lib.page_select(None, 4 * 64, b.digest.bounds.data_ptr(), b.digest.exp.data_ptr(), ints([0, 0, 0]).data_ptr(),
+                                        b.kv_len.data_ptr(), b.table.data_ptr(), ctypes.byref(shape), ctypes.byref(cfg), *ptrs, None)
+    for index in (True, False):
+        outs = [torch.full((size + 2,), 77, dtype=torch.int32, device="cuda") for size in sizes]
+        torch.cuda.synchronize()
+        assert call([t[1:].data_ptr() for t in outs[:3]] + [outs[3][1:].data_ptr() if index else None]) == 0
+        torch.cuda.synchronize()
+        for t, want in zip(outs, (0, 0, -1, -1 if index else 77)):
+            assert (t[1:-1] == want).all() and t[0] == 77 and t[-1] == 77
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):                              # and as part of a graph
+        q, out = b.rows(1, 4)[:0], dsa.page_select(b.rows(1, 4)[:0], b.digest, ints([0, 0, 0]), b.kv_len, b.table, keep=3, q_block=q_block)
+        start, g = ints([0, 0, 0]), torch.cuda.CUDAGraph()
+        s.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            dsa.page_select(q, b.digest, start, b.kv_len, b.table, keep=3, q_block=q_block, out=out)
+        out.page_table.fill_(5)
+        out.q_start.fill_(5)
+        g.replay()
+    torch.cuda.synchronize()
+    assert (out.page_table == -1).all() and not out.q_start.any()
+
+
 def test_no_tokens():
     """A call without rows: blocks without rows, which attend nothing."""
     b = Batch([(1, 100), (1, 40)], 4, 2, 64, 16, False).fill().digest_all()

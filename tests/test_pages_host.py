@@ -188,6 +188,15 @@ def test_lists_arguments(lib):
     assert call(FAR[5] - 2 * 2 * 16 * 4 + 4) == -1 and b"out and page_table overlap" in lib.dsa_last_error()
 
 
+def test_select_without_tokens_checks_its_outputs(lib):
+    s = _shape(n_tok=0)
+    a = dict(q=None, bounds=FAR[1], exp=FAR[2], start=FAR[3], lens=FAR[4], table=FAR[5])
+    for o in ((OK + 1, None, None, None), (None, None, OK + 2, None), (None, None, None, OK + 3)):
+        assert _select(lib, s, o=o, **a) == -4, o
+    for o in ((None, None, FAR[5] + 4, None), (None, FAR[3], None, None), (None, None, FAR[6], FAR[6] + 4)):
+        assert _select(lib, s, o=o, **a) == -1, o
+
+
 def test_nothing_to_do(lib):
     s = _shape(n_tok=0)
     assert _rope(lib, s, q=None, k=None, v=None, out=None) == 0 and _digest(lib, s) == 0 and _lists(lib, s, q=None) == 0
