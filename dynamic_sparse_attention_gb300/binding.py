@@ -794,11 +794,19 @@ _FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
 # the shape alone are kept (_paged_shape), and the device and stream are only switched when
 # the call needs another one than the current.
 
+def _shape_struct(*sizes):
+    """PagedShape of B, n_tok, max_pages, n_pages, page_size, H_q, H_kv, D, dtype."""
+    for (name, _), x in zip(PagedShape._fields_, sizes):
+        if not -2 ** 31 <= x < 2 ** 31:                 # (ctypes would cut it to 32 bits)
+            raise ValueError(f"{name}={x} does not fit in 32 bits")
+    return PagedShape(*sizes)
+
+
 @functools.lru_cache(maxsize=1024)
 def _paged_shape(*sizes):
     """(ctypes shape, workspace bytes of paged_attn) of B, n_tok, max_pages, n_pages,
     page_size, H_q, H_kv, D, dtype."""
-    shape, n = PagedShape(*sizes), ctypes.c_size_t()
+    shape, n = _shape_struct(*sizes), ctypes.c_size_t()
     _check("paged_attn_workspace", load().paged_attn_workspace(ctypes.byref(shape), ctypes.byref(n)))
     return ctypes.byref(shape), n.value
 
@@ -1150,7 +1158,7 @@ class PageSelection:
 @functools.lru_cache(maxsize=1024)
 def _select_sizes(keep, n_sink, n_local, q_block, *sizes):
     """(ctypes shape, ctypes cfg, n_blocks, max_list) of a page_select call."""
-    shape, cfg = PagedShape(*sizes), PageSelectCfg(keep, n_sink, n_local, q_block)
+    shape, cfg = _shape_struct(*sizes), PageSelectCfg(keep, n_sink, n_local, q_block)
     n, m = _c_int(), _c_int()
     _check("page_select_sizes", load().page_select_sizes(ctypes.byref(shape), ctypes.byref(cfg), ctypes.byref(n),
                                                          ctypes.byref(m)))

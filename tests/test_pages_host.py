@@ -248,6 +248,27 @@ def test_binding_rejects(lib, monkeypatch):
         dsa.page_select(q, d, start, one, table, keep=1, out=sel)
 
 
+def test_numbers_past_32_bits_are_not_cut(lib, monkeypatch):
+    """n_tok, and the sizes of tensors, reach the library whole or not at all."""
+    c = dsa.PagedKVCache.empty(4, 16, 2, 64, device="cpu")
+    d = dsa.PageDigest.empty(c)
+    one, table, start = torch.ones(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32)
+    monkeypatch.setattr(binding, "_cache_args", lambda cache: (OK, OK, None, None, cache.k.shape, 0, -1))
+    monkeypatch.setattr(binding, "_digest_args", lambda digest: (OK, OK, *digest.bounds.shape[:2], digest.bounds.shape[3], -1))
+    monkeypatch.setattr(binding, "_current_stream", lambda dev: 0)
+    for n in (2 ** 32, 2 ** 32 + 5, 2 ** 31, -2 ** 32, -1, 2 ** 30 + 1, 2 ** 64):
+        with pytest.raises((ValueError, dsa.DsaError)):
+            dsa.page_digest_update(c, d, n, start, one, table)
+    dsa.page_digest_update(c, d, 0, start, one, table)   # nothing to do, and taken
+    for i in range(9):
+        sizes = [1, 0, 1, 4, 16, 2, 2, 64, 0]
+        sizes[i] += 2 ** 32
+        with pytest.raises(ValueError):
+            binding._paged_shape(*sizes)
+        with pytest.raises(ValueError):
+            binding._select_sizes(3, 1, 1, 1, *sizes)
+
+
 def test_stream_of_another_device(lib, monkeypatch):
     class Default:
         cuda_stream, device_index = 0, 1
