@@ -456,6 +456,44 @@ def test_select_of_short_sequences_and_loose_rows():
         check_select(b, q, 4, 1, 1, q_block, sel, rows0=2)
 
 
+# Blocks of many rows whose CTAs take five tiles of 128 pages or more each, however an item is cut over a
+# cluster (of 8 CTAs at most at these widths): both buffers of digests and of scores come round several times.
+TILES = [
+    # seqs (pages of 16), H_q, D, q_block, least tiles
+    *(([(n, 16 * pages)], 4, D, n, 5) for D in (128, 64) for n, pages in
+      ((16, 4800), (16, 5500), (24, 4800), (32, 5500), (64, 4800), (64, 6300))),   # 64, 96, 128, 256 rows, one set
+    *(([(n, 16 * 4800)], 4, D, n, 5) for D in (128, 64) for n in (65, 128, 150)),   # 260, 512 and 600 rows: sets of 256
+    ([(130, 16 * 5200), (3, 16 * 4900)], 6, 128, 60, 5),       # 360 rows in two sets, then short blocks
+    ([(64, 16 * 57700)], 4, 128, 64, 50),                      # keys so many that sets are of 128 rows
+    ([(150, 16 * 57700)], 4, 128, 150, 50),
+]
+
+
+@pytest.mark.parametrize("seqs,H_q,D,q_block,least", TILES)
+def test_select_of_many_tiles(seqs, H_q, D, q_block, least):
+    b = Batch(seqs, H_q, 1, D, 16, False, n_pages=2000, seed=H_q + D + q_block)
+    b.table_np[:] = b.rng.integers(0, b.n_pages, b.table_np.shape)
+    b.table = ints(b.table_np)
+    b.fill(2.0).digest_all()
+    for n, t in seqs:
+        first = (t - n) // 16 - 1                           # candidates: pages 1 .. first - 1
+        assert all(-(-(-(-(first - 1) // C)) // 128) >= least for C in (1, 2, 4, 8))
+    q = b.rows(b.N, H_q, 3.0)
+    for keep in (1, 400):
+        sel = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=keep, q_block=q_block, want_index=True)
+        check_select(b, q, keep, 1, 1, q_block, sel)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_block", [16, 32, 64])
+def test_select_of_many_tiles_without_clusters(q_block, D):
+    """80 blocks and more, so that each is one CTA's: five to seven tiles, odd and even counts."""
+    b = Batch([(81 * q_block - 5, 81 * q_block - 5 + 16 * 700)], 4, 1, D, 16, False, seed=q_block).fill(2.0).digest_all()
+    q = b.rows(b.N, 4, 3.0)
+    sel = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=50, q_block=q_block, want_index=True)
+    check_select(b, q, 50, 1, 1, q_block, sel)
+
+
 def test_select_over_the_largest_tables():
     """The widest table: 4M keys in pages of 16, a slice of 16,384 pages for each CTA."""
     for q_block, G in ((1, 4), (8, 4)):
