@@ -494,6 +494,32 @@ def test_select_of_many_tiles_without_clusters(q_block, D):
     check_select(b, q, 50, 1, 1, q_block, sel)
 
 
+@pytest.mark.parametrize("q_block", [1, 3])
+def test_select_of_the_largest_batch(q_block):
+    """4,096 sequences, which are as many blocks as a call may have, without keys, with one, with a few pages;
+    and the attention over their lists."""
+    seqs = [(1, t) for t in np.random.default_rng(q_block).integers(0, 200, 4096)]
+    seqs[:3], seqs[-1] = [(1, 0), (1, 1), (1, 16)], (1, 199)
+    b = Batch(seqs, 2, 1, 64, 16, False, n_pages=3000, max_pages=13)
+    b.table_np[:] = b.rng.integers(0, b.n_pages, b.table_np.shape)
+    b.table = ints(b.table_np)
+    b.fill(2.0).digest_all()
+    q = b.rows(b.N, 2)
+    sel = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=2, q_block=q_block, want_index=True)
+    assert sel.kv_len.shape == (4096,)
+    check_select(b, q, 2, 1, 1, q_block, sel)
+    out, lse = dsa.paged_attn(q, b.cache, sel.q_start, sel.kv_len, sel.page_table)
+    check_lists(b, q, sel.q_start, sel.kv_len, sel.page_table, out, lse, blocks=[0, 1, 2, 3, *range(10, 4096, 97), 4095])
+
+
+def test_select_of_the_most_rows():
+    """256 tokens of 128 heads that share their keys: 32,768 rows in one block."""
+    b = Batch([(256, 16 * 700), (1, 16 * 300)], 128, 1, 128, 16, False, seed=5).fill(2.0).digest_all()
+    q = b.rows(b.N, 128, 3.0)
+    sel = dsa.page_select(q, b.digest, b.q_start, b.kv_len, b.table, keep=40, q_block=256, want_index=True)
+    check_select(b, q, 40, 1, 1, 256, sel)
+
+
 def test_select_over_the_largest_tables():
     """The widest table: 4M keys in pages of 16, a slice of 16,384 pages for each CTA."""
     for q_block, G in ((1, 4), (8, 4)):
