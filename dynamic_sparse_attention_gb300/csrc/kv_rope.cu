@@ -3,14 +3,15 @@
 // Mathematics: a head's row x [D] becomes y = x * rsqrt(mean(x^2) + eps) * w, and each pair of
 // its first `rot` dimensions is turned by p * inv_freq[i] for the token's position p.  A turn's
 // fraction is what cosine and sine see, so inv_freq / 2 pi is held as a 64-bit fraction of a turn
-// and multiplied by p modulo 2^64: the top 32 bits are the angle, within 2^-32 of a turn plus p
-// times the fraction's own 2^-53 relative error, wherever the token stands.  Rows are fp32 from load
+// and multiplied by p modulo 2^64: the top 32 bits are the angle.  It is off by p * inv_freq * 2^-52
+// radians (the two roundings of inv_freq / 2 pi) and 2^-23 (the 32 bits, and their fp32) at most: 2^-21
+// at position 2^30 of the fastest pair.  Rows are fp32 from load
 // to store and rounded once: to bf16, or for an FP8 cache by the rule of kv_cache.cu applied to
 // the fp32 values (values are bf16 already, so they come out as kv_cache_write stores them).
 //
 // Bound by HBM: every row is read once and written once.  Measured (of 6,791 GB/s): 34,700 tokens of 32
-// query and 8 key heads of 128, bf16 (1,193 MB), 196 us, 6,090 GB/s (90 %); a decode step's 16 tokens 4.9
-// us, a launch's latencies.
+// query and 8 key heads of 128, bf16 (1,193 MB), 196 us, 6,070 GB/s (89 %), into an FP8 cache (1,095 MB) 207
+// us, 5,280 GB/s (78 %); a decode step's 16 tokens 4.9 us, a launch's latencies.
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
@@ -23,7 +24,7 @@ DSA_CHECK_WORD(kv_rope_check_word)
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxTok = 32;   // tokens per CTA at most
+constexpr int kMaxTok = 16;   // tokens per CTA at most
 
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -259,7 +260,7 @@ cudaError_t launch_kv_write_rope(const RopeWriteArgs &a0, cudaStream_t s) {
   // few tokens: one per CTA, its rows over all warps; many: a warp takes a token's rows, so that its
   // angles are computed once, and a CTA enough of them to pay for its own start
   a.tpc = 1;
-  while (a.tpc < 16 && a.n_tok / (2 * a.tpc) >= 4 * 152) a.tpc *= 2;
+  while (a.tpc < kMaxTok && a.n_tok / (2 * a.tpc) >= 4 * 152) a.tpc *= 2;
   a.wpt = a.tpc >= kWarps ? 1 : kWarps / a.tpc;
   while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
   const dim3 grid((a.n_tok + a.tpc - 1) / a.tpc);

@@ -10,10 +10,12 @@
 // arithmetic alike (products below 2^14 and sums below 2^21 are whole in fp32's 24 bits): the
 // selection has one answer, the same for every kernel and every split of the work.
 //
-// Measured: digests of 131,071 tokens of 8 heads of 128 in bf16 47 us, 5,790 GB/s (85 % of 6,791: HBM);
-// selection of 16 tokens over up to 32,768 keys in pages of 64 10 us, of one token over 1,048,576 24 us
-// (chains of latencies: the digests are 1.4 and 5 us of bytes), of 2,048 tokens in blocks of 64 over
-// 131,072 85 us (32/8 heads; 68 GFLOP in its two products, 35 us of the tensor core's burst rate).
+// Measured: digests of 131,071 tokens of 8 heads of 128 in bf16 47 us, 5,820 GB/s (86 % of 6,791: HBM), in
+// FP8 81 us, 1,725 GB/s (25 %: 8-byte loads, and a scale byte for each row); selection of 16 tokens over up to
+// 32,768 keys in pages of 64 10 us, of one token over 1,048,576 25 us (chains of latencies: the digests are
+// 1.4 and 5 us of bytes), of 2,048 tokens over 131,072 in blocks of 64 85 us, of 32, 16, 8 and 4 tokens 113,
+// 184, 365 and 394 (32/8 heads; 68 GFLOP in two products, 36 us of the tensor core's burst rate; every block
+// gathers and widens the digests for itself, and 64 columns or fewer leave half of an MMA empty).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1113,10 +1115,12 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
   const int items = a.n_blocks * a.H_kv, rows = a.cfg.q_block * (a.H_q / a.H_kv);
   const bool few = rows <= kFewRows;
   // CTAs of an item, while the launch does not fill the GPU with them.  Few rows: 16 tokens of 8 heads
-  // over 512 pages take 11.0 us with one, 12.3 with two, 19.9 with four; over 2,048 pages 28.4, 24.8,
-  // 34.9; a token over 16,384 42.7, 27.4 and 24.3 us with 4, 8 and 16.  Many rows: a block of 64
-  // tokens of 8 heads over 2,048 pages 24.6, 21.9 and 42.4 us with 4, 8 and 16 (16 CTAs of a whole SM
-  // find no room in a cluster's SMs at once).
+  // over 512 pages take 10.3 us with one, 11.7 with two, 19.9 with four; over 2,048 pages 27.5, 22.1,
+  // 30.0; a token over 16,384 47.0, 29.2 and 25.0 us with 4, 8 and 16.  Many rows: a block of 64
+  // tokens of 8 heads over 2,048 pages 24.0, 21.2 and 40.4 us with 4, 8 and 16 (16 CTAs of a whole SM
+  // find no room in a cluster's SMs at once).  The table's width stands for the sequences', which the host
+  // does not know: 16 tokens over 512 pages take 12.3 us in a table of 2,048 or 16,384, one token over 64
+  // pages 13.0 in place of 6.9.
   const int most = few ? 16 : 8;
   int C = 1;
   while (C < most && a.max_pages > C * kTilePages && items * C * (a.max_pages > C * 1024 && few ? 1 : 2) <= 152) C *= 2;
@@ -1126,12 +1130,12 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
     a.slice = (a.max_pages + C - 1) / C;
   }
   const size_t keys = static_cast<size_t>(a.slice) * 4;
-  // (16 rows by tcgen05 instead: 2,048 tokens in blocks of 4 over 2,048 pages 1,053 us in place of 447)
+  // (16 rows by tcgen05 instead: 2,048 tokens in blocks of 4 over 2,048 pages 707 us in place of 394)
   if (rows <= 8) return launch_cluster<select_few_kernel<D, 1>>(items, C, kFewThreads, keys, kFewBytes, s, a);
   if (few) return launch_cluster<select_few_kernel<D, 2>>(items, C, kFewThreads, keys, kFewBytes, s, a);
-  // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
   // about two clocks a nanosecond; at most 2^31 of them, a second
   a.wait_clocks = static_cast<uint32_t>(std::min(2ull * g_wait_limit_ns, 0x7fffffffull));
+  // rows held at a time: as many as a block has, 128 where the keys of a wide table need the room
   const size_t smem = many_layout(D, rows <= 64 ? 64 : 128).oKey + keys, smem256 = many_layout(D, 256).oKey + keys;
   if (rows <= 64) return launch_cluster<select_many_kernel<D, 64>>(items, C, kManyThreads, smem, kManyBytes, s, a);
   if (rows <= 128 || smem256 > kManyBytes)
@@ -1144,8 +1148,7 @@ cudaError_t launch_select_d(PageSelectArgs a, cudaStream_t s) {
 cudaError_t launch_page_digest(const DigestArgs &a0, cudaStream_t s) {
   DigestArgs a = a0;
   while ((1 << a.lg_page) < a.page_size) ++a.lg_page;
-  // token rows per CTA: an equal share of a launch that fills the GPU once with four CTAs an SM; a few
-  // at least, unless each may be a page of its own
+  // token rows per CTA: an equal share of a launch that fills the GPU's 152 SMs once with four CTAs each
   const int heads = (a.H_kv + kDigestHeads - 1) / kDigestHeads;
   const int ctas = std::max(1, 4 * 152 / heads);
   a.window = std::min(std::max((a.n_tok + ctas - 1) / ctas, 1), kMaxWindow);

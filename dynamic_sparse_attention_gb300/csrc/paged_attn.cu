@@ -57,9 +57,9 @@
 //   8,192 tokens, window 1,024 and 256 first keys, bf16: 158 us, 1,004 TFLOP/s of the attended
 //     pairs (54 %): ten key tiles an item, of which three are cut by the mask, and two more that
 //     pass between two items (in FP8 206 us, 41 %).
-//   over lists of pages (a table for each KV head): 16 tokens over 65 pages of 64 each 55 us, 4,840 GB/s (70
-//     %), the gap between two short items; 2,048 tokens in 32 blocks over 65 pages of 64 125 us, 1,090
-//     TFLOP/s (56 %), as prompts.
+//   over lists of pages (a table for each KV head): 16 tokens over 65 pages of 64 each 56 us, 4,740 GB/s (70
+//     %), the gap between two short items, in FP8 51 us, 2,650 GB/s (39 %); 2,048 tokens in 32 blocks over 65
+//     pages of 64 125 us, 1,092 TFLOP/s (57 %), in FP8 158 us, 865 TFLOP/s (45 %): items of 33 key tiles.
 //   one token over 2,048 keys: 15 us, a chain of latencies (share, page, Q and K, two products,
 //     partials, merge) with 1.2 us of bytes in it.
 //

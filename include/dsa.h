@@ -525,8 +525,9 @@ typedef struct {
  *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) * rope_scale, angle p * inv_freq[i],
  * and queries go to q_out [n_tok, H_q, D] bf16 (qo_stride elements between tokens), keys to their
  * pages, values to theirs as kv_cache_write has them.  All of it in fp32 with one rounding at the
- * end (an FP8 cache is quantised from the fp32 values); angles are held as 64-bit fractions of a
- * turn, so far positions lose nothing.  q_out may be q itself (same pointer and stride).  A token
+ * end (an FP8 cache is quantised from the fp32 values; squares too are fp32, so a normed
+ * head whose magnitudes pass 2^60 comes out as zeros).  Angles are off by p * inv_freq[i] * 2^-52 + 2^-23
+ * radians at most (inv_freq is held as a 64-bit fraction of a turn, made in double).  q_out may be q itself (same pointer and stride).  A token
  * whose page is no page still gets its query; tokens outside every chunk are left alone.
  * Errors: INVALID_ARG / UNSUPPORTED (shape, strides, cfg), ALIGNMENT, CUDA. */
 int kv_cache_write_rope(const void *q, long long q_stride, const void *k_new, long long k_stride,
@@ -539,7 +540,7 @@ int kv_cache_write_rope(const void *q, long long q_stride, const void *k_new, lo
 /* page_digest_update -- the digests of the pages that the chunks touch (those that hold a
  * position of rows q_start[b] .. q_start[b+1]-1), over all of their keys below kv_len[b]:
  *   bounds [n_pages, H_kv, 2, D] int8   lo_d = floor(min_t k_d * 2^-e), hi_d = ceil(max_t k_d *
- *          2^-e), kept in [-127, 127]: k_d lies in [lo_d, hi_d] * 2^e
+ *          2^-e), kept in [-127, 127]: k_d lies in [lo_d, hi_d] * 2^e (up to 127 * 2^50)
  *   exp    [n_pages, H_kv] int8         e, the least integer in [-50, 50] with a * 2^-e <= 127 for
  *          a = the page's largest finite magnitude of this head (0 if a is 0)
  * An infinity counts as the largest of its sign, a NaN as nothing (bounds 0 where nothing else
