@@ -1,7 +1,11 @@
 // Error reporting and version entry points of the C ABI.
 #include "api_common.h"
 
+#include <atomic>
 #include <cstring>
+#include <thread>
+
+#include "launch.h"
 
 namespace dsa {
 
@@ -23,6 +27,38 @@ int fail(int status, const char *fmt, ...) {
 
 int cuda_fail(cudaError_t e, const char *what) {
   return fail(DSA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
+}
+
+namespace {
+// The largest limit that each kernel has been given on each device; places are found by hashing and never
+// given up.  (Set anew by every call, as a context that was torn down and made again has forgotten it.)
+struct SharedLimit {
+  const void *kern;
+  int dev;
+  size_t bytes;
+};
+constexpr int kLimits = 1024;   // kernels times devices; where no place is left, a call's own size is set
+SharedLimit g_limit[kLimits];
+std::atomic_flag g_limit_lock = ATOMIC_FLAG_INIT;
+}  // namespace
+
+cudaError_t allow_shared(const void *kern, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  while (g_limit_lock.test_and_set(std::memory_order_acquire)) std::this_thread::yield();
+  SharedLimit *at = nullptr;
+  for (size_t i = 0, h = reinterpret_cast<uintptr_t>(kern) / 16 + static_cast<size_t>(dev) * 31; i < kLimits; ++i) {
+    SharedLimit &l = g_limit[(h + i) % kLimits];
+    if (l.kern && (l.kern != kern || l.dev != dev)) continue;
+    at = &l;
+    break;
+  }
+  const size_t most = at && at->bytes > bytes ? at->bytes : bytes;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (e == cudaSuccess && at) *at = SharedLimit{kern, dev, most};
+  g_limit_lock.clear(std::memory_order_release);
+  return e;
 }
 
 }  // namespace dsa

@@ -263,7 +263,7 @@ cudaError_t launch_decode_t(const DecodeArgs &a, cudaStream_t s) {
   const size_t smem = DecodeSmem<T, D>::bytes(R);
   auto kern = decode_splitk_kernel<T, D, NACC>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(kern, smem);
     if (e != cudaSuccess) return e;
   }
   dim3 grid(a.n_split, a.H_kv, a.B);

@@ -566,7 +566,7 @@ cudaError_t launch_mma_d(const DecodeArgs &a0, cudaStream_t s) {
   auto prepare = [&](const MmaShape &sh, void (**kern)(DecodeArgs)) -> cudaError_t {
     size_t smem;
     shape_for(sh, kern, &smem);
-    cudaError_t e = cudaFuncSetAttribute(*kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(*kern, smem);
     if (e == cudaSuccess && sh.C > 8)
       e = cudaFuncSetAttribute(*kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cfg.gridDim = dim3(sh.C, a.H_kv, a.B);

@@ -798,7 +798,7 @@ cudaError_t launch_score_t(const StageScoreArgs &a, cudaStream_t s) {
   const size_t smem = lay.total;
   dim3 grid((a.max_chunks + C - 1) / C, a.B);
   auto go = [&](auto kern) {
-    if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) allow_shared(kern, smem);
     launch_pdl(kern, grid, dim3(threads), smem, s, a, C);
   };
   if (qreg && threads <= 256) {
@@ -834,7 +834,7 @@ cudaError_t launch_stage_topk(const StageTopkArgs &a, cudaStream_t s) {
   const int parts = std::max(1, std::min(kTopkMaxParts, (a.out_stride + kTopkPartEntries - 1) / kTopkPartEntries));
   auto go = [&](auto kern, int threads, size_t static_bytes, int nparts) {
     if (smem + static_bytes > 48 * 1024)
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      allow_shared(kern, smem);
     launch_pdl(kern, dim3(a.B, nparts), dim3(threads), smem, s, a);
   };
   // 16-byte list access needs 16-byte aligned rows of the explicit input list, and rows

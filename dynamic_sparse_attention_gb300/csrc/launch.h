@@ -18,6 +18,14 @@ namespace dsa {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 bool make_bshd_map(CUtensorMap *m, const void *base, int D, int H, int S, int B, int rows);
 
+// Allows a kernel `bytes` of dynamic shared memory on the current device, at least: the limit belongs to the
+// kernel and is never lowered, as another host thread may be between its own call and its launch.
+cudaError_t allow_shared(const void *kern, size_t bytes);
+template <typename... Args>
+cudaError_t allow_shared(void (*kern)(Args...), size_t bytes) {
+  return allow_shared(reinterpret_cast<const void *>(kern), bytes);
+}
+
 // Launch with programmatic stream serialization allowed: the grid may start while
 // the stream's previous kernel drains (its CTAs then wait in grid_dep_wait()).
 template <typename Kern, typename... Args>

@@ -405,7 +405,7 @@ cudaError_t launch_block_sparse(const BsArgs &a, cudaStream_t s) {
   const dim3 grid((a.nb + R - 1) / R, a.B * a.H_q);
   const size_t smem = bs_smem_bytes(R, a.nb, a.D);
   auto go = [&](auto kern) {
-    cudaError_t st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t st = allow_shared(kern, smem);
     if (st != cudaSuccess) return st;
     ProfScope ps("bs_score_topk", s);
     kern<<<grid, kTopThreads, smem, s>>>(a);

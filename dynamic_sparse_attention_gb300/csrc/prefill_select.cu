@@ -311,7 +311,7 @@ template <int D, int G>
 cudaError_t launch_pf(const PfScoreArgs &a, cudaStream_t s) {
   const size_t smem = PfSmem<D, G>::bytes(a.L, a.in_idx != nullptr);
   auto kern = prefill_score_kernel<D, G>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   // all of the unified L1 / shared memory as shared memory, so two CTAs fit an SM
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);

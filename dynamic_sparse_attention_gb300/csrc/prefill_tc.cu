@@ -862,7 +862,7 @@ cudaError_t launch_tc_d(const PrefillArgs &pa, cudaStream_t s) {
   a.epoch = ep;
   const size_t smem = Layout<D>::bytes(a.n_words);
   auto kern = prefill_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   dim3 grid((a.n_qblk + 1) / 2 * (pa.H_q / pa.H_kv), pa.H_kv, pa.B);
   {

@@ -232,7 +232,7 @@ cudaError_t launch_tc(const StageScoreArgs &a, cudaStream_t s) {
   constexpr int CPW = 16 / G;
   const size_t smem = tc_smem(a, CPW);
   auto kern = stage_score_tc_kernel<D, G>;
-  if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024) allow_shared(kern, smem);
   dim3 grid((a.max_chunks + CPW - 1) / CPW, a.B);
   launch_pdl(kern, grid, dim3(32 * a.H_kv), smem, s, a);
   return cudaGetLastError();

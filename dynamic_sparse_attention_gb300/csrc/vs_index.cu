@@ -340,7 +340,7 @@ cudaError_t launch_vs(const VsArgs &a, cudaStream_t s) {
     const int staged = chunk <= kTkSmemKeys ? 1 : 0;
     const size_t smem = staged ? static_cast<size_t>(chunk) * 4 : 0;
     if (smem > 0) {
-      e = cudaFuncSetAttribute(vs_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = allow_shared(vs_topk_kernel, smem);
       if (e != cudaSuccess) return e;
     }
     ProfScope ps("vs_topk", s);
@@ -351,7 +351,7 @@ cudaError_t launch_vs(const VsArgs &a, cudaStream_t s) {
     const int n_qblk = (a.S + 63) / 64;
     const int n_words = (n_qblk + 31) / 32;
     const size_t smem = (2ull * n_words + n_qblk + a.n_vertical) * 4;
-    e = cudaFuncSetAttribute(vs_convert_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_shared(vs_convert_kernel, smem);
     if (e != cudaSuccess) return e;
     dim3 g4((n_qblk + kConvRun - 1) / kConvRun, a.H_q, a.B);
     ProfScope ps("vs_convert", s);

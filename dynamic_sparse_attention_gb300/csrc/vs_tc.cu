@@ -546,7 +546,7 @@ cudaError_t launch_vs_tc(const VsTcLaunch &l, cudaStream_t s) {
     dim3 grid(a.n_split, l.H_kv, l.B);
     if (pass == 0) {
       auto kern = vs_tc_kernel<0>;
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaError_t e = allow_shared(kern, smem);
       if (e != cudaSuccess) return e;
       ProfScope ps("vs_pass_rowstats", s);
       kern<<<grid, threads, smem, s>>>(a);
@@ -559,7 +559,7 @@ cudaError_t launch_vs_tc(const VsTcLaunch &l, cudaStream_t s) {
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     } else {
       auto kern = vs_tc_kernel<1>;
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaError_t e = allow_shared(kern, smem);
       if (e != cudaSuccess) return e;
       {
         ProfScope ps("vs_pass_sums", s);
