@@ -37,7 +37,8 @@
  *     default stream) and returns at once.  Scratch memory, where needed, is the
  *     caller's `ws` buffer, whose size the matching *_workspace() call returns.
  *     Calls hold no state between them; two calls may run concurrently on
- *     different streams if their ws and output buffers differ.
+ *     different streams, from one host thread or several, if their ws and output buffers
+ *     differ.
  *   - No host synchronisation and fixed-size outputs: a decode step can be
  *     captured in a CUDA graph.
  *   - Return value: DSA_OK or a negative dsa_status.  On a validation failure
@@ -639,7 +640,7 @@ int dsa_profile_collect(dsa_kernel_stat *out, int max_out, int *n_out);
  * frees its resources and sets a device error word (the prefill CTA also writes zero
  * output).  dsa_device_error copies the words to *code (0 = none; bit 0: the prefill
  * attention, bit 1: the estimate; bit 2: in a checked build, a kernel met a kv_len,
- * count, selected position or list entry outside its documented range -- the call then
+ * count, selected position, list entry or digest exponent outside its documented range -- the call then
  * returns DSA_ERR_DEVICE_CHECK; bit 3: the paged attention; bit 4: the page selection) and clears
  * them.  It synchronises with the device
  * (cudaMemcpyFromSymbol); call it between steps, not on a hot path.  Not a
